@@ -10,6 +10,12 @@
  *   ssm_conv1d_fwd / ssm_conv1d_update
  *                     the causal depthwise convolution that feeds the scan,
  *                     and its decode step
+ *   ssm_linear_attn_fwd / ssm_linear_attn_bwd / ssm_linear_attn_update
+ *                     linear attention with a constant decay per head: whole
+ *                     sequences, their gradient, and one recurrent step
+ *   ssm_qk_norm_rope_fwd / ssm_qk_norm_rope_bwd
+ *                     per-head norm and position rotation of the queries and
+ *                     keys that feed it, and their gradient
  *
  * Per batch row b, channel d and state n (A diagonal, B and C shared by all
  * channels of a row):
@@ -398,6 +404,165 @@ int ssm_conv1d_fwd(const void* x, const float* w, const float* bias, const float
  */
 int ssm_conv1d_update(float* state, const void* x_t, const float* w, const float* bias, void* y_t, int64_t batch,
                       int64_t d_inner, int64_t d_conv, int32_t io_dtype, int32_t apply_silu, void* stream);
+
+/*
+ * Linear attention with a constant decay per head.  Per batch row b and head h
+ * (key/value head m = h / (nheads / nheads_kv)), with the state
+ * H [d_v][d_k] and gamma = exp(log_decay[h]):
+ *
+ *   H_t      = gamma * H_{t-1} + v[b,t,m] k[b,t,m]^T
+ *   o[b,t,h] = scale * H_t q[b,t,h]
+ *
+ * i.e. o_t = scale * sum_{i <= t} gamma^(t-i) (q_t . k_i) v_i: attention
+ * without a softmax, whose whole past is one matrix per head.
+ *
+ *   q          : [batch][seqlen][nheads][d_k] io_dtype; k [batch][seqlen]
+ *                [nheads_kv][d_k] and v [batch][seqlen][nheads_kv][d_v] alike.
+ *                Consecutive steps (and the rows of the batch, seqlen steps
+ *                apart) are q_stride, k_stride, v_stride elements apart, so
+ *                that q, k and v may be column ranges of one projection's
+ *                output; 0 stands for the dense nheads * d_k and so on.  All
+ *                three 16-byte aligned, strides multiples of 16 bytes and not
+ *                below the dense ones.
+ *   log_decay  : [nheads] fp32, log(gamma); 0 keeps everything, -inf keeps
+ *                only the current step.  A constant of the layer: it has no
+ *                gradient.  Positive values grow the state without bound.
+ *   lengths    : [batch] int32 or NULL.  Row b has lengths[b] steps (clamped to
+ *                [0, seqlen] on the device); what q, k and v hold behind them
+ *                is not used, o is zero there, and h_last is the state after
+ *                lengths[b] steps.
+ *   h0, h_last : [batch][nheads][d_v][d_k] fp32, 16-byte aligned, or NULL
+ *                (zeros / not written); h_last may be the h0 buffer.
+ *   o          : [batch][seqlen][nheads][d_v] io_dtype, dense, 16-byte
+ *                aligned; must not overlap any input.
+ *   scale      : usually 1 / sqrt(d_k).
+ *   d_k, d_v   : 64 or 128 each.  nheads a multiple of nheads_kv.
+ *   workspace  : ssm_linear_attn_fwd_workspace_size() bytes, 256-byte aligned
+ *                (may be NULL when that is 0); contents on entry ignored.
+ *                Calls that may run at the same time need one each, and so do
+ *                two captured graphs that may be replayed at the same time.
+ * bf16 inputs meet the matrix cores exactly and the state is fp32; operands
+ * formed in between are carried as sums of two or three bf16 values, so that
+ * the rounding of o dominates o's error and h_last has fp32's.  With
+ * SSM_DTYPE_F32 all products are fp32.  A NaN or an infinity at step t can
+ * reach the outputs of steps that share its block of 64.
+ * Sums are taken in a fixed order: results are bitwise reproducible for a
+ * given device, sizes and strides.  Same conventions, validation and error
+ * codes as the scan; nheads above 32768: SSM_ERR_BAD_DIM.
+ */
+int ssm_linear_attn_fwd(const void* q, const void* k, const void* v, const float* log_decay, const int32_t* lengths,
+                        const float* h0, void* o, float* h_last, int64_t batch, int64_t seqlen, int64_t nheads,
+                        int64_t nheads_kv, int64_t d_k, int64_t d_v, int64_t q_stride, int64_t k_stride,
+                        int64_t v_stride, float scale, int32_t io_dtype, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* Workspace bytes of ssm_linear_attn_fwd (0 when the sequence is not cut into
+ * spans).  (size_t)-1 for invalid sizes.  Pure host computation. */
+size_t ssm_linear_attn_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v,
+                                          int32_t io_dtype);
+
+/*
+ * Gradient of ssm_linear_attn_fwd for L = sum(d_o * o) + sum(dh_last * h_last).
+ *
+ *   q, k, v, log_decay, lengths, h0, strides, scale, io_dtype : as in the
+ *             forward call.
+ *   d_o     : [batch][seqlen][nheads][d_v] io_dtype, dense, 16-byte aligned
+ *             (unused behind a row's length).
+ *   dh_last : [batch][nheads][d_v][d_k] fp32 (16-byte aligned), or NULL for 0.
+ *   dq, dk, dv : io_dtype, dense [batch][seqlen][nheads][d_k],
+ *             [batch][seqlen][nheads_kv][d_k], [batch][seqlen][nheads_kv][d_v],
+ *             16-byte aligned; zero behind a row's length.  dk and dv are summed
+ *             over the heads that share them, in fp32 and in head order.
+ *   dh0     : [batch][nheads][d_v][d_k] fp32 (16-byte aligned; of zeros when h0
+ *             is NULL), or NULL.
+ *   workspace : ssm_linear_attn_bwd_workspace_size() bytes, 256-byte aligned.
+ * Outputs are overwritten and must not overlap each other, any input or the
+ * workspace.
+ */
+int ssm_linear_attn_bwd(const void* q, const void* k, const void* v, const float* log_decay, const int32_t* lengths,
+                        const float* h0, const void* d_o, const float* dh_last, void* dq, void* dk, void* dv,
+                        float* dh0, int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_kv, int64_t d_k,
+                        int64_t d_v, int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale,
+                        int32_t io_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of ssm_linear_attn_bwd.  (size_t)-1 for invalid sizes. */
+size_t ssm_linear_attn_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_kv,
+                                          int64_t d_k, int64_t d_v, int32_t io_dtype);
+
+/*
+ * One recurrent step (decode) of the same operator, in place on the state:
+ *   h = gamma * h + v k^T,  o = scale * h q.
+ *
+ *   h       : [n_slots][nheads][d_v][d_k] fp32, 16-byte aligned.
+ *   slots   : [batch] int32 or NULL.  Request b's state is h[slots[b]]; NULL
+ *             stands for slots[b] = b (n_slots must then be batch).  A value
+ *             outside [0, n_slots) marks an unused row: no state is touched and
+ *             its o is zero.  The used values must differ: of two requests with
+ *             one slot, that slot's state and both outputs are unspecified.
+ *   q, k, v : [batch][nheads][d_k], [batch][nheads_kv][d_k],
+ *             [batch][nheads_kv][d_v] io_dtype, rows q_stride, k_stride, v_stride
+ *             elements apart (0: dense); alignment as for ssm_linear_attn_fwd.
+ *   o       : [batch][nheads][d_v] io_dtype, dense; overlaps nothing.
+ *   d_k, d_v: 64 or 128 each.
+ * Equivalent to ssm_linear_attn_fwd with seqlen 1 and h0 = h_last = h[slots].
+ */
+int ssm_linear_attn_update(float* h, const int32_t* slots, const void* q, const void* k, const void* v,
+                           const float* log_decay, void* o, int64_t batch, int64_t n_slots, int64_t nheads,
+                           int64_t nheads_kv, int64_t d_k, int64_t d_v, int64_t q_stride, int64_t k_stride,
+                           int64_t v_stride, float scale, int32_t io_dtype, void* stream);
+
+/*
+ * RMS norm of every query and key head followed by the rotation of position,
+ * in one pass.  For a head x of headdim values at position p:
+ *
+ *   n = w * x / sqrt(mean(x^2) + eps)
+ *   the first rot_dim values of n are turned pair by pair by p * inv_freq[j]:
+ *     (a, b) -> (a cos - b sin, a sin + b cos)
+ *   with the pair j < rot_dim / 2 at (j, j + rot_dim / 2), or at (2 j, 2 j + 1)
+ *   when interleaved is 1.
+ *
+ *   q, k       : [batch][seqlen][nheads][headdim] and [batch][seqlen][nheads_k]
+ *                [headdim] io_dtype, steps q_stride and k_stride elements apart
+ *                (0: dense), 16-byte aligned, strides multiples of 16 bytes.
+ *                nheads or nheads_k may be 0 (that side's pointers are then
+ *                not used).
+ *   wq, wk     : [headdim] fp32, or NULL for ones.
+ *   inv_freq   : [rot_dim / 2] fp32, or NULL when rot_dim is 0 (norm only).
+ *   positions  : [batch][seqlen] int64, or NULL for the step's index in its
+ *                row.  Angles are formed and reduced in 64 bits, so that far
+ *                positions lose nothing.
+ *   q_out, k_out : like q and k, with strides of their own; each may be its
+ *                input exactly (in place, same stride) and must not overlap
+ *                anything else.
+ *   headdim    : a multiple of 16 up to 256; rot_dim a multiple of 16 up to
+ *                headdim; eps >= 0.
+ */
+int ssm_qk_norm_rope_fwd(const void* q, const void* k, const float* wq, const float* wk, const float* inv_freq,
+                         const int64_t* positions, void* q_out, void* k_out, int64_t batch, int64_t seqlen,
+                         int64_t nheads, int64_t nheads_k, int64_t headdim, int64_t rot_dim, int64_t q_stride,
+                         int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride, float eps,
+                         int32_t interleaved, int32_t io_dtype, void* stream);
+
+/*
+ * Gradient of ssm_qk_norm_rope_fwd: from q, k as the forward call read them and
+ * the gradients dq_out, dk_out of its outputs (dense, 16-byte aligned),
+ *   dq, dk   : io_dtype, dense, 16-byte aligned.
+ *   dwq, dwk : [headdim] fp32, summed over rows, steps and heads in a fixed
+ *              order, or NULL when not wanted (also valid for NULL weights).
+ *   workspace : ssm_qk_norm_rope_bwd_workspace_size() bytes, 256-byte aligned
+ *              (unused, may be NULL, when neither dwq nor dwk is wanted).
+ * Outputs must not overlap each other, any input or the workspace.
+ */
+int ssm_qk_norm_rope_bwd(const void* q, const void* k, const float* wq, const float* wk, const float* inv_freq,
+                         const int64_t* positions, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                         float* dwq, float* dwk, int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_k,
+                         int64_t headdim, int64_t rot_dim, int64_t q_stride, int64_t k_stride, float eps,
+                         int32_t interleaved, int32_t io_dtype, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Workspace bytes of ssm_qk_norm_rope_bwd.  (size_t)-1 for invalid sizes. */
+size_t ssm_qk_norm_rope_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_k,
+                                           int64_t headdim);
 
 #ifdef __cplusplus
 }

@@ -8,6 +8,7 @@ kernels.  There is no fallback: if the library is missing, loading raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -36,6 +37,7 @@ _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _U32 = ctypes.c_uint32
 _SZ = ctypes.c_size_t
+_F32 = ctypes.c_float
 
 
 class ScanOpts(ctypes.Structure):
@@ -65,6 +67,14 @@ SIGNATURES = {
     "ssm_ssd_fwd": ([_P] * 10 + [_I64] * 6 + [_I32, _U32, _P, _P], ctypes.c_int),
     "ssm_conv1d_fwd": ([_P] * 6 + [_I64] * 4 + [_I32, _I32, _P], ctypes.c_int),
     "ssm_conv1d_update": ([_P] * 5 + [_I64] * 3 + [_I32, _I32, _P], ctypes.c_int),
+    "ssm_linear_attn_fwd": ([_P] * 8 + [_I64] * 9 + [_F32, _I32, _P, _SZ, _P], ctypes.c_int),
+    "ssm_linear_attn_fwd_workspace_size": ([_I64] * 5 + [_I32], _SZ),
+    "ssm_linear_attn_bwd": ([_P] * 12 + [_I64] * 9 + [_F32, _I32, _P, _SZ, _P], ctypes.c_int),
+    "ssm_linear_attn_bwd_workspace_size": ([_I64] * 6 + [_I32], _SZ),
+    "ssm_linear_attn_update": ([_P] * 7 + [_I64] * 9 + [_F32, _I32, _P], ctypes.c_int),
+    "ssm_qk_norm_rope_fwd": ([_P] * 8 + [_I64] * 10 + [_F32, _I32, _I32, _P], ctypes.c_int),
+    "ssm_qk_norm_rope_bwd": ([_P] * 12 + [_I64] * 8 + [_F32, _I32, _I32, _P, _SZ, _P], ctypes.c_int),
+    "ssm_qk_norm_rope_bwd_workspace_size": ([_I64] * 5, _SZ),
 }
 
 _lib = None
@@ -341,3 +351,280 @@ def ssm_conv1d_update(state, x_t, w, bias=None, *, y_t=None, silu=True, stream=N
     if rc != SSM_OK:
         raise SsmError(rc, "ssm_conv1d_update")
     return y_t
+
+
+def _rows(t, what: str) -> Tuple[Optional[int], int]:
+    """(pointer, elements between steps) of a tensor (..., heads, width) whose
+    leading axes form evenly spaced rows of dense (heads, width) blocks: a
+    dense tensor, or a column range of a wider one."""
+    if not t.is_cuda:
+        raise ValueError("tensor must live on the GPU")
+    heads, width = t.shape[-2:]
+    ok = (width <= 1 or t.stride(-1) == 1) and (heads <= 1 or t.stride(-2) == width)
+    step = None
+    expect = None  # stride of the next axis to the left
+    for n, s in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if n != 1:
+            if step is None:
+                step = s
+            elif s != expect:
+                ok = False
+            expect = s * n
+    if t.numel() > 0 and (not ok or (step is not None and step < heads * width)):
+        raise ValueError("%s must hold dense (heads, width) blocks at one step apart" % what)
+    return t.data_ptr() or None, (heads * width if step is None else step)
+
+
+def _scope(stream, t, *others):
+    """Context in which t's device is current, and so is stream (a torch stream
+    or a raw handle) when one is given: what is allocated inside belongs to the
+    stream that uses it.  Every other tensor must be on t's device."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError("tensor must live on the GPU")
+    dev = t.device
+    for o in others:
+        if o is not None and o.device != dev:
+            raise ValueError("tensors must be on one device, got %s and %s" % (dev, o.device))
+    if stream is None:
+        if torch.cuda.current_device() == dev.index:
+            return contextlib.nullcontext()
+        return torch.cuda.device(dev)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+    if stream.device != dev:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, dev))
+    return torch.cuda.stream(stream)  # also makes the stream's device current
+
+
+def _workspace(workspace, need, device, what):
+    import torch
+    if need == ctypes.c_size_t(-1).value:
+        raise SsmError(SSM_ERR_BAD_DIM, what)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def _want(t, shape, dtype, what):
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError("%s must be %s %s, got %s %s" % (what, tuple(shape), dtype, tuple(t.shape), t.dtype))
+
+
+def _fill(g, names, device):
+    """Checks the outputs given in g and allocates the others; names: (name, shape, dtype)."""
+    import torch
+    for n in g:
+        if n not in [name for name, _, _ in names]:
+            raise ValueError("unknown output %s" % n)
+    for name, shape, dtype in names:
+        _want(g.get(name), shape, dtype, name)
+        if g.get(name) is None:
+            g[name] = torch.empty(tuple(shape), dtype=dtype, device=device)
+
+
+def _attn_shapes(q, k, v, lead):
+    """Sizes of q (*lead, nheads, d_k), k (*lead, nheads_kv, d_k), v (*lead, nheads_kv, d_v)."""
+    nheads, d_k = q.shape[-2:]
+    nheads_kv, d_v = v.shape[-2:]
+    if q.dim() != lead + 2:
+        raise ValueError("q must have %d axes, got %s" % (lead + 2, tuple(q.shape)))
+    _want(k, (*q.shape[:lead], nheads_kv, d_k), q.dtype, "k")
+    _want(v, (*q.shape[:lead], nheads_kv, d_v), q.dtype, "v")
+    return nheads, nheads_kv, d_k, d_v
+
+
+def ssm_linear_attn_fwd(q, k, v, log_decay, *, lengths=None, h0=None, scale=None, o=None, h_last=None,
+                        want_h_last=True, workspace=None, stream=None):
+    """Linear attention with a constant decay per head; returns (o, h_last).
+
+    q: (batch, seqlen, nheads, d_k); k: (batch, seqlen, nheads_kv, d_k);
+    v: (batch, seqlen, nheads_kv, d_v), all bfloat16 or all float32, dense or
+    column ranges of one wider tensor; log_decay: (nheads,) fp32;
+    lengths: (batch,) int32 steps of each row; h0, h_last:
+    (batch, nheads, d_v, d_k) fp32; scale defaults to d_k ** -0.5.
+    """
+    import torch
+    nheads, nheads_kv, d_k, d_v = _attn_shapes(q, k, v, 2)
+    batch, seqlen = q.shape[:2]
+    dt = _io_dtype(q)
+    f32 = torch.float32
+    st = (batch, nheads, d_v, d_k)
+    _want(log_decay, (nheads,), f32, "log_decay")
+    _want(lengths, (batch,), torch.int32, "lengths")
+    _want(h0, st, f32, "h0")
+    _want(o, (batch, seqlen, nheads, d_v), q.dtype, "o")
+    _want(h_last, st, f32, "h_last")
+    lib = load_library()
+    with _scope(stream, q, k, v, log_decay, lengths, h0, o, h_last, workspace):
+        if o is None:
+            o = torch.empty((batch, seqlen, nheads, d_v), dtype=q.dtype, device=q.device)
+        if h_last is None and want_h_last:
+            h_last = torch.empty(st, dtype=f32, device=q.device)
+        need = lib.ssm_linear_attn_fwd_workspace_size(batch, seqlen, nheads, d_k, d_v, dt)
+        workspace, have = _workspace(workspace, need, q.device, "ssm_linear_attn_fwd")
+        (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
+        rc = lib.ssm_linear_attn_fwd(qp, kp, vp, _ptr(log_decay), _ptr(lengths), _ptr(h0), _ptr(o), _ptr(h_last),
+                                     batch, seqlen, nheads, nheads_kv, d_k, d_v, qs, ks, vs,
+                                     d_k ** -0.5 if scale is None else scale, dt, _ptr(workspace), have,
+                                     _stream(None))
+    if rc != SSM_OK:
+        raise SsmError(rc, "ssm_linear_attn_fwd")
+    return o, h_last
+
+
+def ssm_linear_attn_bwd(q, k, v, log_decay, *, do, lengths=None, h0=None, dh_last=None, scale=None, want_dh0=True,
+                        grads=None, workspace=None, stream=None):
+    """Gradient of ssm_linear_attn_fwd for L = sum(do * o) + sum(dh_last * h_last).
+
+    Returns a dict with dq, dk, dv (io dtype, dense) and, when want_dh0, dh0
+    (fp32).  Outputs are allocated unless given in ``grads``.
+    """
+    import torch
+    nheads, nheads_kv, d_k, d_v = _attn_shapes(q, k, v, 2)
+    batch, seqlen = q.shape[:2]
+    dt = _io_dtype(q)
+    f32 = torch.float32
+    st = (batch, nheads, d_v, d_k)
+    _want(log_decay, (nheads,), f32, "log_decay")
+    _want(lengths, (batch,), torch.int32, "lengths")
+    _want(h0, st, f32, "h0")
+    _want(dh_last, st, f32, "dh_last")
+    _want(do, (batch, seqlen, nheads, d_v), q.dtype, "do")
+    g = dict(grads or {})
+    names = [("dq", q.shape, q.dtype), ("dk", k.shape, q.dtype), ("dv", v.shape, q.dtype)]
+    if want_dh0 or "dh0" in g:
+        names.append(("dh0", st, f32))
+    lib = load_library()
+    with _scope(stream, q, k, v, log_decay, lengths, h0, do, dh_last, workspace, *g.values()):
+        _fill(g, names, q.device)
+        need = lib.ssm_linear_attn_bwd_workspace_size(batch, seqlen, nheads, nheads_kv, d_k, d_v, dt)
+        workspace, have = _workspace(workspace, need, q.device, "ssm_linear_attn_bwd")
+        (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
+        rc = lib.ssm_linear_attn_bwd(qp, kp, vp, _ptr(log_decay), _ptr(lengths), _ptr(h0), _ptr(do), _ptr(dh_last),
+                                     _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g.get("dh0")), batch, seqlen,
+                                     nheads, nheads_kv, d_k, d_v, qs, ks, vs,
+                                     d_k ** -0.5 if scale is None else scale, dt, _ptr(workspace), have,
+                                     _stream(None))
+    if rc != SSM_OK:
+        raise SsmError(rc, "ssm_linear_attn_bwd")
+    return g
+
+
+def ssm_linear_attn_update(h, q, k, v, log_decay, *, slots=None, scale=None, o=None, stream=None):
+    """One decode step, in place on h (n_slots, nheads, d_v, d_k) fp32; returns o (batch, nheads, d_v).
+
+    q: (batch, nheads, d_k); k: (batch, nheads_kv, d_k); v: (batch, nheads_kv,
+    d_v); slots: (batch,) int32 places of the requests' states in h (values
+    outside h mark unused rows; used values must differ), or None when h holds
+    the batch in order.
+    """
+    import torch
+    nheads, nheads_kv, d_k, d_v = _attn_shapes(q, k, v, 1)
+    batch = q.shape[0]
+    dt = _io_dtype(q)
+    _want(h, (h.shape[0], nheads, d_v, d_k), torch.float32, "h")
+    _want(slots, (batch,), torch.int32, "slots")
+    _want(log_decay, (nheads,), torch.float32, "log_decay")
+    _want(o, (batch, nheads, d_v), q.dtype, "o")
+    with _scope(stream, q, h, slots, k, v, log_decay, o):
+        if o is None:
+            o = torch.empty((batch, nheads, d_v), dtype=q.dtype, device=q.device)
+        (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
+        rc = load_library().ssm_linear_attn_update(
+            _ptr(h), _ptr(slots), qp, kp, vp, _ptr(log_decay), _ptr(o), batch, h.shape[0], nheads, nheads_kv, d_k,
+            d_v, qs, ks, vs, d_k ** -0.5 if scale is None else scale, dt, _stream(None))
+    if rc != SSM_OK:
+        raise SsmError(rc, "ssm_linear_attn_update")
+    return o
+
+
+def _qk_shapes(q, k):
+    batch, seqlen, nheads, headdim = q.shape
+    nheads_k = 0 if k is None else k.shape[2]
+    _want(k, (batch, seqlen, nheads_k, headdim), q.dtype, "k")
+    return batch, seqlen, nheads, nheads_k, headdim
+
+
+def _qk_params(wq, wk, inv_freq, positions, batch, seqlen, headdim):
+    """Checks of the norm weights, frequencies and positions; returns rot_dim."""
+    import torch
+    _want(wq, (headdim,), torch.float32, "wq")
+    _want(wk, (headdim,), torch.float32, "wk")
+    _want(positions, (batch, seqlen), torch.int64, "positions")
+    if inv_freq is None:
+        return 0
+    _want(inv_freq, (inv_freq.numel(),), torch.float32, "inv_freq")
+    return 2 * inv_freq.numel()
+
+
+def ssm_qk_norm_rope_fwd(q, k, wq=None, wk=None, inv_freq=None, *, positions=None, eps=1e-6, interleaved=False,
+                         q_out=None, k_out=None, stream=None):
+    """RMS norm of every query and key head, then the rotation of its first
+    2 * len(inv_freq) values by position * inv_freq; returns (q_out, k_out).
+
+    q: (batch, seqlen, nheads, headdim), k: (batch, seqlen, nheads_k, headdim)
+    or None; wq, wk: (headdim,) fp32 or None for ones; positions:
+    (batch, seqlen) int64, or None for the step's index.  q_out and k_out may be q
+    and k themselves (in place).
+    """
+    import torch
+    batch, seqlen, nheads, nheads_k, headdim = _qk_shapes(q, k)
+    rot = _qk_params(wq, wk, inv_freq, positions, batch, seqlen, headdim)
+    _want(q_out, q.shape, q.dtype, "q_out")
+    if k is None and k_out is not None:
+        raise ValueError("k_out given without k")
+    if k is not None:
+        _want(k_out, k.shape, q.dtype, "k_out")
+    with _scope(stream, q, k, wq, wk, inv_freq, positions, q_out, k_out):
+        if q_out is None:
+            q_out = torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)
+        if k_out is None and k is not None:
+            k_out = torch.empty(tuple(k.shape), dtype=q.dtype, device=q.device)
+        (qp, qs), (qo, qos) = _rows(q, "q"), _rows(q_out, "q_out")
+        (kp, ks), (ko, kos) = ((None, 0),) * 2 if k is None else (_rows(k, "k"), _rows(k_out, "k_out"))
+        rc = load_library().ssm_qk_norm_rope_fwd(
+            qp, kp, _ptr(wq), _ptr(wk), _ptr(inv_freq), _ptr(positions), qo, ko, batch, seqlen, nheads, nheads_k,
+            headdim, rot, qs, ks, qos, kos, eps, 1 if interleaved else 0, _io_dtype(q), _stream(None))
+    if rc != SSM_OK:
+        raise SsmError(rc, "ssm_qk_norm_rope_fwd")
+    return q_out, k_out
+
+
+def ssm_qk_norm_rope_bwd(q, k, wq=None, wk=None, inv_freq=None, *, dq_out, dk_out=None, positions=None, eps=1e-6,
+                         interleaved=False, want_dw=True, grads=None, workspace=None, stream=None):
+    """Gradient of ssm_qk_norm_rope_fwd from its inputs and the gradients of its
+    outputs: a dict with dq, dk (dense) and, when want_dw, dwq, dwk (fp32).
+    Outputs are allocated unless given in ``grads``."""
+    import torch
+    batch, seqlen, nheads, nheads_k, headdim = _qk_shapes(q, k)
+    rot = _qk_params(wq, wk, inv_freq, positions, batch, seqlen, headdim)
+    _want(dq_out, q.shape, q.dtype, "dq_out")
+    g = dict(grads or {})
+    names = [("dq", q.shape, q.dtype)]
+    if want_dw:
+        names.append(("dwq", (headdim,), torch.float32))
+    if k is not None:
+        if dk_out is None:
+            raise ValueError("dk_out is required with k")
+        _want(dk_out, k.shape, q.dtype, "dk_out")
+        names.append(("dk", k.shape, q.dtype))
+        if want_dw:
+            names.append(("dwk", (headdim,), torch.float32))
+    lib = load_library()
+    with _scope(stream, q, k, wq, wk, inv_freq, positions, dq_out, dk_out, workspace, *g.values()):
+        _fill(g, names, q.device)
+        need = 0
+        if want_dw:
+            need = lib.ssm_qk_norm_rope_bwd_workspace_size(batch, seqlen, nheads, nheads_k, headdim)
+        workspace, have = _workspace(workspace, need, q.device, "ssm_qk_norm_rope_bwd")
+        qp, qs = _rows(q, "q")
+        kp, ks = (None, 0) if k is None else _rows(k, "k")
+        rc = lib.ssm_qk_norm_rope_bwd(
+            qp, kp, _ptr(wq), _ptr(wk), _ptr(inv_freq), _ptr(positions), _ptr(dq_out),
+            None if k is None else _ptr(dk_out), _ptr(g["dq"]), _ptr(g.get("dk")), _ptr(g.get("dwq")),
+            _ptr(g.get("dwk")), batch, seqlen, nheads, nheads_k, headdim, rot, qs, ks, eps, 1 if interleaved else 0,
+            _io_dtype(q), _ptr(workspace), have, _stream(None))
+    if rc != SSM_OK:
+        raise SsmError(rc, "ssm_qk_norm_rope_bwd")
+    return g

@@ -545,9 +545,367 @@ int conv_impl(const void* x, const float* w, const float* bias, const float* sta
   return ssm::launch_conv1d(p) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
+// ---- linear attention and the query/key norm with rotation ---------------
+
+// Rows of a tensor read in place from a wider one: `rows` rows of `width`
+// bytes, `stride` bytes apart.
+struct Rows {
+  const void* p;
+  int64_t rows, width, stride;
+};
+
+// Some byte of x is also one of y.  Two tensors of the same stride may be
+// column ranges of one buffer, whose extents overlap although their rows do not.
+bool overlap(const Rows& x, const Rows& y) {
+  if (x.p == nullptr || y.p == nullptr || x.rows <= 0 || y.rows <= 0 || x.width <= 0 || y.width <= 0) return false;
+  if (!overlap(x.p, (x.rows - 1) * x.stride + x.width, y.p, (y.rows - 1) * y.stride + y.width)) return false;
+  if (x.stride != y.stride || x.rows == 1 || y.rows == 1) return true;
+  const int64_t s = x.stride;
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(y.p) - reinterpret_cast<uintptr_t>(x.p)) % s;
+  const int64_t off = d < 0 ? d + s : d;  // y's first byte within x's rows
+  return off < x.width || off + y.width > s;
+}
+
+Rows dense(const void* p, int64_t bytes) { return Rows{p, 1, bytes, bytes}; }
+
+// Outputs against the inputs, each other and the workspace.
+int check_alias(const Rows* outs, int n_out, const Rows* ins, int n_in) {
+  for (int o = 0; o < n_out; ++o) {
+    for (int k = 0; k < n_in; ++k)
+      if (overlap(outs[o], ins[k])) return SSM_ERR_ALIAS;
+    for (int k = o + 1; k < n_out; ++k)
+      if (overlap(outs[o], outs[k])) return SSM_ERR_ALIAS;
+  }
+  return SSM_OK;
+}
+
+// The row stride (0: dense) of `width` elements, and the extent it gives.
+int check_stride(int64_t* stride, int64_t width, int64_t rows, int64_t es) {
+  if (*stride == 0) *stride = width;
+  if (*stride < width) return SSM_ERR_BAD_DIM;
+  int64_t n;
+  if (__builtin_mul_overflow(rows, *stride, &n) || n > INT64_MAX / 16) return SSM_ERR_BAD_DIM;
+  if ((*stride * es) % 16 != 0) return SSM_ERR_MISALIGNED;
+  return SSM_OK;
+}
+
+constexpr int64_t kMaxHeads = 1 << 15;
+// Every byte count and grid below stays far inside 64 (and 32) bits when no
+// tensor has more elements than this.
+constexpr int64_t kMaxElems = (int64_t)1 << 48;
+
+int check_linear_attn_dims(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_kv, int64_t d_k, int64_t d_v,
+                           int32_t io_dtype) {
+  if (batch < 0 || seqlen < 0 || nheads < 0 || nheads_kv <= 0 || d_k <= 0 || d_v <= 0) return SSM_ERR_BAD_DIM;
+  if (seqlen > kMaxSeqlen || nheads > kMaxHeads) return SSM_ERR_BAD_DIM;
+  if (io_dtype != SSM_DTYPE_F32 && io_dtype != SSM_DTYPE_BF16) return SSM_ERR_UNSUPPORTED;
+  if ((d_k != 64 && d_k != 128) || (d_v != 64 && d_v != 128) || nheads % nheads_kv != 0) return SSM_ERR_UNSUPPORTED;
+  int64_t n, st;
+  if (!mul3(batch, seqlen, nheads * 128, &n) || !mul3(batch, nheads, d_k * d_v, &st)) return SSM_ERR_BAD_DIM;
+  if (n > kMaxElems || st > kMaxElems) return SSM_ERR_BAD_DIM;
+  const ssm::LinAttnPlan pl = ssm::linear_attn_plan(batch, seqlen, nheads, d_k, d_v, io_dtype == SSM_DTYPE_BF16);
+  if (batch * nheads * 2 * pl.n_spans > INT32_MAX || st / 1024 + 1 > INT32_MAX || n / 1024 + 1 > INT32_MAX)
+    return SSM_ERR_BAD_DIM;
+  return SSM_OK;
+}
+
+// Forward (d_o NULL and grad false) and gradient share their checks.
+int linear_attn_impl(ssm::LinAttnLaunch p, int32_t io_dtype, bool grad, size_t workspace_bytes) {
+  int rc = check_linear_attn_dims(p.batch, p.seqlen, p.nheads, p.nheads_kv, p.d_k, p.d_v, io_dtype);
+  if (rc != SSM_OK) return rc;
+  p.bf16 = io_dtype == SSM_DTYPE_BF16;
+  const int64_t es = p.bf16 ? 2 : 4;
+  const int64_t tokens = p.batch * p.seqlen;
+  const int64_t wq = p.nheads * p.d_k, wk = p.nheads_kv * p.d_k, wv = p.nheads_kv * p.d_v, wo = p.nheads * p.d_v;
+  if ((rc = check_stride(&p.q_stride, wq, tokens, es)) != SSM_OK) return rc;
+  if ((rc = check_stride(&p.k_stride, wk, tokens, es)) != SSM_OK) return rc;
+  if ((rc = check_stride(&p.v_stride, wv, tokens, es)) != SSM_OK) return rc;
+  const int64_t n = tokens * p.nheads, b_h = p.batch * p.nheads * p.d_k * p.d_v * 4;
+
+  if (n > 0 && (p.q == nullptr || p.k == nullptr || p.v == nullptr)) return SSM_ERR_NULL_ARG;
+  if (p.nheads > 0 && p.batch > 0 && p.log_decay == nullptr) return SSM_ERR_NULL_ARG;
+  if (n > 0 && !grad && p.o == nullptr) return SSM_ERR_NULL_ARG;
+  if (n > 0 && grad && (p.d_o == nullptr || p.dq == nullptr || p.dk == nullptr || p.dv == nullptr))
+    return SSM_ERR_NULL_ARG;
+
+  const void* a16[] = {p.q, p.k, p.v, p.o, p.h0, p.h_last, p.d_o, p.dh_last, p.dq, p.dk, p.dv, p.dh0};
+  for (const void* q : a16)
+    if (!aligned(q, 16)) return SSM_ERR_MISALIGNED;
+  if (!aligned(p.log_decay, 4) || !aligned(p.lengths, 4)) return SSM_ERR_MISALIGNED;
+
+  // h_last may be h0 itself, so h0 is compared apart from the other inputs.
+  const Rows ins[] = {Rows{p.q, tokens, wq * es, p.q_stride * es}, Rows{p.k, tokens, wk * es, p.k_stride * es},
+                      Rows{p.v, tokens, wv * es, p.v_stride * es}, dense(p.log_decay, p.nheads * 4),
+                      dense(p.lengths, p.batch * 4), dense(p.d_o, tokens * wo * es), dense(p.dh_last, b_h),
+                      dense(p.h_last == p.h0 ? nullptr : p.h0, b_h)};
+  const Rows outs[] = {dense(p.o, tokens * wo * es), dense(p.h_last, b_h), dense(p.dq, tokens * wq * es),
+                       dense(p.dk, tokens * wk * es), dense(p.dv, tokens * wv * es), dense(p.dh0, b_h)};
+  if ((rc = check_alias(outs, 6, ins, 8)) != SSM_OK) return rc;
+
+  const int64_t floats =
+      grad ? ssm::linear_attn_bwd_floats(p.batch, p.seqlen, p.nheads, p.nheads_kv, p.d_k, p.d_v, p.bf16)
+           : ssm::linear_attn_fwd_floats(p.batch, p.seqlen, p.nheads, p.d_k, p.d_v, p.bf16);
+  if (floats > 0) {
+    if (p.workspace == nullptr || workspace_bytes < (size_t)floats * 4) return SSM_ERR_WORKSPACE;
+    if (!aligned(p.workspace, kWorkspaceAlign)) return SSM_ERR_MISALIGNED;
+    const Rows ws = dense(p.workspace, floats * 4);
+    if ((rc = check_alias(&ws, 1, ins, 8)) != SSM_OK || (rc = check_alias(&ws, 1, outs, 6)) != SSM_OK) return rc;
+    if (overlap(ws, dense(p.h0, b_h))) return SSM_ERR_ALIAS;
+  }
+  if (p.batch == 0 || p.nheads == 0) return SSM_OK;
+  const hipError_t err = grad ? ssm::launch_linear_attn_bwd(p) : ssm::launch_linear_attn_fwd(p);
+  return err == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+int linear_attn_update_impl(ssm::LinAttnUpdateLaunch p, int32_t io_dtype) {
+  if (p.batch < 0 || p.n_slots < 0 || p.nheads < 0 || p.nheads_kv <= 0 || p.d_k <= 0 || p.d_v <= 0)
+    return SSM_ERR_BAD_DIM;
+  if (p.nheads > kMaxHeads || p.batch > kMaxSeqlen || p.n_slots > kMaxSeqlen) return SSM_ERR_BAD_DIM;
+  if (p.slots == nullptr && p.n_slots != p.batch) return SSM_ERR_BAD_DIM;
+  if (io_dtype != SSM_DTYPE_F32 && io_dtype != SSM_DTYPE_BF16) return SSM_ERR_UNSUPPORTED;
+  if ((p.d_k != 64 && p.d_k != 128) || (p.d_v != 64 && p.d_v != 128) || p.nheads % p.nheads_kv != 0)
+    return SSM_ERR_UNSUPPORTED;
+  p.bf16 = io_dtype == SSM_DTYPE_BF16;
+  const int64_t es = p.bf16 ? 2 : 4;
+  const int64_t wq = p.nheads * p.d_k, wk = p.nheads_kv * p.d_k, wv = p.nheads_kv * p.d_v, wo = p.nheads * p.d_v;
+  int rc;
+  if ((rc = check_stride(&p.q_stride, wq, p.batch, es)) != SSM_OK) return rc;
+  if ((rc = check_stride(&p.k_stride, wk, p.batch, es)) != SSM_OK) return rc;
+  if ((rc = check_stride(&p.v_stride, wv, p.batch, es)) != SSM_OK) return rc;
+  const int64_t n = p.batch * p.nheads;
+  if (n > 0 && (p.q == nullptr || p.k == nullptr || p.v == nullptr || p.o == nullptr || p.log_decay == nullptr))
+    return SSM_ERR_NULL_ARG;
+  if (n > 0 && p.n_slots > 0 && p.h == nullptr) return SSM_ERR_NULL_ARG;
+  const void* a16[] = {p.h, p.q, p.k, p.v, p.o};
+  for (const void* q : a16)
+    if (!aligned(q, 16)) return SSM_ERR_MISALIGNED;
+  if (!aligned(p.log_decay, 4) || !aligned(p.slots, 4)) return SSM_ERR_MISALIGNED;
+  const Rows ins[] = {Rows{p.q, p.batch, wq * es, p.q_stride * es}, Rows{p.k, p.batch, wk * es, p.k_stride * es},
+                      Rows{p.v, p.batch, wv * es, p.v_stride * es}, dense(p.log_decay, p.nheads * 4),
+                      dense(p.slots, p.batch * 4)};
+  const Rows outs[] = {dense(p.h, p.n_slots * p.nheads * p.d_k * p.d_v * 4), dense(p.o, p.batch * wo * es)};
+  if ((rc = check_alias(outs, 2, ins, 5)) != SSM_OK) return rc;
+  if (n == 0) return SSM_OK;
+  if (ssm::linear_attn_update_blocks(p.batch, p.nheads, p.d_k, p.d_v) > INT32_MAX) return SSM_ERR_BAD_DIM;
+  return ssm::launch_linear_attn_update(p) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+int check_qk_dims(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_k, int64_t headdim) {
+  if (batch < 0 || seqlen < 0 || nheads < 0 || nheads_k < 0 || headdim <= 0) return SSM_ERR_BAD_DIM;
+  if (seqlen > kMaxSeqlen || nheads > kMaxHeads || nheads_k > kMaxHeads) return SSM_ERR_BAD_DIM;
+  if (headdim % 16 != 0 || headdim > 256) return SSM_ERR_UNSUPPORTED;
+  int64_t tokens, n;
+  if (!mul3(batch, seqlen, 1, &tokens) || !mul3(tokens, nheads + nheads_k, headdim, &n) || n > kMaxElems)
+    return SSM_ERR_BAD_DIM;
+  if (tokens > INT32_MAX) return SSM_ERR_BAD_DIM;
+  return SSM_OK;
+}
+
+int qk_norm_rope_impl(ssm::QkNormRopeLaunch p, int32_t io_dtype, int32_t interleaved, bool grad,
+                      size_t workspace_bytes) {
+  int rc = check_qk_dims(p.batch, p.seqlen, p.nheads, p.nheads_k, p.headdim);
+  if (rc != SSM_OK) return rc;
+  if (io_dtype != SSM_DTYPE_F32 && io_dtype != SSM_DTYPE_BF16) return SSM_ERR_UNSUPPORTED;
+  if (p.rot_dim < 0 || p.rot_dim > p.headdim || p.rot_dim % 16 != 0) return SSM_ERR_UNSUPPORTED;
+  if (!(p.eps >= 0.f) || (interleaved != 0 && interleaved != 1)) return SSM_ERR_UNSUPPORTED;
+  p.bf16 = io_dtype == SSM_DTYPE_BF16;
+  p.interleaved = interleaved == 1;
+  const int64_t es = p.bf16 ? 2 : 4, tokens = p.batch * p.seqlen;
+  const int64_t wq = p.nheads * p.headdim, wk = p.nheads_k * p.headdim;
+  if ((rc = check_stride(&p.q_stride, wq, tokens, es)) != SSM_OK) return rc;
+  if ((rc = check_stride(&p.k_stride, wk, tokens, es)) != SSM_OK) return rc;
+  if ((rc = check_stride(&p.q_out_stride, wq, tokens, es)) != SSM_OK) return rc;
+  if ((rc = check_stride(&p.k_out_stride, wk, tokens, es)) != SSM_OK) return rc;
+  const bool has_q = tokens > 0 && p.nheads > 0, has_k = tokens > 0 && p.nheads_k > 0;
+  if (has_q && (p.q == nullptr || p.q_out == nullptr || (grad && p.dq_out == nullptr))) return SSM_ERR_NULL_ARG;
+  if (has_k && (p.k == nullptr || p.k_out == nullptr || (grad && p.dk_out == nullptr))) return SSM_ERR_NULL_ARG;
+  if ((has_q || has_k) && p.rot_dim > 0 && p.inv_freq == nullptr) return SSM_ERR_NULL_ARG;
+  const void* a16[] = {p.q, p.k, p.q_out, p.k_out, p.dq_out, p.dk_out};
+  for (const void* q : a16)
+    if (!aligned(q, 16)) return SSM_ERR_MISALIGNED;
+  if (!aligned(p.wq, 4) || !aligned(p.wk, 4) || !aligned(p.inv_freq, 4) || !aligned(p.positions, 8) ||
+      !aligned(p.dwq, 4) || !aligned(p.dwk, 4))
+    return SSM_ERR_MISALIGNED;
+  const int64_t b_w = p.headdim * 4;
+  const Rows q{p.q, tokens, wq * es, p.q_stride * es}, k{p.k, tokens, wk * es, p.k_stride * es};
+  const Rows qo{p.q_out, tokens, wq * es, p.q_out_stride * es}, ko{p.k_out, tokens, wk * es, p.k_out_stride * es};
+  const bool q_in_place = !grad && p.q_out == p.q && p.q_out_stride == p.q_stride;
+  const bool k_in_place = !grad && p.k_out == p.k && p.k_out_stride == p.k_stride;
+  const Rows none{nullptr, 0, 0, 0};
+  const Rows ins[] = {q_in_place ? none : q, k_in_place ? none : k, dense(p.wq, b_w), dense(p.wk, b_w),
+                      dense(p.inv_freq, p.rot_dim * 2), dense(p.positions, tokens * 8),
+                      dense(p.dq_out, tokens * wq * es), dense(p.dk_out, tokens * wk * es)};
+  const Rows outs[] = {qo, ko, dense(p.dwq, b_w), dense(p.dwk, b_w)};
+  if ((rc = check_alias(outs, 4, ins, 8)) != SSM_OK) return rc;
+  if (grad && (p.dwq != nullptr || p.dwk != nullptr)) {
+    const int64_t need = ssm::qk_norm_rope_bwd_floats(tokens, p.nheads, p.nheads_k, p.headdim) * 4;
+    if (need > 0) {
+      if (p.workspace == nullptr || workspace_bytes < (size_t)need) return SSM_ERR_WORKSPACE;
+      if (!aligned(p.workspace, kWorkspaceAlign)) return SSM_ERR_MISALIGNED;
+      const Rows ws = dense(p.workspace, need);
+      if ((rc = check_alias(&ws, 1, ins, 8)) != SSM_OK || (rc = check_alias(&ws, 1, outs, 4)) != SSM_OK) return rc;
+    }
+  }
+  if (!grad && !has_q && !has_k) return SSM_OK;
+  const hipError_t err = grad ? ssm::launch_qk_norm_rope_bwd(p) : ssm::launch_qk_norm_rope(p);
+  return err == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
 }  // namespace
 
 extern "C" {
+
+int ssm_linear_attn_fwd(const void* q, const void* k, const void* v, const float* log_decay, const int32_t* lengths,
+                        const float* h0, void* o, float* h_last, int64_t batch, int64_t seqlen, int64_t nheads,
+                        int64_t nheads_kv, int64_t d_k, int64_t d_v, int64_t q_stride, int64_t k_stride,
+                        int64_t v_stride, float scale, int32_t io_dtype, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  ssm::LinAttnLaunch p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.log_decay = log_decay;
+  p.lengths = lengths;
+  p.h0 = h0;
+  p.o = o;
+  p.h_last = h_last;
+  p.batch = batch;
+  p.seqlen = seqlen;
+  p.nheads = nheads;
+  p.nheads_kv = nheads_kv;
+  p.d_k = d_k;
+  p.d_v = d_v;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.scale = scale;
+  p.workspace = static_cast<float*>(workspace);
+  p.stream = static_cast<hipStream_t>(stream);
+  return linear_attn_impl(p, io_dtype, false, workspace_bytes);
+}
+
+size_t ssm_linear_attn_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v,
+                                          int32_t io_dtype) {
+  if (check_linear_attn_dims(batch, seqlen, nheads, 1, d_k, d_v, io_dtype) != SSM_OK) return (size_t)-1;
+  return (size_t)ssm::linear_attn_fwd_floats(batch, seqlen, nheads, d_k, d_v, io_dtype == SSM_DTYPE_BF16) * 4;
+}
+
+int ssm_linear_attn_bwd(const void* q, const void* k, const void* v, const float* log_decay, const int32_t* lengths,
+                        const float* h0, const void* d_o, const float* dh_last, void* dq, void* dk, void* dv,
+                        float* dh0, int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_kv, int64_t d_k,
+                        int64_t d_v, int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale,
+                        int32_t io_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  ssm::LinAttnLaunch p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.log_decay = log_decay;
+  p.lengths = lengths;
+  p.h0 = h0;
+  p.d_o = d_o;
+  p.dh_last = dh_last;
+  p.dq = dq;
+  p.dk = dk;
+  p.dv = dv;
+  p.dh0 = dh0;
+  p.batch = batch;
+  p.seqlen = seqlen;
+  p.nheads = nheads;
+  p.nheads_kv = nheads_kv;
+  p.d_k = d_k;
+  p.d_v = d_v;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.scale = scale;
+  p.workspace = static_cast<float*>(workspace);
+  p.stream = static_cast<hipStream_t>(stream);
+  return linear_attn_impl(p, io_dtype, true, workspace_bytes);
+}
+
+size_t ssm_linear_attn_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_kv,
+                                          int64_t d_k, int64_t d_v, int32_t io_dtype) {
+  if (check_linear_attn_dims(batch, seqlen, nheads, nheads_kv, d_k, d_v, io_dtype) != SSM_OK) return (size_t)-1;
+  return (size_t)ssm::linear_attn_bwd_floats(batch, seqlen, nheads, nheads_kv, d_k, d_v,
+                                             io_dtype == SSM_DTYPE_BF16) * 4;
+}
+
+int ssm_linear_attn_update(float* h, const int32_t* slots, const void* q, const void* k, const void* v,
+                           const float* log_decay, void* o, int64_t batch, int64_t n_slots, int64_t nheads,
+                           int64_t nheads_kv, int64_t d_k, int64_t d_v, int64_t q_stride, int64_t k_stride,
+                           int64_t v_stride, float scale, int32_t io_dtype, void* stream) {
+  ssm::LinAttnUpdateLaunch p{h,   slots, q,   k,        v,        log_decay, o,     batch, n_slots, nheads, nheads_kv,
+                             d_k, d_v,   q_stride, k_stride, v_stride, scale, false, static_cast<hipStream_t>(stream)};
+  return linear_attn_update_impl(p, io_dtype);
+}
+
+int ssm_qk_norm_rope_fwd(const void* q, const void* k, const float* wq, const float* wk, const float* inv_freq,
+                         const int64_t* positions, void* q_out, void* k_out, int64_t batch, int64_t seqlen,
+                         int64_t nheads, int64_t nheads_k, int64_t headdim, int64_t rot_dim, int64_t q_stride,
+                         int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride, float eps,
+                         int32_t interleaved, int32_t io_dtype, void* stream) {
+  ssm::QkNormRopeLaunch p{};
+  p.q = q;
+  p.k = k;
+  p.wq = wq;
+  p.wk = wk;
+  p.inv_freq = inv_freq;
+  p.positions = positions;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.batch = batch;
+  p.seqlen = seqlen;
+  p.nheads = nheads;
+  p.nheads_k = nheads_k;
+  p.headdim = headdim;
+  p.rot_dim = rot_dim;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.q_out_stride = q_out_stride;
+  p.k_out_stride = k_out_stride;
+  p.eps = eps;
+  p.stream = static_cast<hipStream_t>(stream);
+  return qk_norm_rope_impl(p, io_dtype, interleaved, false, 0);
+}
+
+int ssm_qk_norm_rope_bwd(const void* q, const void* k, const float* wq, const float* wk, const float* inv_freq,
+                         const int64_t* positions, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                         float* dwq, float* dwk, int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_k,
+                         int64_t headdim, int64_t rot_dim, int64_t q_stride, int64_t k_stride, float eps,
+                         int32_t interleaved, int32_t io_dtype, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  ssm::QkNormRopeLaunch p{};
+  p.q = q;
+  p.k = k;
+  p.wq = wq;
+  p.wk = wk;
+  p.inv_freq = inv_freq;
+  p.positions = positions;
+  p.dq_out = dq_out;
+  p.dk_out = dk_out;
+  p.q_out = dq;
+  p.k_out = dk;
+  p.dwq = dwq;
+  p.dwk = dwk;
+  p.batch = batch;
+  p.seqlen = seqlen;
+  p.nheads = nheads;
+  p.nheads_k = nheads_k;
+  p.headdim = headdim;
+  p.rot_dim = rot_dim;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.eps = eps;
+  p.workspace = static_cast<float*>(workspace);
+  p.stream = static_cast<hipStream_t>(stream);
+  return qk_norm_rope_impl(p, io_dtype, interleaved, true, workspace_bytes);
+}
+
+size_t ssm_qk_norm_rope_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_k,
+                                           int64_t headdim) {
+  if (check_qk_dims(batch, seqlen, nheads, nheads_k, headdim) != SSM_OK) return (size_t)-1;
+  return (size_t)ssm::qk_norm_rope_bwd_floats(batch * seqlen, nheads, nheads_k, headdim) * 4;
+}
 
 int ssm_conv1d_fwd(const void* x, const float* w, const float* bias, const float* state_in, void* y,
                    float* state_out, int64_t batch, int64_t seqlen, int64_t d_inner, int64_t d_conv,

@@ -1,0 +1,442 @@
+// Linear attention with a constant decay per head: the sweep on the fp32
+// matrix instructions, the carries between spans, the sums over shared heads,
+// and the launch sequences of the forward and gradient calls.
+#include "linear_attn.h"
+
+namespace ssm {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+
+// ---- the sweep, fp32 products -------------------------------------------
+//
+// One workgroup (4 waves) per (row, head), span and slice of 64 output
+// columns; wave w owns 16 of them, for the outputs and for the state, which
+// stays in the accumulators.  Blocks of 32 steps: a, b and c are staged in LDS
+// as fp32 while the next block's rows are on their way in registers.  All
+// products run on v_mfma_f32_16x16x4_f32: S^T = B A^T (shared through LDS),
+// out^T = C^T P^T + E^T A^T, E += B^T (w o C).  The contraction index is
+// taken in the order the accumulators hold rows (4 (lane / 16) + j), so the
+// state and the 16-byte LDS reads feed the products without moving.
+//
+// Bound by the fp32 matrix rate (153 TFLOP/s in a large product on this
+// card), an eighth of the bf16 one; 32 steps keep the pair products (which
+// grow with the block) below a fifth of the state products.
+constexpr int kT = 32;        // steps per block
+constexpr int kCols = 64;     // output columns per workgroup
+constexpr int kSc = kCols + 4;  // LDS row strides (floats) with rows 4 apart on different banks
+constexpr int kSp = kT + 4;
+
+template <typename T>
+__device__ __forceinline__ f32x4 load4(const T* p);
+template <>
+__device__ __forceinline__ f32x4 load4<float>(const float* p) {
+  return *reinterpret_cast<const f32x4*>(p);
+}
+template <>
+__device__ __forceinline__ f32x4 load4<uint16_t>(const uint16_t* p) {
+  const u16x4 v = *reinterpret_cast<const u16x4*>(p);
+  return f32x4{io_to_f32(v[0]), io_to_f32(v[1]), io_to_f32(v[2]), io_to_f32(v[3])};
+}
+__device__ __forceinline__ void store4(float* p, const f32x4& v) { *reinterpret_cast<f32x4*>(p) = v; }
+__device__ __forceinline__ void store4(uint16_t* p, const f32x4& v) {
+  u16x4 r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = __builtin_bit_cast(uint16_t, (__bf16)v[j]);
+  *reinterpret_cast<u16x4*>(p) = r;
+}
+
+// SUM: only the state of the span from a zero entry (a and out unused).
+template <typename T, typename O, int KD, bool REV, bool SUM>
+__global__ void __launch_bounds__(256) k_attn_sweep_f32(const AttnSweep s) {
+  constexpr int kSa = KD + 4;
+  constexpr int NT = KD / 16;          // state tiles
+  constexpr int PA = kT * KD / 4 / 256;  // 4-element pieces of a and b per thread
+  constexpr int PC = kT * kCols / 4 / 256;
+  __shared__ __align__(16) float sA[SUM ? 1 : kT * kSa];
+  __shared__ __align__(16) float sB[kT * kSa];
+  __shared__ __align__(16) float sC[kT * kSc];
+  __shared__ __align__(16) float sP[SUM ? 1 : kT * kSp];  // decayed pairs [t][i]
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r16 = lane & 15, q4 = lane >> 4;
+  int64_t id = xcd_remap(blockIdx.x, gridDim.x);
+  const int slice = (int)(id % s.slices);
+  id /= s.slices;
+  const int64_t row = id % s.rows, span = id / s.rows;
+  const int64_t b = row / s.nheads;
+  const int h = (int)(row % s.nheads);
+  const int64_t VD = (int64_t)s.slices * kCols;
+  const int col0 = slice * kCols;
+  const int64_t len = row_length(s.lengths, b, s.seqlen);
+  const int64_t s0 = span * s.span_len;
+  const int64_t s1 = min(s0 + s.span_len, s.seqlen);
+  const int64_t e = min(s1, len) > s0 ? min(s1, len) : s0;  // steps [s0, e) are computed
+  const float g = decay_log2(s.log_decay[h]);
+
+  const T* const A = SUM ? nullptr : static_cast<const T*>(s.a.p) + b * s.seqlen * s.a.stride + (h / s.a.rep) * KD;
+  const T* const B = static_cast<const T*>(s.b.p) + b * s.seqlen * s.b.stride + (h / s.b.rep) * KD;
+  const T* const C = static_cast<const T*>(s.c.p) + b * s.seqlen * s.c.stride + (h / s.c.rep) * VD + col0;
+  O* const out = SUM ? nullptr : static_cast<O*>(s.out) + (b * s.seqlen * s.nheads + h) * VD + col0;
+
+  // State S[n][p], p = 16 w + r16 of the slice: acc[nt][j] = S[16 nt + 4 q4 + j][p].
+  f32x4 acc[NT];
+  const int64_t soff = (int64_t)(col0 + 16 * w + r16) * s.sp;
+  {
+    const float* ep = nullptr;
+    if (!SUM && s.entry != nullptr) ep = s.entry + ((s.n_spans > 1 ? span * s.rows : 0) + row) * KD * VD + soff;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[nt][j] = ep != nullptr ? ep[(16 * nt + 4 * q4 + j) * s.sn] : 0.f;
+  }
+
+  f32x4 ra[SUM ? 1 : PA], rb[PA], rc[PC];
+  auto fetch = [&](int64_t t0) {
+    const int m = (int)min((int64_t)kT, e - t0);
+#pragma unroll
+    for (int r = 0; r < PA; ++r) {
+      const int piece = tid + 256 * r, t = piece / (KD / 4), n = piece % (KD / 4) * 4;
+      const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+      if (!SUM) ra[r] = t < m ? load4<T>(A + (t0 + t) * s.a.stride + n) : z;
+      rb[r] = t < m ? load4<T>(B + (t0 + t) * s.b.stride + n) : z;
+    }
+#pragma unroll
+    for (int r = 0; r < PC; ++r) {
+      const int piece = tid + 256 * r, t = piece / (kCols / 4), p = piece % (kCols / 4) * 4;
+      rc[r] = t < m ? load4<T>(C + (t0 + t) * s.c.stride + p) : f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  };
+
+  const int64_t nblk = (e - s0 + kT - 1) / kT;
+  if (nblk > 0) fetch(s0 + (REV ? nblk - 1 : 0) * kT);
+  for (int64_t k = 0; k < nblk; ++k) {
+    const int64_t t0 = s0 + (REV ? nblk - 1 - k : k) * kT;
+    const int m = (int)min((int64_t)kT, e - t0);
+    __syncthreads();  // the previous block is done with the tiles
+#pragma unroll
+    for (int r = 0; r < PA; ++r) {
+      const int piece = tid + 256 * r, t = piece / (KD / 4), n = piece % (KD / 4) * 4;
+      if (!SUM) *reinterpret_cast<f32x4*>(&sA[t * kSa + n]) = ra[r];
+      *reinterpret_cast<f32x4*>(&sB[t * kSa + n]) = rb[r];
+    }
+#pragma unroll
+    for (int r = 0; r < PC; ++r) {
+      const int piece = tid + 256 * r, t = piece / (kCols / 4), p = piece % (kCols / 4) * 4;
+      *reinterpret_cast<f32x4*>(&sC[t * kSc + p]) = rc[r];
+    }
+    __syncthreads();
+    if (k + 1 < nblk) fetch(s0 + (REV ? nblk - 2 - k : k + 1) * kT);
+
+    if (!SUM) {
+      // Pairs: tile (it, tt) of wave w, rows i, columns t; the masked one is zero.
+      const int it = w >> 1, tt = w & 1;
+      f32x4 sc = {0.f, 0.f, 0.f, 0.f};
+      if (REV ? it >= tt : it <= tt) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const f32x4 bv = *reinterpret_cast<const f32x4*>(&sB[(16 * it + r16) * kSa + 16 * nt + 4 * q4]);
+          const f32x4 av = *reinterpret_cast<const f32x4*>(&sA[(16 * tt + r16) * kSa + 16 * nt + 4 * q4]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sc = __builtin_amdgcn_mfma_f32_16x16x4f32(bv[j], av[j], sc, 0, 0, 0);
+        }
+      }
+      const int t = 16 * tt + r16;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = 16 * it + 4 * q4 + j;
+        const int d = REV ? i - t : t - i;
+        sc[j] = d >= 0 ? sc[j] * (hw_exp2(g * (float)d) * s.s_pair) : 0.f;
+      }
+      *reinterpret_cast<f32x4*>(&sP[t * kSp + 16 * it + 4 * q4]) = sc;
+      __syncthreads();
+    }
+
+    // This wave's columns of c over the block: cv[it][j] = c[16 it + 4 q4 + j][p].
+    f32x4 cv[2];
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) cv[it][j] = sC[(16 * it + 4 * q4 + j) * kSc + 16 * w + r16];
+
+    if (!SUM) {
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt) {
+        const int t = 16 * tt + r16;
+        f32x4 op = {0.f, 0.f, 0.f, 0.f}, oe = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int it = 0; it < 2; ++it) {
+          const f32x4 pv = *reinterpret_cast<const f32x4*>(&sP[t * kSp + 16 * it + 4 * q4]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) op = __builtin_amdgcn_mfma_f32_16x16x4f32(cv[it][j], pv[j], op, 0, 0, 0);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const f32x4 av = *reinterpret_cast<const f32x4*>(&sA[t * kSa + 16 * nt + 4 * q4]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) oe = __builtin_amdgcn_mfma_f32_16x16x4f32(acc[nt][j], av[j], oe, 0, 0, 0);
+        }
+        if (t < m) {
+          const float rf = hw_exp2(g * (float)(REV ? m - 1 - t : t + 1)) * s.s_read;
+          f32x4 v;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(rf, oe[j], op[j]);
+          store4(out + (t0 + t) * s.nheads * VD + 16 * w + 4 * q4, v);
+        }
+      }
+    }
+
+    // E <- gamma^m E + B^T (w o C).
+    const float fac = hw_exp2(g * (float)m);
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = 16 * it + 4 * q4 + j;
+        const float wt = i < m ? hw_exp2(g * (float)(REV ? i + 1 : m - 1 - i)) * s.s_write : 0.f;
+        cv[it][j] *= wt;
+      }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      acc[nt] *= fac;
+#pragma unroll
+      for (int it = 0; it < 2; ++it)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float bv = sB[(16 * it + 4 * q4 + j) * kSa + 16 * nt + r16];
+          acc[nt] = __builtin_amdgcn_mfma_f32_16x16x4f32(bv, cv[it][j], acc[nt], 0, 0, 0);
+        }
+    }
+  }
+
+  if (!SUM) {
+    // Rows behind the sequence's end.
+    for (int64_t t = e + (tid >> 4); t < s1; t += 16)
+      store4(out + t * s.nheads * VD + 4 * (tid & 15), f32x4{0.f, 0.f, 0.f, 0.f});
+  }
+  if (s.exit != nullptr && (SUM || span == (REV ? 0 : s.n_spans - 1))) {
+    float* xp = s.exit + ((SUM ? span * s.rows : 0) + row) * KD * VD + soff;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) xp[(16 * nt + 4 * q4 + j) * s.sn] = acc[nt][j];
+  }
+}
+
+// ---- carries between spans ----------------------------------------------
+// In place: st[span][row][...] holds every span's state from a zero entry and
+// receives the state that enters the span: E_0 = start, E_{s+1} = gamma^len_s
+// E_s + S_s (from the last span downwards in reverse).  Four elements a
+// thread, sums in span order.
+template <bool REV>
+__global__ void __launch_bounds__(256) k_attn_carry(float* st, const float* start, const float* log_decay,
+                                                    const int32_t* lengths, int64_t rows, int32_t nheads,
+                                                    int64_t state4, int64_t seqlen, int64_t span_len,
+                                                    int64_t n_spans) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= rows * state4) return;
+  const int64_t row = i / state4;
+  const float g = decay_log2(log_decay[row % nheads]);
+  const int64_t len = row_length(lengths, row / nheads, seqlen);
+  f32x4* const p = reinterpret_cast<f32x4*>(st) + i;
+  f32x4 e = start != nullptr ? reinterpret_cast<const f32x4*>(start)[i] : f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4 own = p[(REV ? n_spans - 1 : 0) * rows * state4];
+  for (int64_t k = 0; k < n_spans; ++k) {
+    const int64_t s = REV ? n_spans - 1 - k : k;
+    const f32x4 cur = own;
+    if (k + 1 < n_spans) own = p[(REV ? s - 1 : s + 1) * rows * state4];
+    p[s * rows * state4] = e;
+    const int64_t s0 = s * span_len, s1 = min(s0 + span_len, seqlen);
+    const int64_t m = min(s1, len) > s0 ? min(s1, len) - s0 : 0;
+    const float f = hw_exp2(g * (float)m);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) e[j] = __builtin_fmaf(f, e[j], cur[j]);
+  }
+}
+
+// ---- sums over the heads that share a key/value head --------------------
+template <typename T>
+__global__ void __launch_bounds__(256) k_attn_sum_heads(const float* part, T* out, int64_t n4, int32_t d4,
+                                                        int32_t rep) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // (step, kv head, 4 columns)
+  if (i >= n4) return;
+  const int64_t head = i / d4;
+  const f32x4* p = reinterpret_cast<const f32x4*>(part) + head * rep * d4 + i % d4;
+  f32x4 v = p[0];
+  for (int r = 1; r < rep; ++r) v += p[(int64_t)r * d4];
+  store4(out + i * 4, v);
+}
+
+int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
+
+template <typename T, typename O, bool REV, bool SUM>
+hipError_t sweep_f32(const AttnSweep& s, int64_t kd, hipStream_t stream) {
+  const unsigned grid = (unsigned)(s.rows * s.n_spans * s.slices);
+  if (kd == 64) return launch(k_attn_sweep_f32<T, O, 64, REV, SUM>, dim3(grid), dim3(256), 0, stream, s);
+  return launch(k_attn_sweep_f32<T, O, 128, REV, SUM>, dim3(grid), dim3(256), 0, stream, s);
+}
+
+// out32: the outputs go to an fp32 buffer although the inputs are bf16.
+template <bool REV, bool SUM>
+hipError_t sweep(AttnSweep s, int64_t kd, int64_t vd, bool bf16, bool out32, hipStream_t stream) {
+  s.slices = (int32_t)(vd / kCols);
+  if (!bf16) return sweep_f32<float, float, REV, SUM>(s, kd, stream);
+  if (out32 || SUM) return sweep_f32<uint16_t, float, REV, SUM>(s, kd, stream);
+  return sweep_f32<uint16_t, uint16_t, REV, SUM>(s, kd, stream);
+}
+
+template <bool REV>
+hipError_t carry(float* st, const float* start, const LinAttnLaunch& p, const LinAttnPlan& pl) {
+  const int64_t rows = p.batch * p.nheads, state4 = p.d_k * p.d_v / 4;
+  const unsigned grid = (unsigned)((rows * state4 + 255) / 256);
+  return launch(k_attn_carry<REV>, dim3(grid), dim3(256), 0, p.stream, st, start, p.log_decay, p.lengths, rows,
+                (int32_t)p.nheads, state4, p.seqlen, pl.span_len, pl.n_spans);
+}
+
+AttnSweep base(const LinAttnLaunch& p, const LinAttnPlan& pl) {
+  AttnSweep s{};
+  s.log_decay = p.log_decay;
+  s.lengths = p.lengths;
+  s.seqlen = p.seqlen;
+  s.span_len = pl.span_len;
+  s.n_spans = pl.n_spans;
+  s.nheads = (int32_t)p.nheads;
+  s.rows = p.batch * p.nheads;
+  return s;
+}
+
+}  // namespace
+
+// Workgroups a launch should have: below, the sequence is cut into spans of at
+// least kMinSpan steps, at the price of reading b and c twice.
+constexpr int64_t kTargetGroups = 1024;
+constexpr int64_t kMinSpan = 128;
+
+LinAttnPlan linear_attn_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16) {
+  (void)bf16;
+  const int64_t groups = batch * nheads * ((d_k > d_v ? d_k : d_v) / kCols);
+  int64_t n = 1;
+  if (groups > 0 && groups < kTargetGroups / 2) n = kTargetGroups / groups;
+  if (n > seqlen / kMinSpan) n = seqlen / kMinSpan;
+  if (n < 1) n = 1;
+  int64_t len = (seqlen + n - 1) / n;
+  len = (len + kT - 1) / kT * kT;
+  if (len < kT) len = kT;
+  return LinAttnPlan{len, seqlen > 0 ? (seqlen + len - 1) / len : 1};
+}
+
+int64_t linear_attn_fwd_floats(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16) {
+  const LinAttnPlan pl = linear_attn_plan(batch, seqlen, nheads, d_k, d_v, bf16);
+  return pl.n_spans > 1 ? pl.n_spans * batch * nheads * d_k * d_v : 0;
+}
+
+int64_t linear_attn_bwd_floats(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_kv, int64_t d_k,
+                               int64_t d_v, bool bf16) {
+  int64_t n = 2 * linear_attn_fwd_floats(batch, seqlen, nheads, d_k, d_v, bf16);
+  if (nheads != nheads_kv) n += up64(batch * seqlen * nheads * d_k) + up64(batch * seqlen * nheads * d_v);
+  return n;
+}
+
+hipError_t launch_linear_attn_fwd(const LinAttnLaunch& p) {
+  const LinAttnPlan pl = linear_attn_plan(p.batch, p.seqlen, p.nheads, p.d_k, p.d_v, p.bf16);
+  const int32_t rep = (int32_t)(p.nheads / p.nheads_kv);
+  AttnSweep s = base(p, pl);
+  s.a = AttnOperand{p.q, p.q_stride, 1};
+  s.b = AttnOperand{p.k, p.k_stride, rep};
+  s.c = AttnOperand{p.v, p.v_stride, rep};
+  s.sn = 1;
+  s.sp = p.d_k;
+  s.s_pair = s.s_read = p.scale;
+  s.s_write = 1.f;
+  s.entry = p.h0;
+  if (pl.n_spans > 1) {
+    AttnSweep z = s;
+    z.exit = p.workspace;
+    hipError_t rc = sweep<false, true>(z, p.d_k, p.d_v, p.bf16, false, p.stream);
+    if (rc != hipSuccess) return rc;
+    rc = carry<false>(p.workspace, p.h0, p, pl);
+    if (rc != hipSuccess) return rc;
+    s.entry = p.workspace;
+  }
+  s.exit = p.h_last;
+  s.out = p.o;
+  return sweep<false, false>(s, p.d_k, p.d_v, p.bf16, false, p.stream);
+}
+
+hipError_t launch_linear_attn_bwd(const LinAttnLaunch& p) {
+  const LinAttnPlan pl = linear_attn_plan(p.batch, p.seqlen, p.nheads, p.d_k, p.d_v, p.bf16);
+  const int32_t rep = (int32_t)(p.nheads / p.nheads_kv);
+  const AttnOperand q{p.q, p.q_stride, 1}, k{p.k, p.k_stride, rep}, v{p.v, p.v_stride, rep},
+      d{p.d_o, p.nheads * p.d_v, 1};
+  const int64_t states = linear_attn_fwd_floats(p.batch, p.seqlen, p.nheads, p.d_k, p.d_v, p.bf16);
+  const float *h_in = p.h0, *g_in = p.dh_last;
+  hipError_t rc;
+  if (pl.n_spans > 1) {
+    float* const hs = p.workspace;
+    float* const gs = p.workspace + states;
+    AttnSweep z = base(p, pl);
+    z.sn = 1;
+    z.sp = p.d_k;
+    z.b = k;
+    z.c = v;
+    z.s_write = 1.f;
+    z.exit = hs;
+    if ((rc = sweep<false, true>(z, p.d_k, p.d_v, p.bf16, false, p.stream)) != hipSuccess) return rc;
+    z.b = q;
+    z.c = d;
+    z.s_write = p.scale;
+    z.exit = gs;
+    if ((rc = sweep<true, true>(z, p.d_k, p.d_v, p.bf16, false, p.stream)) != hipSuccess) return rc;
+    if ((rc = carry<false>(hs, p.h0, p, pl)) != hipSuccess) return rc;
+    if ((rc = carry<true>(gs, p.dh_last, p, pl)) != hipSuccess) return rc;
+    h_in = hs;
+    g_in = gs;
+  }
+  const bool shared = p.nheads != p.nheads_kv;
+  float* const pk = p.workspace + 2 * states;
+  float* const pv = pk + up64(p.batch * p.seqlen * p.nheads * p.d_k);
+
+  AttnSweep s = base(p, pl);  // dq: the state is H^T
+  s.a = d;
+  s.b = v;
+  s.c = k;
+  s.sn = p.d_k;
+  s.sp = 1;
+  s.s_pair = s.s_read = p.scale;
+  s.s_write = 1.f;
+  s.entry = h_in;
+  s.out = p.dq;
+  if ((rc = sweep<false, false>(s, p.d_v, p.d_k, p.bf16, false, p.stream)) != hipSuccess) return rc;
+  s.a = v;  // dk: the state is G^T
+  s.b = d;
+  s.c = q;
+  s.s_read = 1.f;
+  s.s_write = p.scale;
+  s.entry = g_in;
+  s.out = shared ? pk : p.dk;
+  if ((rc = sweep<true, false>(s, p.d_v, p.d_k, p.bf16, shared, p.stream)) != hipSuccess) return rc;
+  s.a = k;  // dv: the state is G
+  s.b = q;
+  s.c = d;
+  s.sn = 1;
+  s.sp = p.d_k;
+  s.exit = p.dh0;
+  s.out = shared ? pv : p.dv;
+  if ((rc = sweep<true, false>(s, p.d_k, p.d_v, p.bf16, shared, p.stream)) != hipSuccess) return rc;
+  if (!shared) return hipSuccess;
+  auto sum = [&](const float* part, void* out, int64_t dim) {
+    const int64_t n4 = p.batch * p.seqlen * p.nheads_kv * dim / 4;
+    const unsigned grid = (unsigned)((n4 + 255) / 256);
+    if (p.bf16)
+      return launch(k_attn_sum_heads<uint16_t>, dim3(grid), dim3(256), 0, p.stream, part, static_cast<uint16_t*>(out),
+                    n4, (int32_t)(dim / 4), rep);
+    return launch(k_attn_sum_heads<float>, dim3(grid), dim3(256), 0, p.stream, part, static_cast<float*>(out), n4,
+                  (int32_t)(dim / 4), rep);
+  };
+  if ((rc = sum(pk, p.dk, p.d_k)) != hipSuccess) return rc;
+  return sum(pv, p.dv, p.d_v);
+}
+
+}  // namespace ssm

@@ -1,0 +1,149 @@
+"""Norm of query and key heads with the rotation, and its gradient, against the
+64-bit definitions, elementwise within bounds derived from the roundings."""
+import numpy as np
+import pytest
+
+import plain64 as P
+from test_gpu_linear_attn import DEV, _close, _np, _t
+
+pytestmark = pytest.mark.gpu
+
+
+def _tol(out, mag, terms, dtype):
+    """terms roundings of fp32 (twice as coarse for the hardware's reciprocal
+    root and sines), then one of the output."""
+    return P.HALF[dtype] * np.abs(out) + (terms + 16) * 2 * P.U * mag
+
+
+def _make(seed, B, L, H, M, D, R, dtype, far=1 << 20):
+    import torch
+    r = np.random.default_rng(seed)
+    W = (H + M) * D + 48
+    wide = _t(r.standard_normal((B, L, W)), dtype)
+    q = wide[:, :, :H * D].unflatten(2, (H, D))
+    k = wide[:, :, W - M * D:].unflatten(2, (M, D)) if M else None
+    wq, wk = _t(1 + 0.3 * r.standard_normal(D)), _t(1 + 0.3 * r.standard_normal(D))
+    f = _t(10000.0 ** (-np.arange(R // 2) / max(1, R // 2))) if R else None
+    pos = torch.as_tensor(r.integers(-far, far, (B, L)), device=DEV)
+    dq, dk = _t(r.standard_normal((B, L, H, D)), dtype), (_t(r.standard_normal((B, L, M, D)), dtype) if M else None)
+    return q, k, wq, wk, f, pos, dq, dk
+
+
+def _freq(f):
+    return np.zeros(0) if f is None else _np(f)
+
+
+def _check(q, k, wq, wk, f, pos, dq, dk, dtype, eps, inter, D):
+    import torch
+    from selective_state_space_84_amd import binding
+    yq, yk = binding.ssm_qk_norm_rope_fwd(q, k, wq, wk, f, positions=pos, eps=eps, interleaved=inter)
+    g = binding.ssm_qk_norm_rope_bwd(q, k, wq, wk, f, dq_out=dq, dk_out=dk, positions=pos, eps=eps, interleaved=inter)
+    torch.cuda.synchronize()
+    B, L = q.shape[:2]
+    p = np.arange(L)[None].repeat(B, 0) if pos is None else pos.cpu().numpy()
+    for side, x, w, dy, y in (("q", q, wq, dq, yq), ("k", k, wk, dk, yk)):
+        if x is None:
+            assert y is None
+            continue
+        w = None if w is None else _np(w)
+        ref, mag = P.norm_rope(_np(x), w, p, _freq(f), eps, inter)
+        _close(side, _np(y), ref, _tol(ref, mag, D, dtype))
+        dx, dw, dxm, dwm = P.norm_rope_bwd(_np(x), w, p, _freq(f), eps, inter, _np(dy))
+        _close("d" + side, _np(g["d" + side]), dx, _tol(dx, dxm, 2 * D, dtype))
+        rows = x.shape[0] * x.shape[1] * x.shape[2]
+        _close("dw" + side, _np(g["dw" + side]), dw, _tol(dw, dwm, rows + D, "f32"))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D,R", [(16, 16), (32, 16), (64, 64), (80, 32), (96, 96), (128, 0), (128, 64), (128, 128),
+                                 (208, 112), (256, 256)])
+def test_widths(lib, D, R, inter, dtype):
+    print("case", D, R, inter, dtype, flush=True)
+    _check(*_make(D + R, 2, 9, 5, 3, D, R, dtype), dtype, 1e-6, inter, D)
+
+
+@pytest.mark.parametrize("B,L,H,M", [(1, 1, 1, 0), (1, 1, 32, 8), (3, 1, 1, 1), (1, 1100, 1, 1), (2, 700, 3, 2),
+                                     (1, 1030, 40, 2)])
+def test_sizes(lib, B, L, H, M):
+    """One head of one step to more steps than the gradient has workgroups; no key side."""
+    print("case", B, L, H, M, flush=True)
+    _check(*_make(B + L + H, B, L, H, M, 64, 32, "bf16"), "bf16", 1e-6, False, 64)
+
+
+def test_defaults_and_zero_heads(lib):
+    """No weights, positions from 0, a head of zeros with and without eps."""
+    q, k, _, _, f, _, dq, dk = _make(3, 2, 7, 2, 2, 64, 64, "f32")
+    q[0, 0, 0] = 0
+    _check(q, k, None, None, f, None, dq, dk, "f32", 1e-2, False, 64)
+
+
+def test_far_positions_lose_nothing(lib):
+    """Positions up to 2^40: the angle's fraction of a turn stays exact to fp32."""
+    q, k, wq, wk, f, pos, dq, dk = _make(4, 2, 9, 2, 1, 64, 64, "f32", far=1 << 40)
+    # 64-bit products round by 2^-53 of up to 2^40 radians, 2^-13: compare where the reference itself is exact,
+    # i.e. at frequencies that are powers of two.
+    f.copy_(_t(2.0 ** -np.arange(32)))
+    import torch
+    from selective_state_space_84_amd import binding
+    y, _ = binding.ssm_qk_norm_rope_fwd(q, k, wq, wk, f, positions=pos)
+    torch.cuda.synchronize()
+    from fractions import Fraction
+    # Angles reduced with an exact rational 2 pi (a 40-digit value), then in 64 bits.
+    two_pi = Fraction("6.283185307179586476925286766559005768394")
+    p = pos.cpu().numpy()
+    red = np.array([[[float(Fraction(int(p[b, t])) * Fraction(2) ** -j % two_pi) for j in range(32)]
+                     for t in range(9)] for b in range(2)])
+    x = _np(q)
+    n = x / np.sqrt((x * x).mean(-1, keepdims=True) + 1e-6) * _np(wq)
+    c, s = np.cos(red)[:, :, None], np.sin(red)[:, :, None]
+    ref = np.concatenate([n[..., :32] * c - n[..., 32:] * s, n[..., :32] * s + n[..., 32:] * c], -1)
+    # Up to 2^40 / 2 pi turns with a relative error of 3 * 2^-53: 2^-14 turns.
+    mag = P.rotate_mag(n, 64, False)
+    _close("q", _np(y), ref, _tol(ref, mag, 64, "f32") + 2.0 ** -14 * 6.3 * mag)
+
+
+def test_in_place_on_a_fused_row(lib):
+    import torch
+    from selective_state_space_84_amd import binding
+    q, k, wq, wk, f, pos, _, _ = _make(5, 2, 33, 4, 2, 128, 64, "bf16")
+    want = binding.ssm_qk_norm_rope_fwd(q, k, wq, wk, f, positions=pos)
+    got = binding.ssm_qk_norm_rope_fwd(q, k, wq, wk, f, positions=pos, q_out=q, k_out=k)
+    assert got[0] is q and torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
+def test_repeat_stream_and_graph(lib):
+    import torch
+    from selective_state_space_84_amd import binding
+    q, k, wq, wk, f, pos, dq, dk = _make(6, 2, 800, 3, 1, 64, 64, "bf16")
+
+    def step(stream=None):
+        y = binding.ssm_qk_norm_rope_fwd(q, k, wq, wk, f, positions=pos, stream=stream)
+        g = binding.ssm_qk_norm_rope_bwd(q, k, wq, wk, f, dq_out=dq, dk_out=dk, positions=pos, stream=stream)
+        return [*y, g["dq"], g["dk"], g["dwq"], g["dwk"]]
+    want = step()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = step(s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for i in range(3):
+        dq.mul_(1.5)
+        want = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, outs)), i
+
+
+def test_empty(lib):
+    import torch
+    from selective_state_space_84_amd import binding
+    q, k, wq, wk, f, _, _, _ = _make(7, 2, 3, 2, 2, 64, 64, "f32")
+    g = binding.ssm_qk_norm_rope_bwd(q[:, :0], k[:, :0], wq, wk, f, dq_out=torch.zeros(2, 0, 2, 64, device=DEV),
+                                     dk_out=torch.zeros(2, 0, 2, 64, device=DEV))
+    assert not g["dwq"].any() and not g["dwk"].any()
+    y, _ = binding.ssm_qk_norm_rope_fwd(q[:, :0], k[:, :0], wq, wk, f)
+    assert y.shape == (2, 0, 2, 64)

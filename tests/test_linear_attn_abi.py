@@ -1,0 +1,189 @@
+"""Argument checks of the linear attention and norm-with-rotation entry points
+(nothing is launched): on the host, before any memory is touched."""
+import ctypes
+
+import pytest
+
+from selective_state_space_84_amd import binding as bd
+
+P0 = 0x7F0000000000
+MB = 1 << 20
+BAD = ctypes.c_size_t(-1).value
+
+
+def _fwd(lib, q=P0, k=P0 + MB, v=P0 + 2 * MB, g=P0 + 3 * MB, lens=None, h0=None, o=P0 + 4 * MB, hl=None, b=2, L=40, H=4,
+         M=2, dk=64, dv=128, qs=0, ks=0, vs=0, dtype=1, ws=None, wsb=0):
+    return lib.ssm_linear_attn_fwd(q, k, v, g, lens, h0, o, hl, b, L, H, M, dk, dv, qs, ks, vs, 0.125, dtype, ws, wsb,
+                                   None)
+
+
+def test_fwd_errors(lib):
+    for name in ("q", "k", "v", "g", "o"):
+        assert _fwd(lib, **{name: None}) == bd.SSM_ERR_NULL_ARG, name
+    assert _fwd(lib, b=-1) == bd.SSM_ERR_BAD_DIM
+    assert _fwd(lib, L=-1) == bd.SSM_ERR_BAD_DIM
+    assert _fwd(lib, M=0) == bd.SSM_ERR_BAD_DIM
+    assert _fwd(lib, H=(1 << 15) + 1, M=1) == bd.SSM_ERR_BAD_DIM
+    assert _fwd(lib, L=(1 << 31) - 100) == bd.SSM_ERR_BAD_DIM
+    assert _fwd(lib, b=1 << 40, L=1 << 20) == bd.SSM_ERR_BAD_DIM
+    assert _fwd(lib, qs=64) == bd.SSM_ERR_BAD_DIM
+    assert _fwd(lib, M=3) == bd.SSM_ERR_UNSUPPORTED
+    assert _fwd(lib, dk=32) == bd.SSM_ERR_UNSUPPORTED
+    assert _fwd(lib, dv=96) == bd.SSM_ERR_UNSUPPORTED
+    assert _fwd(lib, dtype=2) == bd.SSM_ERR_UNSUPPORTED
+    assert _fwd(lib, ks=2 * 64 + 4) == bd.SSM_ERR_MISALIGNED
+    for name, p in (("q", P0), ("k", P0 + MB), ("v", P0 + 2 * MB), ("o", P0 + 4 * MB), ("h0", P0 + 5 * MB),
+                    ("hl", P0 + 5 * MB)):
+        assert _fwd(lib, **{name: p + 8}) == bd.SSM_ERR_MISALIGNED, name
+    assert _fwd(lib, g=P0 + 3 * MB + 2) == bd.SSM_ERR_MISALIGNED
+    assert _fwd(lib, lens=P0 + 6 * MB + 2) == bd.SSM_ERR_MISALIGNED
+    assert _fwd(lib, o=P0 + 64) == bd.SSM_ERR_ALIAS
+    assert _fwd(lib, hl=P0 + 2 * MB) == bd.SSM_ERR_ALIAS
+    assert _fwd(lib, hl=P0 + 4 * MB + 64) == bd.SSM_ERR_ALIAS
+    assert _fwd(lib, h0=P0 + 5 * MB, hl=P0 + 5 * MB + 64) == bd.SSM_ERR_ALIAS
+    # An output between the rows of a strided input overlaps nothing; one that meets a row does.
+    wide = 4 * 64 + 2 * 64 + 2 * 128
+    assert _fwd(lib, q=P0, k=P0 + 512, v=P0 + 768, qs=wide, ks=wide, vs=wide, o=P0 + 1024) == bd.SSM_ERR_ALIAS
+
+
+def test_fwd_workspace(lib):
+    size = lib.ssm_linear_attn_fwd_workspace_size
+    assert size(2, 40, 4, 64, 128, 1) == 0
+    need = size(1, 8192, 4, 128, 128, 1)
+    assert need > 0 and need % (4 * 128 * 128 * 4) == 0
+    a = dict(b=1, L=8192, H=4, M=4, dk=128, dv=128, k=P0 + 64 * MB, v=P0 + 128 * MB, g=P0 + 192 * MB, o=P0 + 256 * MB)
+    assert _fwd(lib, **a) == bd.SSM_ERR_WORKSPACE
+    assert _fwd(lib, ws=P0 + 512 * MB, wsb=need - 1, **a) == bd.SSM_ERR_WORKSPACE
+    assert _fwd(lib, ws=P0 + 512 * MB + 64, wsb=need, **a) == bd.SSM_ERR_MISALIGNED
+    assert _fwd(lib, ws=P0 + 256 * MB, wsb=need, **a) == bd.SSM_ERR_ALIAS
+    assert _fwd(lib, ws=P0 + 512 * MB, wsb=need, h0=P0 + 512 * MB, **a) == bd.SSM_ERR_ALIAS
+    for bad in ((-1, 8, 4, 64, 64, 1), (1, 8, 4, 96, 64, 1), (1, 8, 4, 64, 64, 5), (1 << 40, 1 << 30, 4, 64, 64, 1)):
+        assert size(*bad) == BAD
+
+
+def test_fwd_empty(lib):
+    assert _fwd(lib, b=0, q=None, k=None, v=None, o=None) == bd.SSM_OK
+    assert _fwd(lib, H=0, q=None, k=None, v=None, o=None, g=None) == bd.SSM_OK
+
+
+def _bwd(lib, q=P0, k=P0 + MB, v=P0 + 2 * MB, g=P0 + 3 * MB, lens=None, h0=None, do=P0 + 4 * MB, dh=None, dq=P0 + 5 * MB,
+         dk_=P0 + 6 * MB, dv_=P0 + 7 * MB, dh0=None, b=2, L=40, H=4, M=4, dk=64, dv=128, dtype=1, ws=None, wsb=0):
+    return lib.ssm_linear_attn_bwd(q, k, v, g, lens, h0, do, dh, dq, dk_, dv_, dh0, b, L, H, M, dk, dv, 0, 0, 0, 0.125,
+                                   dtype, ws, wsb, None)
+
+
+def test_bwd_errors(lib):
+    for name in ("q", "k", "v", "g", "do", "dq", "dk_", "dv_"):
+        assert _bwd(lib, **{name: None}) == bd.SSM_ERR_NULL_ARG, name
+    assert _bwd(lib, dk=48) == bd.SSM_ERR_UNSUPPORTED
+    assert _bwd(lib, do=P0 + 4 * MB + 8) == bd.SSM_ERR_MISALIGNED
+    assert _bwd(lib, dh0=P0 + 8 * MB + 8) == bd.SSM_ERR_MISALIGNED
+    assert _bwd(lib, dq=P0) == bd.SSM_ERR_ALIAS
+    assert _bwd(lib, dv_=P0 + 6 * MB) == bd.SSM_ERR_ALIAS
+    assert _bwd(lib, dh=P0 + 8 * MB, dh0=P0 + 8 * MB) == bd.SSM_ERR_ALIAS
+    # Shared key/value heads need room for the per-head gradients.
+    size = lib.ssm_linear_attn_bwd_workspace_size
+    assert size(2, 40, 4, 4, 64, 128, 1) == 0
+    need = size(2, 40, 4, 2, 64, 128, 1)
+    assert need > 0
+    assert _bwd(lib, M=2) == bd.SSM_ERR_WORKSPACE
+    assert _bwd(lib, M=2, ws=P0 + 64 * MB, wsb=need - 4) == bd.SSM_ERR_WORKSPACE
+    assert size(2, 40, 4, 3, 64, 128, 1) == BAD
+    assert _bwd(lib, b=0) == bd.SSM_OK
+
+
+def _upd(lib, h=P0, slots=None, q=P0 + 16 * MB, k=P0 + 17 * MB, v=P0 + 18 * MB, g=P0 + 19 * MB, o=P0 + 20 * MB, b=4, n=4,
+         H=4, M=2, dk=64, dv=64, qs=0, ks=0, vs=0, dtype=1):
+    return lib.ssm_linear_attn_update(h, slots, q, k, v, g, o, b, n, H, M, dk, dv, qs, ks, vs, 0.125, dtype, None)
+
+
+def test_update_errors(lib):
+    for name in ("h", "q", "k", "v", "g", "o"):
+        assert _upd(lib, **{name: None}) == bd.SSM_ERR_NULL_ARG, name
+    assert _upd(lib, b=-1) == bd.SSM_ERR_BAD_DIM
+    assert _upd(lib, n=5) == bd.SSM_ERR_BAD_DIM  # without slots the states are the batch's
+    assert _upd(lib, n=1 << 31, slots=P0 + 30 * MB) == bd.SSM_ERR_BAD_DIM
+    assert _upd(lib, ks=64) == bd.SSM_ERR_BAD_DIM
+    assert _upd(lib, dv=256) == bd.SSM_ERR_UNSUPPORTED
+    assert _upd(lib, M=3) == bd.SSM_ERR_UNSUPPORTED
+    assert _upd(lib, dtype=9) == bd.SSM_ERR_UNSUPPORTED
+    assert _upd(lib, h=P0 + 4) == bd.SSM_ERR_MISALIGNED
+    assert _upd(lib, vs=132) == bd.SSM_ERR_MISALIGNED
+    assert _upd(lib, slots=P0 + 30 * MB + 1) == bd.SSM_ERR_MISALIGNED
+    assert _upd(lib, o=P0) == bd.SSM_ERR_ALIAS
+    assert _upd(lib, h=P0 + 16 * MB) == bd.SSM_ERR_ALIAS
+    assert _upd(lib, b=0, n=0) == bd.SSM_OK
+
+
+def _qk(lib, q=P0, k=P0 + MB, wq=None, wk=None, f=P0 + 2 * MB, pos=None, qo=P0 + 3 * MB, ko=P0 + 4 * MB, b=2, L=10, H=4,
+        M=2, D=64, R=64, qs=0, ks=0, qos=0, kos=0, eps=1e-6, inter=0, dtype=1):
+    return lib.ssm_qk_norm_rope_fwd(q, k, wq, wk, f, pos, qo, ko, b, L, H, M, D, R, qs, ks, qos, kos, eps, inter, dtype,
+                                    None)
+
+
+def test_qk_errors(lib):
+    for name in ("q", "k", "f", "qo", "ko"):
+        assert _qk(lib, **{name: None}) == bd.SSM_ERR_NULL_ARG, name
+    for a in (dict(b=-1), dict(M=-1), dict(L=1 << 31), dict(H=1 << 20), dict(qs=128), dict(kos=100), dict(b=1 << 40),
+              dict(b=1 << 16, L=1 << 16)):
+        assert _qk(lib, **a) == bd.SSM_ERR_BAD_DIM, a
+    for a in (dict(D=72), dict(D=272), dict(R=80), dict(R=24), dict(R=-16), dict(eps=-1.0), dict(eps=float("nan")),
+              dict(inter=2), dict(dtype=3)):
+        assert _qk(lib, **a) == bd.SSM_ERR_UNSUPPORTED, a
+    for a in (dict(q=P0 + 8), dict(ko=P0 + 4 * MB + 2), dict(wq=P0 + 5 * MB + 2), dict(pos=P0 + 6 * MB + 4),
+              dict(qs=260)):
+        assert _qk(lib, **a) == bd.SSM_ERR_MISALIGNED, a
+    # In place only exactly; not with another stride, not one output over the other input.
+    for a in (dict(qo=P0 + 16), dict(qo=P0, qos=512), dict(qo=P0 + MB), dict(ko=P0 + 3 * MB)):
+        assert _qk(lib, **a) == bd.SSM_ERR_ALIAS, a
+    # Column ranges of one buffer: k's rows begin inside q's.
+    assert _qk(lib, q=P0, k=P0 + 256, qs=384, ks=384, qo=P0, qos=384, ko=P0 + 256, kos=384) == bd.SSM_ERR_ALIAS
+    assert _qk(lib, b=0, q=None, k=None, qo=None, ko=None) == bd.SSM_OK
+    assert _qk(lib, H=0, M=0, q=None, k=None, qo=None, ko=None) == bd.SSM_OK
+
+
+def test_qk_bwd_errors(lib):
+    def bwd(dqo=P0 + 3 * MB, dko=P0 + 4 * MB, dq=P0 + 5 * MB, dk=P0 + 6 * MB, dwq=P0 + 7 * MB, dwk=None, ws=P0 + 8 * MB,
+            wsb=None, D=64, L=10):
+        if wsb is None:
+            wsb = lib.ssm_qk_norm_rope_bwd_workspace_size(2, L, 4, 2, 64)
+        return lib.ssm_qk_norm_rope_bwd(P0, P0 + MB, None, None, P0 + 2 * MB, None, dqo, dko, dq, dk, dwq, dwk, 2, L, 4, 2,
+                                        D, 64, 0, 0, 1e-6, 0, 1, ws, wsb, None)
+    for a in (dict(dqo=None), dict(dko=None), dict(dq=None), dict(dk=None)):
+        assert bwd(**a) == bd.SSM_ERR_NULL_ARG, a
+    assert bwd(D=24) == bd.SSM_ERR_UNSUPPORTED
+    assert bwd(dq=P0) == bd.SSM_ERR_ALIAS  # in place is for the forward call only
+    assert bwd(dq=P0 + 3 * MB) == bd.SSM_ERR_ALIAS
+    assert bwd(dwk=P0 + 7 * MB) == bd.SSM_ERR_ALIAS
+    assert bwd(ws=None) == bd.SSM_ERR_WORKSPACE
+    assert bwd(wsb=16) == bd.SSM_ERR_WORKSPACE
+    assert bwd(ws=P0 + 8 * MB + 16) == bd.SSM_ERR_MISALIGNED
+    assert bwd(ws=P0 + 5 * MB) == bd.SSM_ERR_ALIAS
+    assert lib.ssm_qk_norm_rope_bwd_workspace_size(2, 10, 4, 2, 24) == BAD
+    assert lib.ssm_qk_norm_rope_bwd_workspace_size(-2, 10, 4, 2, 64) == BAD
+
+
+def test_binding_refuses_rows_that_share_memory():
+    """An expanded axis (stride 0) or overlapping steps are not rows of a wider tensor."""
+    torch = pytest.importorskip("torch")
+
+    class Fake:  # only what the layout check reads
+        is_cuda = True
+
+        def __init__(self, t):
+            self.t = t
+
+        def __getattr__(self, n):
+            return getattr(self.t, n)
+    x = torch.zeros(2, 5, 4, 64)
+    assert bd._rows(Fake(x), "x")[1] == 256
+    wide = torch.zeros(2, 5, 6 * 64)[:, :, 64:64 + 256].unflatten(2, (4, 64))
+    assert bd._rows(Fake(wide), "x")[1] == 384
+    assert bd._rows(Fake(wide[:, :1]), "x")[1] == 5 * 384
+    for bad in (torch.zeros(1, 1, 4, 64).expand(2, 5, 4, 64), torch.zeros(2, 1, 4, 64).expand(2, 5, 4, 64),
+                x.transpose(1, 2).contiguous().transpose(1, 2), wide[:, :, ::2], wide[:, ::2], x[..., ::2],
+                torch.zeros(700).as_strided((2, 3, 4, 16), (192, 32, 16, 1))):
+        with pytest.raises(ValueError):
+            bd._rows(Fake(bad), "x")
+    with pytest.raises(ValueError):
+        bd.ssm_linear_attn_fwd(x, x, x, torch.zeros(4))  # on the CPU
