@@ -422,8 +422,8 @@ int ssm_conv1d_update(float* state, const void* x_t, const float* w, const float
  *                apart) are q_stride, k_stride, v_stride elements apart, so
  *                that q, k and v may be column ranges of one projection's
  *                output; 0 stands for the dense nheads * d_k and so on.  All
- *                three 16-byte aligned, strides multiples of 16 bytes and not
- *                below the dense ones.
+ *                three 16-byte aligned, strides multiples of 16 bytes, not
+ *                below the dense ones and at most 2^23 elements.
  *   log_decay  : [nheads] fp32, log(gamma); 0 keeps everything, -inf keeps
  *                only the current step.  A constant of the layer: it has no
  *                gradient.  Positive values grow the state without bound.

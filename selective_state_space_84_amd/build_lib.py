@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libssm_scan.so")
 SOURCES = ["scan_mode0.hip", "scan_mode1.hip", "scan_mode2.hip", "scan_mode3.hip", "scan_mode4.hip", "scan_mode5.hip",
            "scan_mode6.hip", "scan_mode7.hip", "scan_aux.hip",
            "update_kernel.hip", "conv_kernels.hip", "scan_bwd.hip", "ssd_kernel.hip", "linear_attn.hip",
-           "linear_attn_update.hip", "qk_norm_rope.hip", "abi.hip"]
+           "linear_attn_bf16.hip", "linear_attn_update.hip", "qk_norm_rope.hip", "abi.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # Packed fp32 VALU forms are kept out of the generated code.

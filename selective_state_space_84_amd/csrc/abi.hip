@@ -579,10 +579,13 @@ int check_alias(const Rows* outs, int n_out, const Rows* ins, int n_in) {
   return SSM_OK;
 }
 
+// A block of 64 rows is addressed with 32-bit byte offsets.
+constexpr int64_t kMaxStride = (int64_t)1 << 23;
+
 // The row stride (0: dense) of `width` elements, and the extent it gives.
 int check_stride(int64_t* stride, int64_t width, int64_t rows, int64_t es) {
   if (*stride == 0) *stride = width;
-  if (*stride < width) return SSM_ERR_BAD_DIM;
+  if (*stride < width || *stride > kMaxStride) return SSM_ERR_BAD_DIM;
   int64_t n;
   if (__builtin_mul_overflow(rows, *stride, &n) || n > INT64_MAX / 16) return SSM_ERR_BAD_DIM;
   if ((*stride * es) % 16 != 0) return SSM_ERR_MISALIGNED;

@@ -47,10 +47,15 @@ struct AttnSweep {
   void* out;               // [batch][seqlen][nheads][VD]
   int64_t sn, sp;          // state element (n, p) at n sn + p sp
   int64_t seqlen, span_len, n_spans;
-  int32_t nheads, slices;  // slices of the VD columns, one workgroup each
+  int32_t nheads, slices;  // slices of the VD columns, one workgroup each (fp32 sweep)
   int64_t rows;            // batch * nheads
   float s_pair, s_read, s_write;
 };
+
+// The sweep for bf16 operands (linear_attn_bf16.hip).  sum: only the spans'
+// states; out32: fp32 outputs.
+hipError_t launch_attn_sweep_bf16(const AttnSweep& s, int64_t kd, int64_t vd, bool rev, bool sum, bool out32,
+                                  hipStream_t stream);
 
 // log2(gamma); -inf is kept finite so that 0 steps of decay give 1 (0 * -inf
 // would be NaN) and one step or more still gives 0.

@@ -28,17 +28,7 @@ constexpr int kCols = 64;     // output columns per workgroup
 constexpr int kSc = kCols + 4;  // LDS row strides (floats) with rows 4 apart on different banks
 constexpr int kSp = kT + 4;
 
-template <typename T>
-__device__ __forceinline__ f32x4 load4(const T* p);
-template <>
-__device__ __forceinline__ f32x4 load4<float>(const float* p) {
-  return *reinterpret_cast<const f32x4*>(p);
-}
-template <>
-__device__ __forceinline__ f32x4 load4<uint16_t>(const uint16_t* p) {
-  const u16x4 v = *reinterpret_cast<const u16x4*>(p);
-  return f32x4{io_to_f32(v[0]), io_to_f32(v[1]), io_to_f32(v[2]), io_to_f32(v[3])};
-}
+__device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
 __device__ __forceinline__ void store4(float* p, const f32x4& v) { *reinterpret_cast<f32x4*>(p) = v; }
 __device__ __forceinline__ void store4(uint16_t* p, const f32x4& v) {
   u16x4 r;
@@ -48,7 +38,7 @@ __device__ __forceinline__ void store4(uint16_t* p, const f32x4& v) {
 }
 
 // SUM: only the state of the span from a zero entry (a and out unused).
-template <typename T, typename O, int KD, bool REV, bool SUM>
+template <int KD, bool REV, bool SUM>
 __global__ void __launch_bounds__(256) k_attn_sweep_f32(const AttnSweep s) {
   constexpr int kSa = KD + 4;
   constexpr int NT = KD / 16;          // state tiles
@@ -76,10 +66,10 @@ __global__ void __launch_bounds__(256) k_attn_sweep_f32(const AttnSweep s) {
   const int64_t e = min(s1, len) > s0 ? min(s1, len) : s0;  // steps [s0, e) are computed
   const float g = decay_log2(s.log_decay[h]);
 
-  const T* const A = SUM ? nullptr : static_cast<const T*>(s.a.p) + b * s.seqlen * s.a.stride + (h / s.a.rep) * KD;
-  const T* const B = static_cast<const T*>(s.b.p) + b * s.seqlen * s.b.stride + (h / s.b.rep) * KD;
-  const T* const C = static_cast<const T*>(s.c.p) + b * s.seqlen * s.c.stride + (h / s.c.rep) * VD + col0;
-  O* const out = SUM ? nullptr : static_cast<O*>(s.out) + (b * s.seqlen * s.nheads + h) * VD + col0;
+  const float* const A = SUM ? nullptr : static_cast<const float*>(s.a.p) + b * s.seqlen * s.a.stride + (h / s.a.rep) * KD;
+  const float* const B = static_cast<const float*>(s.b.p) + b * s.seqlen * s.b.stride + (h / s.b.rep) * KD;
+  const float* const C = static_cast<const float*>(s.c.p) + b * s.seqlen * s.c.stride + (h / s.c.rep) * VD + col0;
+  float* const out = SUM ? nullptr : static_cast<float*>(s.out) + (b * s.seqlen * s.nheads + h) * VD + col0;
 
   // State S[n][p], p = 16 w + r16 of the slice: acc[nt][j] = S[16 nt + 4 q4 + j][p].
   f32x4 acc[NT];
@@ -100,13 +90,13 @@ __global__ void __launch_bounds__(256) k_attn_sweep_f32(const AttnSweep s) {
     for (int r = 0; r < PA; ++r) {
       const int piece = tid + 256 * r, t = piece / (KD / 4), n = piece % (KD / 4) * 4;
       const f32x4 z = {0.f, 0.f, 0.f, 0.f};
-      if (!SUM) ra[r] = t < m ? load4<T>(A + (t0 + t) * s.a.stride + n) : z;
-      rb[r] = t < m ? load4<T>(B + (t0 + t) * s.b.stride + n) : z;
+      if (!SUM) ra[r] = t < m ? load4(A + (t0 + t) * s.a.stride + n) : z;
+      rb[r] = t < m ? load4(B + (t0 + t) * s.b.stride + n) : z;
     }
 #pragma unroll
     for (int r = 0; r < PC; ++r) {
       const int piece = tid + 256 * r, t = piece / (kCols / 4), p = piece % (kCols / 4) * 4;
-      rc[r] = t < m ? load4<T>(C + (t0 + t) * s.c.stride + p) : f32x4{0.f, 0.f, 0.f, 0.f};
+      rc[r] = t < m ? load4(C + (t0 + t) * s.c.stride + p) : f32x4{0.f, 0.f, 0.f, 0.f};
     }
   };
 
@@ -271,20 +261,14 @@ __global__ void __launch_bounds__(256) k_attn_sum_heads(const float* part, T* ou
 
 int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
 
-template <typename T, typename O, bool REV, bool SUM>
-hipError_t sweep_f32(const AttnSweep& s, int64_t kd, hipStream_t stream) {
-  const unsigned grid = (unsigned)(s.rows * s.n_spans * s.slices);
-  if (kd == 64) return launch(k_attn_sweep_f32<T, O, 64, REV, SUM>, dim3(grid), dim3(256), 0, stream, s);
-  return launch(k_attn_sweep_f32<T, O, 128, REV, SUM>, dim3(grid), dim3(256), 0, stream, s);
-}
-
 // out32: the outputs go to an fp32 buffer although the inputs are bf16.
 template <bool REV, bool SUM>
 hipError_t sweep(AttnSweep s, int64_t kd, int64_t vd, bool bf16, bool out32, hipStream_t stream) {
+  if (bf16) return launch_attn_sweep_bf16(s, kd, vd, REV, SUM, out32, stream);
   s.slices = (int32_t)(vd / kCols);
-  if (!bf16) return sweep_f32<float, float, REV, SUM>(s, kd, stream);
-  if (out32 || SUM) return sweep_f32<uint16_t, float, REV, SUM>(s, kd, stream);
-  return sweep_f32<uint16_t, uint16_t, REV, SUM>(s, kd, stream);
+  const unsigned grid = (unsigned)(s.rows * s.n_spans * s.slices);
+  if (kd == 64) return launch(k_attn_sweep_f32<64, REV, SUM>, dim3(grid), dim3(256), 0, stream, s);
+  return launch(k_attn_sweep_f32<128, REV, SUM>, dim3(grid), dim3(256), 0, stream, s);
 }
 
 template <bool REV>
@@ -311,19 +295,19 @@ AttnSweep base(const LinAttnLaunch& p, const LinAttnPlan& pl) {
 
 // Workgroups a launch should have: below, the sequence is cut into spans of at
 // least kMinSpan steps, at the price of reading b and c twice.
-constexpr int64_t kTargetGroups = 1024;
-constexpr int64_t kMinSpan = 128;
+constexpr int64_t kTargetGroups = 512;
+constexpr int64_t kMinSpan = 256;
+constexpr int64_t kSpanStep = 64;  // spans start on block boundaries of both sweeps
 
 LinAttnPlan linear_attn_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16) {
-  (void)bf16;
-  const int64_t groups = batch * nheads * ((d_k > d_v ? d_k : d_v) / kCols);
+  const int64_t groups = batch * nheads * (bf16 ? 1 : (d_k > d_v ? d_k : d_v) / kCols);
   int64_t n = 1;
-  if (groups > 0 && groups < kTargetGroups / 2) n = kTargetGroups / groups;
+  if (groups > 0 && groups < kTargetGroups) n = kTargetGroups / groups;
   if (n > seqlen / kMinSpan) n = seqlen / kMinSpan;
   if (n < 1) n = 1;
   int64_t len = (seqlen + n - 1) / n;
-  len = (len + kT - 1) / kT * kT;
-  if (len < kT) len = kT;
+  len = (len + kSpanStep - 1) / kSpanStep * kSpanStep;
+  if (len < kSpanStep) len = kSpanStep;
   return LinAttnPlan{len, seqlen > 0 ? (seqlen + len - 1) / len : 1};
 }
 

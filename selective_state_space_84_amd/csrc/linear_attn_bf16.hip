@@ -1,0 +1,358 @@
+// The linear attention sweep for bf16 operands, on the bf16 matrix
+// instructions (roles, formulas and the state's recurrence: linear_attn.h).
+//
+// One workgroup (4 waves) per (row, head) and span; wave w owns R = VD / 4 of the
+// VD output columns, for the outputs and for the state S[n][p], which stays in
+// fp32 accumulators.  Per block of 64 steps:
+//   pairs   P[t][i] = decay (a_t . b_i), shared between the waves through LDS
+//   read    out^T = (S^T A^T) diag(s_read decay)      then the state moves on:
+//   update  S = gamma^m S + B^T (w o C)
+//   join    out^T += C^T P^T
+// on R x R tiles (v_mfma_f32_32x32x16_bf16 for VD = 128, 16x16x32 for 64).
+//
+// Precision.  a, b and c meet the matrix cores exactly.  What is formed in
+// between is split: P and the state of `read` into two bf16 values (about 16
+// significant bits, so that the rounding of a bf16 output stays the largest
+// error), w o C into three (24 bits: the state keeps fp32's precision over any
+// number of blocks, since each block adds to it at that precision).
+//
+// Mapping.
+//   * The accumulators' layout (lane = column p, four rows n per register
+//     quad) is the A operand of S^T A^T when the contraction takes n in the
+//     order the registers hold it; a is read from its rows in the same order
+//     (two 8-byte reads), so the state never moves.
+//   * c is needed with the steps along the contraction for both join and
+//     update: ds_read_b64_tr_b16 transposes this wave's columns once per block.
+//     b^T for the update comes out of b's rows the same way.
+//   * read and update do not need P: they run between the writing of P and the
+//     barrier that completes it, so the barrier finds the waves together.  After
+//     it only P and registers are read, so the next block's rows are staged
+//     without another barrier: two barriers a block.
+//   * The next block's rows are requested into registers right after the first
+//     barrier and are on their way during the whole block.
+#include "linear_attn.h"
+
+namespace ssm {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int kQ = 64;  // steps per block
+
+// R x R result tile: A holds row lane % R, B column lane % R, both 8 contraction
+// positions 8 (lane / R) + j; register f of the result is row
+// (256 / R) (f / 4) + 4 (lane / R) + f % 4 of column lane % R.
+template <int R>
+struct Tile;
+template <>
+struct Tile<32> {
+  typedef f32x16 acc;
+  static __device__ __forceinline__ acc mma(u32x4 a, u32x4 b, acc c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                    0, 0);
+  }
+};
+template <>
+struct Tile<16> {
+  typedef f32x4 acc;
+  static __device__ __forceinline__ acc mma(u32x4 a, u32x4 b, acc c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                    0, 0);
+  }
+};
+
+__device__ __forceinline__ uint32_t pack(float v0, float v1) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v0, v1}, bf16x2));
+}
+__device__ __forceinline__ float lo_f32(uint32_t v) { return __builtin_bit_cast(float, v << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t v) { return __builtin_bit_cast(float, v & 0xffff0000u); }
+// A pair of values as a sum of bf16 pairs: takes the leading one off v0, v1.
+__device__ __forceinline__ uint32_t peel(float& v0, float& v1) {
+  const uint32_t p = pack(v0, v1);
+  v0 -= lo_f32(p);
+  v1 -= hi_f32(p);
+  return p;
+}
+
+__device__ __forceinline__ u32x2 lds_tr4(const uint16_t* p) {
+  return __builtin_bit_cast(u32x2,
+                            __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(s16x4*)const_cast<uint16_t*>(p)));
+}
+__device__ __forceinline__ u32x4 cat(u32x2 a, u32x2 b) { return u32x4{a[0], a[1], b[0], b[1]}; }
+__device__ __forceinline__ u32x4 lds16(const uint16_t* p) { return *reinterpret_cast<const u32x4*>(p); }
+
+__device__ __forceinline__ void put4(uint16_t* p, float a, float b, float c, float d) {
+  *reinterpret_cast<u32x2*>(p) = u32x2{pack(a, b), pack(c, d)};
+}
+__device__ __forceinline__ void put4(float* p, float a, float b, float c, float d) {
+  *reinterpret_cast<f32x4*>(p) = f32x4{a, b, c, d};
+}
+
+// Rows of one operand on their way from memory to LDS: 16-byte pieces, 256
+// threads, W columns.
+template <int W, int S>  // S: LDS row stride
+struct Stage {
+  static constexpr int kPerRow = W / 8, kRows = 256 / kPerRow, N = kQ / kRows;
+  u32x4 r[N];
+  __device__ __forceinline__ void load(const uint16_t* base, int64_t stride, int m) {
+    const int t = threadIdx.x / kPerRow, c = threadIdx.x % kPerRow * 8;
+    const uint32_t off = (uint32_t)t * ((uint32_t)stride * 2) + c * 2;
+    const gchar* p = uniform_ptr(base);
+    if (m == kQ) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) r[k] = gldr<u32x4>(p + (int64_t)k * kRows * stride * 2, off);
+    } else {  // steps behind the end are zero
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        r[k] = u32x4{0, 0, 0, 0};
+        if (t + k * kRows < m) r[k] = gldr<u32x4>(p + (int64_t)k * kRows * stride * 2, off);
+      }
+    }
+  }
+  __device__ __forceinline__ void put(uint16_t* lds) const {
+    const int t = threadIdx.x / kPerRow, c = threadIdx.x % kPerRow * 8;
+#pragma unroll
+    for (int k = 0; k < N; ++k) *reinterpret_cast<u32x4*>(&lds[(t + k * kRows) * S + c]) = r[k];
+  }
+};
+
+// SUM: only the state of the span from a zero entry (a and out unused).
+template <typename O, int KD, int R, bool REV, bool SUM>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
+k_attn_sweep_bf16(const AttnSweep s) {
+  constexpr int VD = 4 * R;
+  constexpr int NG = 64 / R;       // lane groups
+  constexpr int KC = 8 * NG;       // contraction of one instruction
+  constexpr int AR = R * R / 64;   // accumulator registers of a tile
+  constexpr int NS = KD * R / 64;  // state registers
+  constexpr int TT = kQ / R;       // tiles of steps
+  constexpr int KT = kQ / KC;      // contraction slices over the steps
+  // LDS row strides: rows read along the contraction 4 (mod 64) dwords apart,
+  // rows read through the transpose 8 apart.
+  constexpr int SA = KD + 8, SB = KD + 16, SC = VD + 16, SP = kQ + 8;
+  typedef Tile<R> M;
+  typedef typename M::acc Acc;
+  __shared__ __align__(16) uint16_t sA[SUM ? 8 : kQ * SA];
+  __shared__ __align__(16) uint16_t sB[kQ * SB];
+  __shared__ __align__(16) uint16_t sC[kQ * SC];
+  __shared__ __align__(16) uint16_t sP[2][SUM ? 8 : kQ * SP];  // pairs [t][i], leading and second part
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane % R, g = lane / R;
+  const int r16 = lane & 15, q4 = lane >> 4;
+  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
+  const int64_t row = id % s.rows, span = id / s.rows;
+  const int64_t b = row / s.nheads;
+  const int h = (int)(row % s.nheads);
+  const int64_t len = row_length(s.lengths, b, s.seqlen);
+  const int64_t s0 = span * s.span_len;
+  const int64_t s1 = min(s0 + s.span_len, s.seqlen);
+  const int64_t e = min(s1, len) > s0 ? min(s1, len) : s0;  // steps [s0, e) are computed
+  const float gl = decay_log2(s.log_decay[h]);
+
+  const uint16_t* const A =
+      SUM ? nullptr : static_cast<const uint16_t*>(s.a.p) + b * s.seqlen * s.a.stride + (h / s.a.rep) * KD;
+  const uint16_t* const B = static_cast<const uint16_t*>(s.b.p) + b * s.seqlen * s.b.stride + (h / s.b.rep) * KD;
+  const uint16_t* const C = static_cast<const uint16_t*>(s.c.p) + b * s.seqlen * s.c.stride + (h / s.c.rep) * VD;
+  O* const out = SUM ? nullptr : static_cast<O*>(s.out) + (b * s.seqlen * s.nheads + h) * VD;
+
+  // State register f: S[4 NG (f / 4) + 4 g + f % 4][R w + r].
+  Acc st[NS / AR];
+  const int64_t soff = (int64_t)(R * w + r) * s.sp;
+  {
+    const float* ep = nullptr;
+    if (!SUM && s.entry != nullptr) ep = s.entry + ((s.n_spans > 1 ? span * s.rows : 0) + row) * KD * VD + soff;
+#pragma unroll
+    for (int f = 0; f < NS; ++f)
+      st[f / AR][f % AR] = ep != nullptr ? ep[(4 * NG * (f / 4) + 4 * g + f % 4) * s.sn] : 0.f;
+  }
+
+  // The masked 16 x 16 tiles of P inside the tiles that join reads are never
+  // written: zero once.
+  if (!SUM && tid < 128) {
+    const int t = (REV ? 16 : 0) + 32 * (tid >> 6) + (lane >> 2), i = (REV ? 0 : 16) + 32 * (tid >> 6) + 4 * (lane & 3);
+    *reinterpret_cast<u32x2*>(&sP[0][t * SP + i]) = u32x2{0, 0};
+    *reinterpret_cast<u32x2*>(&sP[1][t * SP + i]) = u32x2{0, 0};
+  }
+
+  Stage<KD, SA> ga;
+  Stage<KD, SB> gb;
+  Stage<VD, SC> gc;
+  const int64_t nblk = (e - s0 + kQ - 1) / kQ;
+  auto fetch = [&](int64_t k) {
+    const int64_t t0 = s0 + (REV ? nblk - 1 - k : k) * kQ;
+    const int m = (int)min((int64_t)kQ, e - t0);
+    if (!SUM) ga.load(A + t0 * s.a.stride, s.a.stride, m);
+    gb.load(B + t0 * s.b.stride, s.b.stride, m);
+    gc.load(C + t0 * s.c.stride, s.c.stride, m);
+  };
+  if (nblk > 0) fetch(0);
+  for (int64_t k = 0; k < nblk; ++k) {
+    const int64_t t0 = s0 + (REV ? nblk - 1 - k : k) * kQ;
+    const int m = (int)min((int64_t)kQ, e - t0);
+    if (!SUM) ga.put(sA);
+    gb.put(sB);
+    gc.put(sC);
+    __syncthreads();
+    if (k + 1 < nblk) fetch(k + 1);
+
+    Acc o[SUM ? 1 : TT];
+    if (!SUM) {
+      // pairs: wave w has the steps t of tile w, tiles it of i up to (from) it:
+      // S^T = B A^T, decayed and split.
+      u32x4 av[KD / 32];
+#pragma unroll
+      for (int kk = 0; kk < KD / 32; ++kk) av[kk] = lds16(&sA[(16 * w + r16) * SA + 32 * kk + 8 * q4]);
+      for (int it = REV ? w : 0; it < (REV ? 4 : w + 1); ++it) {
+        f32x4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kk = 0; kk < KD / 32; ++kk)
+          p = Tile<16>::mma(lds16(&sB[(16 * it + r16) * SB + 32 * kk + 8 * q4]), av[kk], p);
+        const int d0 = (16 * w + r16 - (16 * it + 4 * q4)) * (REV ? -1 : 1);  // steps between t and i, j = 0
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int d = REV ? d0 + j : d0 - j;
+          v[j] = d >= 0 ? p[j] * (hw_exp2(gl * (float)d) * s.s_pair) : 0.f;
+        }
+        const int at = (16 * w + r16) * SP + 16 * it + 4 * q4;
+        const uint32_t h0 = peel(v[0], v[1]), h1 = peel(v[2], v[3]);
+        *reinterpret_cast<u32x2*>(&sP[0][at]) = u32x2{h0, h1};
+        *reinterpret_cast<u32x2*>(&sP[1][at]) = u32x2{pack(v[0], v[1]), pack(v[2], v[3])};
+      }
+
+      // read
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+        for (int j = 0; j < AR; ++j) o[tt][j] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KD / KC; ++ks) {
+        u32x4 hi, lo;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int f = 8 * ks + 2 * q;
+          float v0 = st[f / AR][f % AR], v1 = st[(f + 1) / AR][(f + 1) % AR];
+          hi[q] = peel(v0, v1);
+          lo[q] = pack(v0, v1);
+        }
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) {
+          const uint16_t* p = &sA[(R * tt + r) * SA + KC * ks + 4 * g];
+          const u32x4 a = cat(*reinterpret_cast<const u32x2*>(p), *reinterpret_cast<const u32x2*>(p + 4 * NG));
+          o[tt] = M::mma(hi, a, o[tt]);
+          o[tt] = M::mma(lo, a, o[tt]);
+        }
+      }
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) {
+        const int t = R * tt + r;
+        // Behind the end (t >= m) the exponent is clamped: those columns are not stored.
+        const float rf = hw_exp2(gl * (float)(REV ? max(m - 1 - t, 0) : t + 1)) * s.s_read;
+        o[tt] *= rf;
+      }
+    }
+
+    // This wave's columns of c, steps along the contraction: lane (r, g) of slice
+    // kt holds c[KC kt + 8 g + j][R w + r].
+    u32x4 cv[KT];
+    {
+      const int sub = lane & 15;
+      const uint16_t* p = &sC[(8 * g + (sub >> 2)) * SC + R * w + (r & 16) + 4 * (sub & 3)];
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) cv[kt] = cat(lds_tr4(p + KC * kt * SC), lds_tr4(p + (KC * kt + 4) * SC));
+    }
+
+    // update
+    const float fac = hw_exp2(gl * (float)m);
+#pragma unroll
+    for (int i = 0; i < NS / AR; ++i) st[i] *= fac;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+      u32x4 w0, w1, w2;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = KC * kt + 8 * g + 2 * q;
+        // c is zero behind the end; the exponent is clamped to keep its weight finite.
+        float v0 = lo_f32(cv[kt][q]) * (hw_exp2(gl * (float)(REV ? i + 1 : max(m - 1 - i, 0))) * s.s_write);
+        float v1 = hi_f32(cv[kt][q]) * (hw_exp2(gl * (float)(REV ? i + 2 : max(m - 2 - i, 0))) * s.s_write);
+        w0[q] = peel(v0, v1);
+        w1[q] = peel(v0, v1);
+        w2[q] = pack(v0, v1);
+      }
+      const int sub = lane & 15;
+      const uint16_t* p = &sB[(KC * kt + 8 * g + (sub >> 2)) * SB + (r & 16) + 4 * (sub & 3)];
+#pragma unroll
+      for (int nt = 0; nt < KD / R; ++nt) {
+        const u32x4 bv = cat(lds_tr4(p + R * nt), lds_tr4(p + 4 * SB + R * nt));
+        st[nt] = M::mma(bv, w0, st[nt]);
+        st[nt] = M::mma(bv, w1, st[nt]);
+        st[nt] = M::mma(bv, w2, st[nt]);
+      }
+    }
+    __syncthreads();  // P complete; a, b and c no longer read
+
+    if (!SUM) {
+      // join, and out.
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) {
+        const uint16_t* p = &sP[0][(R * tt + r) * SP + 8 * g];
+        const int first = REV ? R * tt / KC : 0, last = REV ? KT : (R * tt + R + KC - 1) / KC;
+#pragma unroll
+        for (int kt = first; kt < last; ++kt) {
+          o[tt] = M::mma(cv[kt], lds16(p + KC * kt), o[tt]);
+          o[tt] = M::mma(cv[kt], lds16(p + kQ * SP + KC * kt), o[tt]);
+        }
+        if (R * tt + r < m) {
+          O* op = out + (t0 + R * tt + r) * s.nheads * VD + R * w + 4 * g;
+#pragma unroll
+          for (int q = 0; q < AR / 4; ++q)
+            put4(op + 4 * NG * q, o[tt][4 * q], o[tt][4 * q + 1], o[tt][4 * q + 2], o[tt][4 * q + 3]);
+        }
+      }
+    }
+  }
+
+  if (!SUM) {
+    // Rows behind the sequence's end.
+    for (int64_t t = e + tid / (VD / 4); t < s1; t += 256 / (VD / 4))
+      put4(out + t * s.nheads * VD + 4 * (tid % (VD / 4)), 0.f, 0.f, 0.f, 0.f);
+  }
+  if (s.exit != nullptr && (SUM || span == (REV ? 0 : s.n_spans - 1))) {
+    float* xp = s.exit + ((SUM ? span * s.rows : 0) + row) * KD * VD + soff;
+#pragma unroll
+    for (int f = 0; f < NS; ++f) xp[(4 * NG * (f / 4) + 4 * g + f % 4) * s.sn] = st[f / AR][f % AR];
+  }
+}
+
+template <typename O, bool REV, bool SUM>
+hipError_t by_width(const AttnSweep& s, int64_t kd, int64_t vd, hipStream_t stream) {
+  const unsigned grid = (unsigned)(s.rows * s.n_spans);
+  auto go = [&](auto kern) { return launch(kern, dim3(grid), dim3(256), 0, stream, s); };
+  if (kd == 64) return vd == 64 ? go(k_attn_sweep_bf16<O, 64, 16, REV, SUM>) : go(k_attn_sweep_bf16<O, 64, 32, REV, SUM>);
+  return vd == 64 ? go(k_attn_sweep_bf16<O, 128, 16, REV, SUM>) : go(k_attn_sweep_bf16<O, 128, 32, REV, SUM>);
+}
+
+}  // namespace
+
+hipError_t launch_attn_sweep_bf16(const AttnSweep& s, int64_t kd, int64_t vd, bool rev, bool sum, bool out32,
+                                  hipStream_t stream) {
+  if (sum)
+    return rev ? by_width<float, true, true>(s, kd, vd, stream) : by_width<float, false, true>(s, kd, vd, stream);
+  if (out32)
+    return rev ? by_width<float, true, false>(s, kd, vd, stream) : by_width<float, false, false>(s, kd, vd, stream);
+  return rev ? by_width<uint16_t, true, false>(s, kd, vd, stream)
+             : by_width<uint16_t, false, false>(s, kd, vd, stream);
+}
+
+}  // namespace ssm

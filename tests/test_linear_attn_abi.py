@@ -27,6 +27,7 @@ def test_fwd_errors(lib):
     assert _fwd(lib, L=(1 << 31) - 100) == bd.SSM_ERR_BAD_DIM
     assert _fwd(lib, b=1 << 40, L=1 << 20) == bd.SSM_ERR_BAD_DIM
     assert _fwd(lib, qs=64) == bd.SSM_ERR_BAD_DIM
+    assert _fwd(lib, vs=(1 << 23) + 8) == bd.SSM_ERR_BAD_DIM
     assert _fwd(lib, M=3) == bd.SSM_ERR_UNSUPPORTED
     assert _fwd(lib, dk=32) == bd.SSM_ERR_UNSUPPORTED
     assert _fwd(lib, dv=96) == bd.SSM_ERR_UNSUPPORTED
@@ -124,7 +125,7 @@ def _qk(lib, q=P0, k=P0 + MB, wq=None, wk=None, f=P0 + 2 * MB, pos=None, qo=P0 +
 def test_qk_errors(lib):
     for name in ("q", "k", "f", "qo", "ko"):
         assert _qk(lib, **{name: None}) == bd.SSM_ERR_NULL_ARG, name
-    for a in (dict(b=-1), dict(M=-1), dict(L=1 << 31), dict(H=1 << 20), dict(qs=128), dict(kos=100), dict(b=1 << 40),
+    for a in (dict(b=-1), dict(M=-1), dict(L=1 << 31), dict(H=1 << 20), dict(qs=128), dict(qs=(1 << 23) + 8), dict(kos=100), dict(b=1 << 40),
               dict(b=1 << 16, L=1 << 16)):
         assert _qk(lib, **a) == bd.SSM_ERR_BAD_DIM, a
     for a in (dict(D=72), dict(D=272), dict(R=80), dict(R=24), dict(R=-16), dict(eps=-1.0), dict(eps=float("nan")),
