@@ -83,6 +83,10 @@ __device__ __forceinline__ uint32_t peel(float& v0, float& v1) {
   return p;
 }
 
+__device__ __forceinline__ float uniform_f32(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
+}
+
 __device__ __forceinline__ u32x2 lds_tr4(const uint16_t* p) {
   return __builtin_bit_cast(u32x2,
                             __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(s16x4*)const_cast<uint16_t*>(p)));
@@ -90,36 +94,41 @@ __device__ __forceinline__ u32x2 lds_tr4(const uint16_t* p) {
 __device__ __forceinline__ u32x4 cat(u32x2 a, u32x2 b) { return u32x4{a[0], a[1], b[0], b[1]}; }
 __device__ __forceinline__ u32x4 lds16(const uint16_t* p) { return *reinterpret_cast<const u32x4*>(p); }
 
-__device__ __forceinline__ void put4(uint16_t* p, float a, float b, float c, float d) {
-  *reinterpret_cast<u32x2*>(p) = u32x2{pack(a, b), pack(c, d)};
-}
-__device__ __forceinline__ void put4(float* p, float a, float b, float c, float d) {
-  *reinterpret_cast<f32x4*>(p) = f32x4{a, b, c, d};
+template <typename O>
+__device__ __forceinline__ void put4(gchar* base, uint32_t off, float a, float b, float c, float d) {
+  if constexpr (sizeof(O) == 2) {
+    gstr<u32x2>(base, off, u32x2{pack(a, b), pack(c, d)});
+  } else {
+    gstr<f32x4>(base, off, f32x4{a, b, c, d});
+  }
 }
 
 // Rows of one operand on their way from memory to LDS: 16-byte pieces, 256
-// threads, W columns.
-template <int W, int S>  // S: LDS row stride
+// threads, W columns, LDS row stride S.  Rows outside [lo, hi) are zero: the
+// loads take the nearest row inside instead (no branch, so that nothing waits
+// for a load before the rows are put).
+template <int W, int S>
 struct Stage {
   static constexpr int kPerRow = W / 8, kRows = 256 / kPerRow, N = kQ / kRows;
   u32x4 r[N];
-  __device__ __forceinline__ void load(const uint16_t* base, int64_t stride, int m) {
-    const int t = threadIdx.x / kPerRow, c = threadIdx.x % kPerRow * 8;
-    const uint32_t off = (uint32_t)t * ((uint32_t)stride * 2) + c * 2;
+  __device__ __forceinline__ void load(const uint16_t* base, int64_t stride, int lo, int hi) {
+    const uint32_t sb = (uint32_t)stride * 2;
+    const uint32_t first = (uint32_t)lo * sb, last = (uint32_t)(hi - 1) * sb;
+    uint32_t row = threadIdx.x / kPerRow * sb;
+    asm volatile("" : "+v"(row));  // keeps the clamped offsets from being held in registers between blocks
+    const uint32_t c = threadIdx.x % kPerRow * 16;
     const gchar* p = uniform_ptr(base);
-    if (m == kQ) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) r[k] = gldr<u32x4>(p + (int64_t)k * kRows * stride * 2, off);
-    } else {  // steps behind the end are zero
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        r[k] = u32x4{0, 0, 0, 0};
-        if (t + k * kRows < m) r[k] = gldr<u32x4>(p + (int64_t)k * kRows * stride * 2, off);
-      }
-    }
+    for (int k = 0; k < N; ++k)
+      r[k] = gldr<u32x4>(p, max(min(row + (uint32_t)(k * kRows) * sb, last), first) + c);
   }
-  __device__ __forceinline__ void put(uint16_t* lds) const {
+  __device__ __forceinline__ void put(uint16_t* lds, int lo, int hi) {
     const int t = threadIdx.x / kPerRow, c = threadIdx.x % kPerRow * 8;
+    if (hi - lo != kQ) {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (t + k * kRows < lo || t + k * kRows >= hi) r[k] = u32x4{0, 0, 0, 0};
+    }
 #pragma unroll
     for (int k = 0; k < N; ++k) *reinterpret_cast<u32x4*>(&lds[(t + k * kRows) * S + c]) = r[k];
   }
@@ -173,64 +182,109 @@ k_attn_sweep_bf16(const AttnSweep s) {
     const float* ep = nullptr;
     if (!SUM && s.entry != nullptr) ep = s.entry + ((s.n_spans > 1 ? span * s.rows : 0) + row) * KD * VD + soff;
 #pragma unroll
-    for (int f = 0; f < NS; ++f)
-      st[f / AR][f % AR] = ep != nullptr ? ep[(4 * NG * (f / 4) + 4 * g + f % 4) * s.sn] : 0.f;
+    for (int f = 0; f < NS; f += 4) {
+      const int n0 = NG * f + 4 * g;
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      if (ep != nullptr) {
+        if (s.sn == 1) {
+          v = *reinterpret_cast<const f32x4*>(ep + n0);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = ep[(n0 + j) * s.sn];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) st[(f + j) / AR][(f + j) % AR] = v[j];
+    }
   }
 
   // The masked 16 x 16 tiles of P inside the tiles that join reads are never
   // written: zero once.
-  if (!SUM && tid < 128) {
+  if (!SUM && tid < 2 * kQ) {
     const int t = (REV ? 16 : 0) + 32 * (tid >> 6) + (lane >> 2), i = (REV ? 0 : 16) + 32 * (tid >> 6) + 4 * (lane & 3);
     *reinterpret_cast<u32x2*>(&sP[0][t * SP + i]) = u32x2{0, 0};
     *reinterpret_cast<u32x2*>(&sP[1][t * SP + i]) = u32x2{0, 0};
   }
 
+  // Decays that are the same in every block.  A step's weight in the update is
+  // gamma^(63 - i) (gamma^(i + 1) in reverse) for row i = KC kt + 8 g + j of the
+  // block: a power of the lane group times one of (kt, j), the latter uniform.
+  // So that this also holds for a block of fewer than 64 steps, forward blocks
+  // keep their steps in the last rows (in reverse: the first), the others zero.
+  const float wg = hw_exp2(gl * (float)(REV ? 8 * g : 8 * (NG - 1 - g))) * s.s_write;
+  float wj[8], wk[KT];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) wj[j] = uniform_f32(hw_exp2(gl * (float)(REV ? j + 1 : 7 - j)));
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) wk[kt] = uniform_f32(hw_exp2(gl * (float)(REV ? KC * kt : KC * (KT - 1 - kt))));
+  // Pairs of neighbouring 16 x 16 tiles: gamma^|t - i| at j = 3 (j = 0 in
+  // reverse), the smallest power of the lane's four (at least 1).
+  const float po = hw_exp2(gl * (float)(16 + (REV ? 4 * q4 - r16 : r16 - 4 * q4 - 3))) * s.s_pair;
+  const uint32_t ooff = ((uint32_t)r * (uint32_t)(s.nheads * VD) + R * w + 4 * g) * sizeof(O);
+  const float g16 = hw_exp2(gl * 16.f);
+
   Stage<KD, SA> ga;
   Stage<KD, SB> gb;
   Stage<VD, SC> gc;
   const int64_t nblk = (e - s0 + kQ - 1) / kQ;
-  auto fetch = [&](int64_t k) {
+  // Block k: m steps, of which row x is step tb + x.
+  auto block = [&](int64_t k, int64_t& tb, int& m) {
     const int64_t t0 = s0 + (REV ? nblk - 1 - k : k) * kQ;
-    const int m = (int)min((int64_t)kQ, e - t0);
-    if (!SUM) ga.load(A + t0 * s.a.stride, s.a.stride, m);
-    gb.load(B + t0 * s.b.stride, s.b.stride, m);
-    gc.load(C + t0 * s.c.stride, s.c.stride, m);
+    m = (int)min((int64_t)kQ, e - t0);
+    tb = REV ? t0 : t0 - (kQ - m);
+  };
+  auto fetch = [&](int64_t k) {
+    int64_t tb;
+    int m;
+    block(k, tb, m);
+    const int lo = REV ? 0 : kQ - m, hi = REV ? m : kQ;
+    if (!SUM) ga.load(A + tb * s.a.stride, s.a.stride, lo, hi);
+    gb.load(B + tb * s.b.stride, s.b.stride, lo, hi);
+    gc.load(C + tb * s.c.stride, s.c.stride, lo, hi);
   };
   if (nblk > 0) fetch(0);
   for (int64_t k = 0; k < nblk; ++k) {
-    const int64_t t0 = s0 + (REV ? nblk - 1 - k : k) * kQ;
-    const int m = (int)min((int64_t)kQ, e - t0);
-    if (!SUM) ga.put(sA);
-    gb.put(sB);
-    gc.put(sC);
+    int64_t tb;
+    int m;
+    block(k, tb, m);
+    const int lo = REV ? 0 : kQ - m, hi = REV ? m : kQ;
+    if (!SUM) ga.put(sA, lo, hi);
+    gb.put(sB, lo, hi);
+    gc.put(sC, lo, hi);
     __syncthreads();
     if (k + 1 < nblk) fetch(k + 1);
 
     Acc o[SUM ? 1 : TT];
     if (!SUM) {
-      // pairs: wave w has the steps t of tile w, tiles it of i up to (from) it:
-      // S^T = B A^T, decayed and split.
-      u32x4 av[KD / 32];
-#pragma unroll
-      for (int kk = 0; kk < KD / 32; ++kk) av[kk] = lds16(&sA[(16 * w + r16) * SA + 32 * kk + 8 * q4]);
-      for (int it = REV ? w : 0; it < (REV ? 4 : w + 1); ++it) {
+      // pairs: the ten tiles (rows i of tile it, steps t of tile tt) on or beside
+      // the diagonal, dealt to the waves.
+      for (int x = w; x < kQ / 16 * (kQ / 16 + 1) / 2; x += 4) {
+        const int big = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, small = x - big * (big + 1) / 2;
+        const int it = REV ? big : small, tt = REV ? small : big;
         f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kk = 0; kk < KD / 32; ++kk)
-          p = Tile<16>::mma(lds16(&sB[(16 * it + r16) * SB + 32 * kk + 8 * q4]), av[kk], p);
-        const int d0 = (16 * w + r16 - (16 * it + 4 * q4)) * (REV ? -1 : 1);  // steps between t and i, j = 0
+          p = Tile<16>::mma(lds16(&sB[(16 * it + r16) * SB + 32 * kk + 8 * q4]),
+                            lds16(&sA[(16 * tt + r16) * SA + 32 * kk + 8 * q4]), p);
         float v[4];
+        if (big == small) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int d = REV ? d0 + j : d0 - j;
-          v[j] = d >= 0 ? p[j] * (hw_exp2(gl * (float)d) * s.s_pair) : 0.f;
+          for (int j = 0; j < 4; ++j) {
+            const int d = REV ? 4 * q4 + j - r16 : r16 - 4 * q4 - j;
+            v[j] = d >= 0 ? p[j] * (hw_exp2(gl * (float)d) * s.s_pair) : 0.f;
+          }
+        } else {
+          const float f = po * (big - small == 1 ? 1.f : (big - small == 2 ? g16 : g16 * g16));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = p[j] * (f * (REV ? (j == 0 ? 1.f : wj[j - 1]) : wj[4 + j]));
         }
-        const int at = (16 * w + r16) * SP + 16 * it + 4 * q4;
+        const int at = (16 * tt + r16) * SP + 16 * it + 4 * q4;
         const uint32_t h0 = peel(v[0], v[1]), h1 = peel(v[2], v[3]);
         *reinterpret_cast<u32x2*>(&sP[0][at]) = u32x2{h0, h1};
         *reinterpret_cast<u32x2*>(&sP[1][at]) = u32x2{pack(v[0], v[1]), pack(v[2], v[3])};
       }
 
+        __builtin_amdgcn_sched_barrier(0);
       // read
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt)
@@ -246,19 +300,23 @@ k_attn_sweep_bf16(const AttnSweep s) {
           hi[q] = peel(v0, v1);
           lo[q] = pack(v0, v1);
         }
+        u32x4 a[TT];
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt) {
           const uint16_t* p = &sA[(R * tt + r) * SA + KC * ks + 4 * g];
-          const u32x4 a = cat(*reinterpret_cast<const u32x2*>(p), *reinterpret_cast<const u32x2*>(p + 4 * NG));
-          o[tt] = M::mma(hi, a, o[tt]);
-          o[tt] = M::mma(lo, a, o[tt]);
+          a[tt] = cat(*reinterpret_cast<const u32x2*>(p), *reinterpret_cast<const u32x2*>(p + 4 * NG));
         }
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) o[tt] = M::mma(hi, a[tt], o[tt]);
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) o[tt] = M::mma(lo, a[tt], o[tt]);
+        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) {
-        const int t = R * tt + r;
-        // Behind the end (t >= m) the exponent is clamped: those columns are not stored.
-        const float rf = hw_exp2(gl * (float)(REV ? max(m - 1 - t, 0) : t + 1)) * s.s_read;
+        // Rows without a step (exponent below the first's) are not stored.
+        const int x = R * tt + r;
+        const float rf = hw_exp2(gl * (float)max(REV ? m - 1 - x : x + 1 - (kQ - m), 0)) * s.s_read;
         o[tt] *= rf;
       }
     }
@@ -273,6 +331,7 @@ k_attn_sweep_bf16(const AttnSweep s) {
       for (int kt = 0; kt < KT; ++kt) cv[kt] = cat(lds_tr4(p + KC * kt * SC), lds_tr4(p + (KC * kt + 4) * SC));
     }
 
+        __builtin_amdgcn_sched_barrier(0);
     // update
     const float fac = hw_exp2(gl * (float)m);
 #pragma unroll
@@ -280,12 +339,12 @@ k_attn_sweep_bf16(const AttnSweep s) {
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
       u32x4 w0, w1, w2;
+      float wl = wg * wk[kt];
+      asm volatile("" : "+v"(wl));  // keeps wl * wj[] from being held in 8 KT registers
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int i = KC * kt + 8 * g + 2 * q;
-        // c is zero behind the end; the exponent is clamped to keep its weight finite.
-        float v0 = lo_f32(cv[kt][q]) * (hw_exp2(gl * (float)(REV ? i + 1 : max(m - 1 - i, 0))) * s.s_write);
-        float v1 = hi_f32(cv[kt][q]) * (hw_exp2(gl * (float)(REV ? i + 2 : max(m - 2 - i, 0))) * s.s_write);
+        float v0 = lo_f32(cv[kt][q]) * (wl * wj[2 * q]);
+        float v1 = hi_f32(cv[kt][q]) * (wl * wj[2 * q + 1]);
         w0[q] = peel(v0, v1);
         w1[q] = peel(v0, v1);
         w2[q] = pack(v0, v1);
@@ -299,6 +358,7 @@ k_attn_sweep_bf16(const AttnSweep s) {
         st[nt] = M::mma(bv, w1, st[nt]);
         st[nt] = M::mma(bv, w2, st[nt]);
       }
+        __builtin_amdgcn_sched_barrier(0);
     }
     __syncthreads();  // P complete; a, b and c no longer read
 
@@ -313,11 +373,12 @@ k_attn_sweep_bf16(const AttnSweep s) {
           o[tt] = M::mma(cv[kt], lds16(p + KC * kt), o[tt]);
           o[tt] = M::mma(cv[kt], lds16(p + kQ * SP + KC * kt), o[tt]);
         }
-        if (R * tt + r < m) {
-          O* op = out + (t0 + R * tt + r) * s.nheads * VD + R * w + 4 * g;
+        const int x = R * tt + r;
+        if (x >= lo && x < hi) {
+          gchar* op = uniform_ptr(out + (tb + R * tt) * s.nheads * VD);
 #pragma unroll
           for (int q = 0; q < AR / 4; ++q)
-            put4(op + 4 * NG * q, o[tt][4 * q], o[tt][4 * q + 1], o[tt][4 * q + 2], o[tt][4 * q + 3]);
+            put4<O>(op, ooff + 4 * NG * q * sizeof(O), o[tt][4 * q], o[tt][4 * q + 1], o[tt][4 * q + 2], o[tt][4 * q + 3]);
         }
       }
     }
@@ -325,13 +386,27 @@ k_attn_sweep_bf16(const AttnSweep s) {
 
   if (!SUM) {
     // Rows behind the sequence's end.
-    for (int64_t t = e + tid / (VD / 4); t < s1; t += 256 / (VD / 4))
-      put4(out + t * s.nheads * VD + 4 * (tid % (VD / 4)), 0.f, 0.f, 0.f, 0.f);
+    for (int64_t t = e + tid / (VD / 4); t < s1; t += 256 / (VD / 4)) {
+      O* op = out + t * s.nheads * VD + 4 * (tid % (VD / 4));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) io_store(op + j, 0.f);
+    }
   }
   if (s.exit != nullptr && (SUM || span == (REV ? 0 : s.n_spans - 1))) {
     float* xp = s.exit + ((SUM ? span * s.rows : 0) + row) * KD * VD + soff;
 #pragma unroll
-    for (int f = 0; f < NS; ++f) xp[(4 * NG * (f / 4) + 4 * g + f % 4) * s.sn] = st[f / AR][f % AR];
+    for (int f = 0; f < NS; f += 4) {
+      const int n0 = NG * f + 4 * g;
+      f32x4 v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = st[(f + j) / AR][(f + j) % AR];
+      if (s.sn == 1) {
+        *reinterpret_cast<f32x4*>(xp + n0) = v;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xp[(n0 + j) * s.sn] = v[j];
+      }
+    }
   }
 }
 
@@ -339,8 +414,11 @@ template <typename O, bool REV, bool SUM>
 hipError_t by_width(const AttnSweep& s, int64_t kd, int64_t vd, hipStream_t stream) {
   const unsigned grid = (unsigned)(s.rows * s.n_spans);
   auto go = [&](auto kern) { return launch(kern, dim3(grid), dim3(256), 0, stream, s); };
-  if (kd == 64) return vd == 64 ? go(k_attn_sweep_bf16<O, 64, 16, REV, SUM>) : go(k_attn_sweep_bf16<O, 64, 32, REV, SUM>);
-  return vd == 64 ? go(k_attn_sweep_bf16<O, 128, 16, REV, SUM>) : go(k_attn_sweep_bf16<O, 128, 32, REV, SUM>);
+  if (kd == 64)
+    return vd == 64 ? go(k_attn_sweep_bf16<O, 64, 16, REV, SUM>)
+                    : go(k_attn_sweep_bf16<O, 64, 32, REV, SUM>);
+  return vd == 64 ? go(k_attn_sweep_bf16<O, 128, 16, REV, SUM>)
+                  : go(k_attn_sweep_bf16<O, 128, 32, REV, SUM>);
 }
 
 }  // namespace
