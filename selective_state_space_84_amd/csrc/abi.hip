@@ -741,7 +741,7 @@ int qk_norm_rope_impl(ssm::QkNormRopeLaunch p, int32_t io_dtype, int32_t interle
   const Rows outs[] = {qo, ko, dense(p.dwq, b_w), dense(p.dwk, b_w)};
   if ((rc = check_alias(outs, 4, ins, 8)) != SSM_OK) return rc;
   if (grad && (p.dwq != nullptr || p.dwk != nullptr)) {
-    const int64_t need = ssm::qk_norm_rope_bwd_floats(tokens, p.nheads, p.nheads_k, p.headdim) * 4;
+    const int64_t need = ssm::qk_norm_rope_bwd_floats(tokens, p.headdim) * 4;
     if (need > 0) {
       if (p.workspace == nullptr || workspace_bytes < (size_t)need) return SSM_ERR_WORKSPACE;
       if (!aligned(p.workspace, kWorkspaceAlign)) return SSM_ERR_MISALIGNED;
@@ -907,7 +907,7 @@ int ssm_qk_norm_rope_bwd(const void* q, const void* k, const float* wq, const fl
 size_t ssm_qk_norm_rope_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_k,
                                            int64_t headdim) {
   if (check_qk_dims(batch, seqlen, nheads, nheads_k, headdim) != SSM_OK) return (size_t)-1;
-  return (size_t)ssm::qk_norm_rope_bwd_floats(batch * seqlen, nheads, nheads_k, headdim) * 4;
+  return (size_t)ssm::qk_norm_rope_bwd_floats(batch * seqlen, headdim) * 4;
 }
 
 int ssm_conv1d_fwd(const void* x, const float* w, const float* bias, const float* state_in, void* y,

@@ -266,8 +266,7 @@ struct QkNormRopeLaunch {
   float* dwk;  // nullable
   float* workspace;
 };
-int64_t qk_norm_rope_blocks(int64_t tokens, int64_t nheads, int64_t nheads_k, int64_t rot_dim);
-int64_t qk_norm_rope_bwd_floats(int64_t tokens, int64_t nheads, int64_t nheads_k, int64_t headdim);
+int64_t qk_norm_rope_bwd_floats(int64_t tokens, int64_t headdim);
 hipError_t launch_qk_norm_rope(const QkNormRopeLaunch& p);
 hipError_t launch_qk_norm_rope_bwd(const QkNormRopeLaunch& p);
 
