@@ -360,10 +360,13 @@ def _rows(t, what: str) -> Tuple[Optional[int], int]:
     if not t.is_cuda:
         raise ValueError("tensor must live on the GPU")
     heads, width = t.shape[-2:]
-    ok = (width <= 1 or t.stride(-1) == 1) and (heads <= 1 or t.stride(-2) == width)
+    if t.is_contiguous():
+        return t.data_ptr() or None, heads * width
+    *lead, s_head, s_elem = t.stride()
+    ok = (width <= 1 or s_elem == 1) and (heads <= 1 or s_head == width)
     step = None
     expect = None  # stride of the next axis to the left
-    for n, s in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+    for n, s in zip(reversed(t.shape[:-2]), reversed(lead)):
         if n != 1:
             if step is None:
                 step = s
@@ -375,26 +378,33 @@ def _rows(t, what: str) -> Tuple[Optional[int], int]:
     return t.data_ptr() or None, (heads * width if step is None else step)
 
 
+_no_scope = contextlib.nullcontext()
+
+
 def _scope(stream, t, *others):
     """Context in which t's device is current, and so is stream (a torch stream
     or a raw handle) when one is given: what is allocated inside belongs to the
     stream that uses it.  Every other tensor must be on t's device."""
     import torch
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("tensor must live on the GPU")
-    dev = t.device
     for o in others:
-        if o is not None and o.device != dev:
-            raise ValueError("tensors must be on one device, got %s and %s" % (dev, o.device))
+        if o is not None and o.get_device() != dev:
+            raise ValueError("tensors must be on one device, got %s and %s" % (t.device, o.device))
     if stream is None:
-        if torch.cuda.current_device() == dev.index:
-            return contextlib.nullcontext()
-        return torch.cuda.device(dev)
+        return _no_scope if torch.cuda.current_device() == dev else torch.cuda.device(dev)
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
-    if stream.device != dev:
-        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, dev))
+        stream = torch.cuda.ExternalStream(stream, device=t.device) if stream else torch.cuda.default_stream(t.device)
+    if stream.device != t.device:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, t.device))
     return torch.cuda.stream(stream)  # also makes the stream's device current
+
+
+def _here(t) -> Optional[int]:
+    """Raw handle of the stream that is current on t's device."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) or None
 
 
 def _workspace(workspace, need, device, what):
@@ -407,7 +417,7 @@ def _workspace(workspace, need, device, what):
 
 
 def _want(t, shape, dtype, what):
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+    if t is not None and (t.shape != shape or t.dtype != dtype):
         raise ValueError("%s must be %s %s, got %s %s" % (what, tuple(shape), dtype, tuple(t.shape), t.dtype))
 
 
@@ -429,8 +439,9 @@ def _attn_shapes(q, k, v, lead):
     nheads_kv, d_v = v.shape[-2:]
     if q.dim() != lead + 2:
         raise ValueError("q must have %d axes, got %s" % (lead + 2, tuple(q.shape)))
-    _want(k, (*q.shape[:lead], nheads_kv, d_k), q.dtype, "k")
-    _want(v, (*q.shape[:lead], nheads_kv, d_v), q.dtype, "v")
+    rows = q.shape[:lead]
+    _want(k, rows + (nheads_kv, d_k), q.dtype, "k")
+    _want(v, rows + (nheads_kv, d_v), q.dtype, "v")
     return nheads, nheads_kv, d_k, d_v
 
 
@@ -467,7 +478,7 @@ def ssm_linear_attn_fwd(q, k, v, log_decay, *, lengths=None, h0=None, scale=None
         rc = lib.ssm_linear_attn_fwd(qp, kp, vp, _ptr(log_decay), _ptr(lengths), _ptr(h0), _ptr(o), _ptr(h_last),
                                      batch, seqlen, nheads, nheads_kv, d_k, d_v, qs, ks, vs,
                                      d_k ** -0.5 if scale is None else scale, dt, _ptr(workspace), have,
-                                     _stream(None))
+                                     _here(q))
     if rc != SSM_OK:
         raise SsmError(rc, "ssm_linear_attn_fwd")
     return o, h_last
@@ -505,7 +516,7 @@ def ssm_linear_attn_bwd(q, k, v, log_decay, *, do, lengths=None, h0=None, dh_las
                                      _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g.get("dh0")), batch, seqlen,
                                      nheads, nheads_kv, d_k, d_v, qs, ks, vs,
                                      d_k ** -0.5 if scale is None else scale, dt, _ptr(workspace), have,
-                                     _stream(None))
+                                     _here(q))
     if rc != SSM_OK:
         raise SsmError(rc, "ssm_linear_attn_bwd")
     return g
@@ -533,7 +544,7 @@ def ssm_linear_attn_update(h, q, k, v, log_decay, *, slots=None, scale=None, o=N
         (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
         rc = load_library().ssm_linear_attn_update(
             _ptr(h), _ptr(slots), qp, kp, vp, _ptr(log_decay), _ptr(o), batch, h.shape[0], nheads, nheads_kv, d_k,
-            d_v, qs, ks, vs, d_k ** -0.5 if scale is None else scale, dt, _stream(None))
+            d_v, qs, ks, vs, d_k ** -0.5 if scale is None else scale, dt, _here(q))
     if rc != SSM_OK:
         raise SsmError(rc, "ssm_linear_attn_update")
     return o
@@ -585,7 +596,7 @@ def ssm_qk_norm_rope_fwd(q, k, wq=None, wk=None, inv_freq=None, *, positions=Non
         (kp, ks), (ko, kos) = ((None, 0),) * 2 if k is None else (_rows(k, "k"), _rows(k_out, "k_out"))
         rc = load_library().ssm_qk_norm_rope_fwd(
             qp, kp, _ptr(wq), _ptr(wk), _ptr(inv_freq), _ptr(positions), qo, ko, batch, seqlen, nheads, nheads_k,
-            headdim, rot, qs, ks, qos, kos, eps, 1 if interleaved else 0, _io_dtype(q), _stream(None))
+            headdim, rot, qs, ks, qos, kos, eps, 1 if interleaved else 0, _io_dtype(q), _here(q))
     if rc != SSM_OK:
         raise SsmError(rc, "ssm_qk_norm_rope_fwd")
     return q_out, k_out
@@ -624,7 +635,7 @@ def ssm_qk_norm_rope_bwd(q, k, wq=None, wk=None, inv_freq=None, *, dq_out, dk_ou
             qp, kp, _ptr(wq), _ptr(wk), _ptr(inv_freq), _ptr(positions), _ptr(dq_out),
             None if k is None else _ptr(dk_out), _ptr(g["dq"]), _ptr(g.get("dk")), _ptr(g.get("dwq")),
             _ptr(g.get("dwk")), batch, seqlen, nheads, nheads_k, headdim, rot, qs, ks, eps, 1 if interleaved else 0,
-            _io_dtype(q), _ptr(workspace), have, _stream(None))
+            _io_dtype(q), _ptr(workspace), have, _here(q))
     if rc != SSM_OK:
         raise SsmError(rc, "ssm_qk_norm_rope_bwd")
     return g

@@ -232,17 +232,26 @@ __global__ void __launch_bounds__(256) k_attn_carry(float* st, const float* star
   const int64_t len = row_length(lengths, row / nheads, seqlen);
   f32x4* const p = reinterpret_cast<f32x4*>(st) + i;
   f32x4 e = start != nullptr ? reinterpret_cast<const f32x4*>(start)[i] : f32x4{0.f, 0.f, 0.f, 0.f};
-  f32x4 own = p[(REV ? n_spans - 1 : 0) * rows * state4];
-  for (int64_t k = 0; k < n_spans; ++k) {
-    const int64_t s = REV ? n_spans - 1 - k : k;
-    const f32x4 cur = own;
-    if (k + 1 < n_spans) own = p[(REV ? s - 1 : s + 1) * rows * state4];
-    p[s * rows * state4] = e;
-    const int64_t s0 = s * span_len, s1 = min(s0 + span_len, seqlen);
-    const int64_t m = min(s1, len) > s0 ? min(s1, len) - s0 : 0;
-    const float f = hw_exp2(g * (float)m);
+  constexpr int kAhead = 8;  // spans on their way
+  for (int64_t k0 = 0; k0 < n_spans; k0 += kAhead) {
+    f32x4 own[kAhead];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) e[j] = __builtin_fmaf(f, e[j], cur[j]);
+    for (int x = 0; x < kAhead; ++x) {
+      const int64_t k = k0 + x < n_spans ? k0 + x : n_spans - 1;
+      own[x] = p[(REV ? n_spans - 1 - k : k) * rows * state4];
+    }
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      const int64_t k = k0 + x;
+      if (k >= n_spans) break;
+      const int64_t s = REV ? n_spans - 1 - k : k;
+      p[s * rows * state4] = e;
+      const int64_t s0 = s * span_len, s1 = min(s0 + span_len, seqlen);
+      const int64_t m = min(s1, len) > s0 ? min(s1, len) - s0 : 0;
+      const float f = hw_exp2(g * (float)m);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[j] = __builtin_fmaf(f, e[j], own[x][j]);
+    }
   }
 }
 
@@ -293,18 +302,22 @@ AttnSweep base(const LinAttnLaunch& p, const LinAttnPlan& pl) {
 
 }  // namespace
 
-// Workgroups a launch should have: below, the sequence is cut into spans of at
-// least kMinSpan steps, at the price of reading b and c twice.
+// When the (row, head) pairs are few, the sequence is cut into spans of at least
+// kMinSpan steps, at the price of a summary sweep that reads b and c once more:
+// as many as make two workgroups a CU (512 in all).  Two spans do not pay: a CU
+// takes two blocks of different workgroups together in ~1.6 times the time of
+// one, and the summary costs 0.4 of a sweep (8 x 2048 steps x 32 heads of 128,
+// 256 pairs: 157 us whole, 202 us in two spans; 1 x 32768 x 32: 417 us in 16
+// spans, 472 us in 8, 440 us in 32).
 constexpr int64_t kTargetGroups = 512;
-constexpr int64_t kMinSpan = 256;
+constexpr int64_t kMinSpan = 128;
 constexpr int64_t kSpanStep = 64;  // spans start on block boundaries of both sweeps
 
 LinAttnPlan linear_attn_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16) {
   const int64_t groups = batch * nheads * (bf16 ? 1 : (d_k > d_v ? d_k : d_v) / kCols);
-  int64_t n = 1;
-  if (groups > 0 && groups < kTargetGroups) n = kTargetGroups / groups;
+  int64_t n = groups > 0 ? kTargetGroups / groups : 1;
   if (n > seqlen / kMinSpan) n = seqlen / kMinSpan;
-  if (n < 1) n = 1;
+  if (n < 3) n = 1;
   int64_t len = (seqlen + n - 1) / n;
   len = (len + kSpanStep - 1) / kSpanStep * kSpanStep;
   if (len < kSpanStep) len = kSpanStep;
