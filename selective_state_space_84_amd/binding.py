@@ -421,16 +421,29 @@ def _want(t, shape, dtype, what):
         raise ValueError("%s must be %s %s, got %s %s" % (what, tuple(shape), dtype, tuple(t.shape), t.dtype))
 
 
+def _dense(t, what) -> Optional[int]:
+    """_ptr of a tensor that is known to be on the GPU."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    return t.data_ptr() or None
+
+
 def _fill(g, names, device):
     """Checks the outputs given in g and allocates the others; names: (name, shape, dtype)."""
     import torch
-    for n in g:
-        if n not in [name for name, _, _ in names]:
-            raise ValueError("unknown output %s" % n)
+    if g:
+        known = [name for name, _, _ in names]
+        for n in g:
+            if n not in known:
+                raise ValueError("unknown output %s" % n)
     for name, shape, dtype in names:
-        _want(g.get(name), shape, dtype, name)
-        if g.get(name) is None:
-            g[name] = torch.empty(tuple(shape), dtype=dtype, device=device)
+        t = g.get(name)
+        if t is None:
+            g[name] = torch.empty(shape, dtype=dtype, device=device)
+        else:
+            _want(t, shape, dtype, name)
 
 
 def _attn_shapes(q, k, v, lead):
@@ -532,19 +545,22 @@ def ssm_linear_attn_update(h, q, k, v, log_decay, *, slots=None, scale=None, o=N
     """
     import torch
     nheads, nheads_kv, d_k, d_v = _attn_shapes(q, k, v, 1)
-    batch = q.shape[0]
+    batch, n_slots = q.shape[0], h.shape[0]
     dt = _io_dtype(q)
-    _want(h, (h.shape[0], nheads, d_v, d_k), torch.float32, "h")
-    _want(slots, (batch,), torch.int32, "slots")
-    _want(log_decay, (nheads,), torch.float32, "log_decay")
-    _want(o, (batch, nheads, d_v), q.dtype, "o")
+    f32 = torch.float32
+    _want(h, (n_slots, nheads, d_v, d_k), f32, "h")
+    _want(log_decay, (nheads,), f32, "log_decay")
+    if slots is not None:
+        _want(slots, (batch,), torch.int32, "slots")
+    if o is not None:
+        _want(o, (batch, nheads, d_v), q.dtype, "o")
     with _scope(stream, q, h, slots, k, v, log_decay, o):
         if o is None:
             o = torch.empty((batch, nheads, d_v), dtype=q.dtype, device=q.device)
         (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
         rc = load_library().ssm_linear_attn_update(
-            _ptr(h), _ptr(slots), qp, kp, vp, _ptr(log_decay), _ptr(o), batch, h.shape[0], nheads, nheads_kv, d_k,
-            d_v, qs, ks, vs, d_k ** -0.5 if scale is None else scale, dt, _here(q))
+            _dense(h, "h"), _dense(slots, "slots"), qp, kp, vp, _dense(log_decay, "log_decay"), _dense(o, "o"), batch,
+            n_slots, nheads, nheads_kv, d_k, d_v, qs, ks, vs, d_k ** -0.5 if scale is None else scale, dt, _here(q))
     if rc != SSM_OK:
         raise SsmError(rc, "ssm_linear_attn_update")
     return o
@@ -560,13 +576,33 @@ def _qk_shapes(q, k):
 def _qk_params(wq, wk, inv_freq, positions, batch, seqlen, headdim):
     """Checks of the norm weights, frequencies and positions; returns rot_dim."""
     import torch
-    _want(wq, (headdim,), torch.float32, "wq")
-    _want(wk, (headdim,), torch.float32, "wk")
-    _want(positions, (batch, seqlen), torch.int64, "positions")
+    f32 = torch.float32
+    if wq is not None:
+        _want(wq, (headdim,), f32, "wq")
+    if wk is not None:
+        _want(wk, (headdim,), f32, "wk")
+    if positions is not None:
+        _want(positions, (batch, seqlen), torch.int64, "positions")
     if inv_freq is None:
         return 0
-    _want(inv_freq, (inv_freq.numel(),), torch.float32, "inv_freq")
-    return 2 * inv_freq.numel()
+    n = inv_freq.numel()
+    _want(inv_freq, (n,), f32, "inv_freq")
+    return 2 * n
+
+
+def _side(x, out, what):
+    """(input, its step, output, its step, output tensor) of q or k; the output is allocated when None."""
+    import torch
+    if x is None:
+        if out is not None:
+            raise ValueError("%s_out given without %s" % (what, what))
+        return None, 0, None, 0, None
+    p, step = _rows(x, what)
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        return p, step, out.data_ptr() or None, 0, out
+    _want(out, x.shape, x.dtype, what + "_out")
+    return (p, step, *_rows(out, what + "_out"), out)
 
 
 def ssm_qk_norm_rope_fwd(q, k, wq=None, wk=None, inv_freq=None, *, positions=None, eps=1e-6, interleaved=False,
@@ -579,24 +615,15 @@ def ssm_qk_norm_rope_fwd(q, k, wq=None, wk=None, inv_freq=None, *, positions=Non
     (batch, seqlen) int64, or None for the step's index.  q_out and k_out may be q
     and k themselves (in place).
     """
-    import torch
     batch, seqlen, nheads, nheads_k, headdim = _qk_shapes(q, k)
     rot = _qk_params(wq, wk, inv_freq, positions, batch, seqlen, headdim)
-    _want(q_out, q.shape, q.dtype, "q_out")
-    if k is None and k_out is not None:
-        raise ValueError("k_out given without k")
-    if k is not None:
-        _want(k_out, k.shape, q.dtype, "k_out")
     with _scope(stream, q, k, wq, wk, inv_freq, positions, q_out, k_out):
-        if q_out is None:
-            q_out = torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)
-        if k_out is None and k is not None:
-            k_out = torch.empty(tuple(k.shape), dtype=q.dtype, device=q.device)
-        (qp, qs), (qo, qos) = _rows(q, "q"), _rows(q_out, "q_out")
-        (kp, ks), (ko, kos) = ((None, 0),) * 2 if k is None else (_rows(k, "k"), _rows(k_out, "k_out"))
+        qp, qs, qo, qos, q_out = _side(q, q_out, "q")
+        kp, ks, ko, kos, k_out = _side(k, k_out, "k")
         rc = load_library().ssm_qk_norm_rope_fwd(
-            qp, kp, _ptr(wq), _ptr(wk), _ptr(inv_freq), _ptr(positions), qo, ko, batch, seqlen, nheads, nheads_k,
-            headdim, rot, qs, ks, qos, kos, eps, 1 if interleaved else 0, _io_dtype(q), _here(q))
+            qp, kp, _dense(wq, "wq"), _dense(wk, "wk"), _dense(inv_freq, "inv_freq"), _dense(positions, "positions"),
+            qo, ko, batch, seqlen, nheads, nheads_k, headdim, rot, qs, ks, qos, kos, eps, 1 if interleaved else 0,
+            _io_dtype(q), _here(q))
     if rc != SSM_OK:
         raise SsmError(rc, "ssm_qk_norm_rope_fwd")
     return q_out, k_out
