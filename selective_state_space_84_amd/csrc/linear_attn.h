@@ -52,10 +52,14 @@ struct AttnSweep {
   float s_pair, s_read, s_write;
 };
 
-// The sweep for bf16 operands (linear_attn_bf16.hip).  sum: only the spans'
-// states; out32: fp32 outputs.
-hipError_t launch_attn_sweep_bf16(const AttnSweep& s, int64_t kd, int64_t vd, bool rev, bool sum, bool out32,
-                                  hipStream_t stream);
+// The sweeps for bf16 operands (linear_attn_bf16.hip): a forward sweep with bf16
+// outputs; the spans' states forwards and (r not NULL) in reverse; the three
+// gradient sweeps, dk and dv to fp32 buffers when out32.
+hipError_t launch_attn_sweep_bf16(const AttnSweep& s, int64_t kd, int64_t vd, hipStream_t stream);
+hipError_t launch_attn_span_states_bf16(const AttnSweep& f, const AttnSweep* r, int64_t kd, int64_t vd,
+                                        hipStream_t stream);
+hipError_t launch_attn_sweep_grad_bf16(const AttnSweep& q, const AttnSweep& k, const AttnSweep& v, int64_t d_k,
+                                       int64_t d_v, bool out32, hipStream_t stream);
 
 // log2(gamma); -inf is kept finite so that 0 steps of decay give 1 (0 * -inf
 // would be NaN) and one step or more still gives 0.

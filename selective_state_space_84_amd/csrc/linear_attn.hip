@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(256) k_attn_sweep_f32(const AttnSweep s) {
   int64_t id = xcd_remap(blockIdx.x, gridDim.x);
   const int slice = (int)(id % s.slices);
   id /= s.slices;
-  const int64_t row = id % s.rows, span = id / s.rows;
+  const int64_t row = id % s.rows, span = id / s.rows + (SUM && REV ? 1 : 0);
   const int64_t b = row / s.nheads;
   const int h = (int)(row % s.nheads);
   const int64_t VD = (int64_t)s.slices * kCols;
@@ -216,37 +216,38 @@ __global__ void __launch_bounds__(256) k_attn_sweep_f32(const AttnSweep s) {
 }
 
 // ---- carries between spans ----------------------------------------------
-// In place: st[span][row][...] holds every span's state from a zero entry and
-// receives the state that enters the span: E_0 = start, E_{s+1} = gamma^len_s
-// E_s + S_s (from the last span downwards in reverse).  Four elements a
-// thread, sums in span order.
+// In place: st[span][row][...] holds every span's state from a zero entry (but
+// the last one's) and receives the state that enters the span: E_0 = start,
+// E_{s+1} = gamma^len_s E_s + S_s (from the last span downwards in reverse).
+// Four elements a thread, sums in span order.
+struct AttnCarry {
+  float* st;
+  const float* start;  // nullable for zeros
+};
 template <bool REV>
-__global__ void __launch_bounds__(256) k_attn_carry(float* st, const float* start, const float* log_decay,
-                                                    const int32_t* lengths, int64_t rows, int32_t nheads,
-                                                    int64_t state4, int64_t seqlen, int64_t span_len,
-                                                    int64_t n_spans) {
+__device__ __forceinline__ void carry_spans(const AttnCarry& c, const AttnSweep& s, int64_t state4) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * state4) return;
-  const int64_t row = i / state4;
-  const float g = decay_log2(log_decay[row % nheads]);
-  const int64_t len = row_length(lengths, row / nheads, seqlen);
-  f32x4* const p = reinterpret_cast<f32x4*>(st) + i;
-  f32x4 e = start != nullptr ? reinterpret_cast<const f32x4*>(start)[i] : f32x4{0.f, 0.f, 0.f, 0.f};
+  if (i >= s.rows * state4) return;
+  const int64_t row = i / state4, n = s.n_spans;
+  const float g = decay_log2(s.log_decay[row % s.nheads]);
+  const int64_t len = row_length(s.lengths, row / s.nheads, s.seqlen);
+  f32x4* const p = reinterpret_cast<f32x4*>(c.st) + i;
+  f32x4 e = c.start != nullptr ? reinterpret_cast<const f32x4*>(c.start)[i] : f32x4{0.f, 0.f, 0.f, 0.f};
   constexpr int kAhead = 8;  // spans on their way
-  for (int64_t k0 = 0; k0 < n_spans; k0 += kAhead) {
+  for (int64_t k0 = 0; k0 < n; k0 += kAhead) {
     f32x4 own[kAhead];
 #pragma unroll
     for (int x = 0; x < kAhead; ++x) {
-      const int64_t k = k0 + x < n_spans ? k0 + x : n_spans - 1;
-      own[x] = p[(REV ? n_spans - 1 - k : k) * rows * state4];
+      const int64_t k = k0 + x < n - 1 ? k0 + x : n - 2;
+      own[x] = p[(REV ? n - 1 - k : k) * s.rows * state4];
     }
 #pragma unroll
     for (int x = 0; x < kAhead; ++x) {
       const int64_t k = k0 + x;
-      if (k >= n_spans) break;
-      const int64_t s = REV ? n_spans - 1 - k : k;
-      p[s * rows * state4] = e;
-      const int64_t s0 = s * span_len, s1 = min(s0 + span_len, seqlen);
+      if (k >= n) break;
+      const int64_t sp = REV ? n - 1 - k : k;
+      p[sp * s.rows * state4] = e;
+      const int64_t s0 = sp * s.span_len, s1 = min(s0 + s.span_len, s.seqlen);
       const int64_t m = min(s1, len) > s0 ? min(s1, len) - s0 : 0;
       const float f = hw_exp2(g * (float)m);
 #pragma unroll
@@ -254,38 +255,65 @@ __global__ void __launch_bounds__(256) k_attn_carry(float* st, const float* star
     }
   }
 }
+// blockIdx.y 1: in reverse.
+__global__ void __launch_bounds__(256) k_attn_carry(const AttnCarry f, const AttnCarry r, const AttnSweep s,
+                                                    int64_t state4) {
+  if (blockIdx.y == 0) {
+    carry_spans<false>(f, s, state4);
+  } else {
+    carry_spans<true>(r, s, state4);
+  }
+}
 
 // ---- sums over the heads that share a key/value head --------------------
+// blockIdx.y: dk or dv; part holds [step][nheads][4 d4] fp32.
+struct HeadSum {
+  const float* part;
+  void* out;
+  int64_t n4;  // steps x kv heads x d4
+  int32_t d4;
+};
 template <typename T>
-__global__ void __launch_bounds__(256) k_attn_sum_heads(const float* part, T* out, int64_t n4, int32_t d4,
-                                                        int32_t rep) {
+__global__ void __launch_bounds__(256) k_attn_sum_heads(const HeadSum k, const HeadSum v, int32_t rep) {
+  const HeadSum& s = blockIdx.y == 0 ? k : v;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // (step, kv head, 4 columns)
-  if (i >= n4) return;
-  const int64_t head = i / d4;
-  const f32x4* p = reinterpret_cast<const f32x4*>(part) + head * rep * d4 + i % d4;
-  f32x4 v = p[0];
-  for (int r = 1; r < rep; ++r) v += p[(int64_t)r * d4];
-  store4(out + i * 4, v);
+  if (i >= s.n4) return;
+  const int64_t head = i / s.d4;
+  const f32x4* p = reinterpret_cast<const f32x4*>(s.part) + head * rep * s.d4 + i % s.d4;
+  f32x4 x = p[0];
+  for (int r = 1; r < rep; ++r) x += p[(int64_t)r * s.d4];
+  store4(static_cast<T*>(s.out) + i * 4, x);
 }
 
 int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
 
-// out32: the outputs go to an fp32 buffer although the inputs are bf16.
 template <bool REV, bool SUM>
-hipError_t sweep(AttnSweep s, int64_t kd, int64_t vd, bool bf16, bool out32, hipStream_t stream) {
-  if (bf16) return launch_attn_sweep_bf16(s, kd, vd, REV, SUM, out32, stream);
+hipError_t sweep_f32(AttnSweep s, int64_t kd, int64_t vd, hipStream_t stream) {
   s.slices = (int32_t)(vd / kCols);
-  const unsigned grid = (unsigned)(s.rows * s.n_spans * s.slices);
+  const unsigned grid = (unsigned)(s.rows * (s.n_spans - (SUM ? 1 : 0)) * s.slices);
   if (kd == 64) return launch(k_attn_sweep_f32<64, REV, SUM>, dim3(grid), dim3(256), 0, stream, s);
   return launch(k_attn_sweep_f32<128, REV, SUM>, dim3(grid), dim3(256), 0, stream, s);
 }
 
-template <bool REV>
-hipError_t carry(float* st, const float* start, const LinAttnLaunch& p, const LinAttnPlan& pl) {
-  const int64_t rows = p.batch * p.nheads, state4 = p.d_k * p.d_v / 4;
-  const unsigned grid = (unsigned)((rows * state4 + 255) / 256);
-  return launch(k_attn_carry<REV>, dim3(grid), dim3(256), 0, p.stream, st, start, p.log_decay, p.lengths, rows,
-                (int32_t)p.nheads, state4, p.seqlen, pl.span_len, pl.n_spans);
+// The states that enter the spans, of H from h0 into hs and (gs not NULL) of G
+// from dh_last into gs; f and r are the sweeps that add to them.
+hipError_t span_entries(const LinAttnLaunch& p, AttnSweep f, AttnSweep r, float* hs, float* gs) {
+  f.sn = r.sn = 1;
+  f.sp = r.sp = p.d_k;
+  f.exit = hs;
+  r.exit = gs;
+  hipError_t rc;
+  if (p.bf16) {
+    rc = launch_attn_span_states_bf16(f, gs != nullptr ? &r : nullptr, p.d_k, p.d_v, p.stream);
+  } else {
+    rc = sweep_f32<false, true>(f, p.d_k, p.d_v, p.stream);
+    if (rc == hipSuccess && gs != nullptr) rc = sweep_f32<true, true>(r, p.d_k, p.d_v, p.stream);
+  }
+  if (rc != hipSuccess) return rc;
+  const int64_t state4 = p.d_k * p.d_v / 4;
+  const unsigned grid = (unsigned)((f.rows * state4 + 255) / 256);
+  return launch(k_attn_carry, dim3(grid, gs != nullptr ? 2 : 1), dim3(256), 0, p.stream, AttnCarry{hs, p.h0},
+                AttnCarry{gs, p.dh_last}, f, state4);
 }
 
 AttnSweep base(const LinAttnLaunch& p, const LinAttnPlan& pl) {
@@ -313,8 +341,7 @@ constexpr int64_t kTargetGroups = 512;
 constexpr int64_t kMinSpan = 128;
 constexpr int64_t kSpanStep = 64;  // spans start on block boundaries of both sweeps
 
-LinAttnPlan linear_attn_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16) {
-  const int64_t groups = batch * nheads * (bf16 ? 1 : (d_k > d_v ? d_k : d_v) / kCols);
+static LinAttnPlan make_plan(int64_t groups, int64_t seqlen) {
   int64_t n = groups > 0 ? kTargetGroups / groups : 1;
   if (n > seqlen / kMinSpan) n = seqlen / kMinSpan;
   if (n < 3) n = 1;
@@ -324,20 +351,30 @@ LinAttnPlan linear_attn_plan(int64_t batch, int64_t seqlen, int64_t nheads, int6
   return LinAttnPlan{len, seqlen > 0 ? (seqlen + len - 1) / len : 1};
 }
 
-int64_t linear_attn_fwd_floats(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16) {
-  const LinAttnPlan pl = linear_attn_plan(batch, seqlen, nheads, d_k, d_v, bf16);
+LinAttnPlan linear_attn_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16,
+                             bool grad) {
+  // Workgroups of a launch per span: the three gradient sweeps share one in bf16.
+  const int64_t each = bf16 ? (grad ? 3 : 1) : (d_k > d_v ? d_k : d_v) / kCols;
+  return make_plan(batch * nheads * each, seqlen);
+}
+
+static int64_t span_floats(int64_t batch, int64_t nheads, int64_t d_k, int64_t d_v, const LinAttnPlan& pl) {
   return pl.n_spans > 1 ? pl.n_spans * batch * nheads * d_k * d_v : 0;
+}
+
+int64_t linear_attn_fwd_floats(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16) {
+  return span_floats(batch, nheads, d_k, d_v, linear_attn_plan(batch, seqlen, nheads, d_k, d_v, bf16, false));
 }
 
 int64_t linear_attn_bwd_floats(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_kv, int64_t d_k,
                                int64_t d_v, bool bf16) {
-  int64_t n = 2 * linear_attn_fwd_floats(batch, seqlen, nheads, d_k, d_v, bf16);
+  int64_t n = 2 * span_floats(batch, nheads, d_k, d_v, linear_attn_plan(batch, seqlen, nheads, d_k, d_v, bf16, true));
   if (nheads != nheads_kv) n += up64(batch * seqlen * nheads * d_k) + up64(batch * seqlen * nheads * d_v);
   return n;
 }
 
 hipError_t launch_linear_attn_fwd(const LinAttnLaunch& p) {
-  const LinAttnPlan pl = linear_attn_plan(p.batch, p.seqlen, p.nheads, p.d_k, p.d_v, p.bf16);
+  const LinAttnPlan pl = linear_attn_plan(p.batch, p.seqlen, p.nheads, p.d_k, p.d_v, p.bf16, false);
   const int32_t rep = (int32_t)(p.nheads / p.nheads_kv);
   AttnSweep s = base(p, pl);
   s.a = AttnOperand{p.q, p.q_stride, 1};
@@ -349,91 +386,76 @@ hipError_t launch_linear_attn_fwd(const LinAttnLaunch& p) {
   s.s_write = 1.f;
   s.entry = p.h0;
   if (pl.n_spans > 1) {
-    AttnSweep z = s;
-    z.exit = p.workspace;
-    hipError_t rc = sweep<false, true>(z, p.d_k, p.d_v, p.bf16, false, p.stream);
-    if (rc != hipSuccess) return rc;
-    rc = carry<false>(p.workspace, p.h0, p, pl);
+    const hipError_t rc = span_entries(p, s, s, p.workspace, nullptr);
     if (rc != hipSuccess) return rc;
     s.entry = p.workspace;
   }
   s.exit = p.h_last;
   s.out = p.o;
-  return sweep<false, false>(s, p.d_k, p.d_v, p.bf16, false, p.stream);
+  return p.bf16 ? launch_attn_sweep_bf16(s, p.d_k, p.d_v, p.stream)
+                : sweep_f32<false, false>(s, p.d_k, p.d_v, p.stream);
 }
 
 hipError_t launch_linear_attn_bwd(const LinAttnLaunch& p) {
-  const LinAttnPlan pl = linear_attn_plan(p.batch, p.seqlen, p.nheads, p.d_k, p.d_v, p.bf16);
+  const LinAttnPlan pl = linear_attn_plan(p.batch, p.seqlen, p.nheads, p.d_k, p.d_v, p.bf16, true);
   const int32_t rep = (int32_t)(p.nheads / p.nheads_kv);
   const AttnOperand q{p.q, p.q_stride, 1}, k{p.k, p.k_stride, rep}, v{p.v, p.v_stride, rep},
       d{p.d_o, p.nheads * p.d_v, 1};
-  const int64_t states = linear_attn_fwd_floats(p.batch, p.seqlen, p.nheads, p.d_k, p.d_v, p.bf16);
-  const float *h_in = p.h0, *g_in = p.dh_last;
-  hipError_t rc;
-  if (pl.n_spans > 1) {
-    float* const hs = p.workspace;
-    float* const gs = p.workspace + states;
-    AttnSweep z = base(p, pl);
-    z.sn = 1;
-    z.sp = p.d_k;
-    z.b = k;
-    z.c = v;
-    z.s_write = 1.f;
-    z.exit = hs;
-    if ((rc = sweep<false, true>(z, p.d_k, p.d_v, p.bf16, false, p.stream)) != hipSuccess) return rc;
-    z.b = q;
-    z.c = d;
-    z.s_write = p.scale;
-    z.exit = gs;
-    if ((rc = sweep<true, true>(z, p.d_k, p.d_v, p.bf16, false, p.stream)) != hipSuccess) return rc;
-    if ((rc = carry<false>(hs, p.h0, p, pl)) != hipSuccess) return rc;
-    if ((rc = carry<true>(gs, p.dh_last, p, pl)) != hipSuccess) return rc;
-    h_in = hs;
-    g_in = gs;
-  }
+  const int64_t states = span_floats(p.batch, p.nheads, p.d_k, p.d_v, pl);
   const bool shared = p.nheads != p.nheads_kv;
   float* const pk = p.workspace + 2 * states;
   float* const pv = pk + up64(p.batch * p.seqlen * p.nheads * p.d_k);
 
-  AttnSweep s = base(p, pl);  // dq: the state is H^T
-  s.a = d;
-  s.b = v;
-  s.c = k;
-  s.sn = p.d_k;
-  s.sp = 1;
-  s.s_pair = s.s_read = p.scale;
-  s.s_write = 1.f;
-  s.entry = h_in;
-  s.out = p.dq;
-  if ((rc = sweep<false, false>(s, p.d_v, p.d_k, p.bf16, false, p.stream)) != hipSuccess) return rc;
-  s.a = v;  // dk: the state is G^T
-  s.b = d;
-  s.c = q;
-  s.s_read = 1.f;
-  s.s_write = p.scale;
-  s.entry = g_in;
-  s.out = shared ? pk : p.dk;
-  if ((rc = sweep<true, false>(s, p.d_v, p.d_k, p.bf16, shared, p.stream)) != hipSuccess) return rc;
-  s.a = k;  // dv: the state is G
-  s.b = q;
-  s.c = d;
-  s.sn = 1;
-  s.sp = p.d_k;
-  s.exit = p.dh0;
-  s.out = shared ? pv : p.dv;
-  if ((rc = sweep<true, false>(s, p.d_k, p.d_v, p.bf16, shared, p.stream)) != hipSuccess) return rc;
-  if (!shared) return hipSuccess;
-  auto sum = [&](const float* part, void* out, int64_t dim) {
-    const int64_t n4 = p.batch * p.seqlen * p.nheads_kv * dim / 4;
-    const unsigned grid = (unsigned)((n4 + 255) / 256);
-    if (p.bf16)
-      return launch(k_attn_sum_heads<uint16_t>, dim3(grid), dim3(256), 0, p.stream, part, static_cast<uint16_t*>(out),
-                    n4, (int32_t)(dim / 4), rep);
-    return launch(k_attn_sum_heads<float>, dim3(grid), dim3(256), 0, p.stream, part, static_cast<float*>(out), n4,
-                  (int32_t)(dim / 4), rep);
-  };
-  if ((rc = sum(pk, p.dk, p.d_k)) != hipSuccess) return rc;
-  return sum(pv, p.dv, p.d_v);
+  AttnSweep sq = base(p, pl);  // dq: the state is H^T
+  sq.a = d;
+  sq.b = v;
+  sq.c = k;
+  sq.sn = p.d_k;
+  sq.sp = 1;
+  sq.s_pair = sq.s_read = p.scale;
+  sq.s_write = 1.f;
+  sq.entry = p.h0;
+  sq.out = p.dq;
+  AttnSweep sk = sq;  // dk: the state is G^T
+  sk.a = v;
+  sk.b = d;
+  sk.c = q;
+  sk.s_read = 1.f;
+  sk.s_write = p.scale;
+  sk.entry = p.dh_last;
+  sk.out = shared ? pk : p.dk;
+  AttnSweep sv = sk;  // dv: the state is G
+  sv.a = k;
+  sv.b = q;
+  sv.c = d;
+  sv.sn = 1;
+  sv.sp = p.d_k;
+  sv.exit = p.dh0;
+  sv.out = shared ? pv : p.dv;
+  hipError_t rc;
+  if (pl.n_spans > 1) {
+    AttnSweep f = sq, r = sv;
+    f.b = k;
+    f.c = v;
+    rc = span_entries(p, f, r, p.workspace, p.workspace + states);
+    if (rc != hipSuccess) return rc;
+    sq.entry = p.workspace;
+    sk.entry = sv.entry = p.workspace + states;
+  }
+  if (p.bf16) {
+    rc = launch_attn_sweep_grad_bf16(sq, sk, sv, p.d_k, p.d_v, shared, p.stream);
+  } else {
+    rc = sweep_f32<false, false>(sq, p.d_v, p.d_k, p.stream);
+    if (rc == hipSuccess) rc = sweep_f32<true, false>(sk, p.d_v, p.d_k, p.stream);
+    if (rc == hipSuccess) rc = sweep_f32<true, false>(sv, p.d_k, p.d_v, p.stream);
+  }
+  const int64_t heads = p.batch * p.seqlen * p.nheads_kv;
+  if (rc != hipSuccess || !shared || heads == 0) return rc;
+  const HeadSum hk{pk, p.dk, heads * p.d_k / 4, (int32_t)(p.d_k / 4)}, hv{pv, p.dv, heads * p.d_v / 4,
+                                                                          (int32_t)(p.d_v / 4)};
+  const dim3 grid((unsigned)(((hk.n4 > hv.n4 ? hk.n4 : hv.n4) + 255) / 256), 2);
+  if (p.bf16) return launch(k_attn_sum_heads<uint16_t>, grid, dim3(256), 0, p.stream, hk, hv, rep);
+  return launch(k_attn_sum_heads<float>, grid, dim3(256), 0, p.stream, hk, hv, rep);
 }
 
 }  // namespace ssm

@@ -1,14 +1,14 @@
 // The linear attention sweep for bf16 operands, on the bf16 matrix
 // instructions (roles, formulas and the state's recurrence: linear_attn.h).
 //
-// One workgroup (4 waves) per (row, head) and span; wave w owns R = VD / 4 of the
-// VD output columns, for the outputs and for the state S[n][p], which stays in
-// fp32 accumulators.  Per block of 64 steps:
+// One workgroup (4 waves, or 8) per (row, head) and span; wave w owns R = 16 or 32
+// of the VD output columns, for the outputs and for the state S[n][p], which
+// stays in fp32 accumulators.  Per block of 64 steps:
 //   pairs   P[t][i] = decay (a_t . b_i), shared between the waves through LDS
 //   read    out^T = (S^T A^T) diag(s_read decay)      then the state moves on:
 //   update  S = gamma^m S + B^T (w o C)
 //   join    out^T += C^T P^T
-// on R x R tiles (v_mfma_f32_32x32x16_bf16 for VD = 128, 16x16x32 for 64).
+// on R x R tiles (v_mfma_f32_32x32x16_bf16 or 16x16x32_bf16).
 //
 // Precision.  a, b and c meet the matrix cores exactly.  What is formed in
 // between is split: P and the state of `read` into two bf16 values (about 16
@@ -103,13 +103,14 @@ __device__ __forceinline__ void put4(gchar* base, uint32_t off, float a, float b
   }
 }
 
-// Rows of one operand on their way from memory to LDS: 16-byte pieces, 256
+// Rows of one operand on their way from memory to LDS: 16-byte pieces, NT
 // threads, W columns, LDS row stride S.  Rows outside [lo, hi) are zero: the
 // loads take the nearest row inside instead (no branch, so that nothing waits
 // for a load before the rows are put).
-template <int W, int S>
+template <int W, int S, int NT>
 struct Stage {
-  static constexpr int kPerRow = W / 8, kRows = 256 / kPerRow, N = kQ / kRows;
+  static constexpr int kPerRow = W / 8, kRows = NT / kPerRow, N = kQ / kRows;
+  static_assert(N >= 1 && kQ % kRows == 0, "every thread takes whole pieces");
   u32x4 r[N];
   __device__ __forceinline__ void load(const uint16_t* base, int64_t stride, int lo, int hi) {
     const uint32_t sb = (uint32_t)stride * 2;
@@ -134,33 +135,39 @@ struct Stage {
   }
 };
 
-// SUM: only the state of the span from a zero entry (a and out unused).
-template <typename O, int KD, int R, bool REV, bool SUM>
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
-k_attn_sweep_bf16(const AttnSweep s) {
-  constexpr int VD = 4 * R;
+// LDS of a sweep with operands of KD and VD columns (elements).
+constexpr int kSP = kQ + 8;  // row strides: rows read along the contraction 4 (mod 64) dwords apart,
+constexpr int row_stride_a(int kd) { return kd + 8; }
+constexpr int row_stride_t(int w) { return w + 16; }  // rows read through the transpose 8 apart
+constexpr int sum_lds(int kd, int vd) { return kQ * (row_stride_t(kd) + row_stride_t(vd)); }
+constexpr int sweep_lds(int kd, int vd) { return sum_lds(kd, vd) + kQ * (row_stride_a(kd) + 2 * kSP); }
+constexpr int larger(int a, int b) { return a > b ? a : b; }
+
+// One span of one row by NW waves of R columns each.  SUM: only the state of the
+// span from a zero entry (a and out unused).
+template <typename O, int KD, int R, int NW, bool REV, bool SUM>
+__device__ __forceinline__ void sweep_span(const AttnSweep& s, uint16_t* lds, int64_t row, int64_t span) {
+  constexpr int VD = NW * R;
+  constexpr int TH = 64 * NW;
   constexpr int NG = 64 / R;       // lane groups
   constexpr int KC = 8 * NG;       // contraction of one instruction
   constexpr int AR = R * R / 64;   // accumulator registers of a tile
   constexpr int NS = KD * R / 64;  // state registers
   constexpr int TT = kQ / R;       // tiles of steps
   constexpr int KT = kQ / KC;      // contraction slices over the steps
-  // LDS row strides: rows read along the contraction 4 (mod 64) dwords apart,
-  // rows read through the transpose 8 apart.
-  constexpr int SA = KD + 8, SB = KD + 16, SC = VD + 16, SP = kQ + 8;
+  constexpr int SA = row_stride_a(KD), SB = row_stride_t(KD), SC = row_stride_t(VD), SP = kSP;
   typedef Tile<R> M;
   typedef typename M::acc Acc;
-  __shared__ __align__(16) uint16_t sA[SUM ? 8 : kQ * SA];
-  __shared__ __align__(16) uint16_t sB[kQ * SB];
-  __shared__ __align__(16) uint16_t sC[kQ * SC];
-  __shared__ __align__(16) uint16_t sP[2][SUM ? 8 : kQ * SP];  // pairs [t][i], leading and second part
+  uint16_t* const sB = lds;
+  uint16_t* const sC = sB + kQ * SB;
+  uint16_t* const sA = sC + kQ * SC;
+  uint16_t* const sP = sA + kQ * SA;  // pairs [t][i], leading and second part
+  constexpr int kP2 = kQ * SP;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane % R, g = lane / R;
   const int r16 = lane & 15, q4 = lane >> 4;
-  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
-  const int64_t row = id % s.rows, span = id / s.rows;
   const int64_t b = row / s.nheads;
   const int h = (int)(row % s.nheads);
   const int64_t len = row_length(s.lengths, b, s.seqlen);
@@ -202,8 +209,8 @@ k_attn_sweep_bf16(const AttnSweep s) {
   // written: zero once.
   if (!SUM && tid < 2 * kQ) {
     const int t = (REV ? 16 : 0) + 32 * (tid >> 6) + (lane >> 2), i = (REV ? 0 : 16) + 32 * (tid >> 6) + 4 * (lane & 3);
-    *reinterpret_cast<u32x2*>(&sP[0][t * SP + i]) = u32x2{0, 0};
-    *reinterpret_cast<u32x2*>(&sP[1][t * SP + i]) = u32x2{0, 0};
+    *reinterpret_cast<u32x2*>(&sP[t * SP + i]) = u32x2{0, 0};
+    *reinterpret_cast<u32x2*>(&sP[kP2 + t * SP + i]) = u32x2{0, 0};
   }
 
   // Decays that are the same in every block.  A step's weight in the update is
@@ -223,9 +230,9 @@ k_attn_sweep_bf16(const AttnSweep s) {
   const uint32_t ooff = ((uint32_t)r * (uint32_t)(s.nheads * VD) + R * w + 4 * g) * sizeof(O);
   const float g16 = hw_exp2(gl * 16.f);
 
-  Stage<KD, SA> ga;
-  Stage<KD, SB> gb;
-  Stage<VD, SC> gc;
+  Stage<KD, SA, TH> ga;
+  Stage<KD, SB, TH> gb;
+  Stage<VD, SC, TH> gc;
   const int64_t nblk = (e - s0 + kQ - 1) / kQ;
   // Block k: m steps, of which row x is step tb + x.
   auto block = [&](int64_t k, int64_t& tb, int& m) {
@@ -258,7 +265,7 @@ k_attn_sweep_bf16(const AttnSweep s) {
     if (!SUM) {
       // pairs: the ten tiles (rows i of tile it, steps t of tile tt) on or beside
       // the diagonal, dealt to the waves.
-      for (int x = w; x < kQ / 16 * (kQ / 16 + 1) / 2; x += 4) {
+      for (int x = w; x < kQ / 16 * (kQ / 16 + 1) / 2; x += NW) {
         const int big = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, small = x - big * (big + 1) / 2;
         const int it = REV ? big : small, tt = REV ? small : big;
         f32x4 p = {0.f, 0.f, 0.f, 0.f};
@@ -280,11 +287,11 @@ k_attn_sweep_bf16(const AttnSweep s) {
         }
         const int at = (16 * tt + r16) * SP + 16 * it + 4 * q4;
         const uint32_t h0 = peel(v[0], v[1]), h1 = peel(v[2], v[3]);
-        *reinterpret_cast<u32x2*>(&sP[0][at]) = u32x2{h0, h1};
-        *reinterpret_cast<u32x2*>(&sP[1][at]) = u32x2{pack(v[0], v[1]), pack(v[2], v[3])};
+        *reinterpret_cast<u32x2*>(&sP[at]) = u32x2{h0, h1};
+        *reinterpret_cast<u32x2*>(&sP[kP2 + at]) = u32x2{pack(v[0], v[1]), pack(v[2], v[3])};
       }
 
-        __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_sched_barrier(0);
       // read
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt)
@@ -331,7 +338,7 @@ k_attn_sweep_bf16(const AttnSweep s) {
       for (int kt = 0; kt < KT; ++kt) cv[kt] = cat(lds_tr4(p + KC * kt * SC), lds_tr4(p + (KC * kt + 4) * SC));
     }
 
-        __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_sched_barrier(0);
     // update
     const float fac = hw_exp2(gl * (float)m);
 #pragma unroll
@@ -366,12 +373,12 @@ k_attn_sweep_bf16(const AttnSweep s) {
       // join, and out.
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) {
-        const uint16_t* p = &sP[0][(R * tt + r) * SP + 8 * g];
+        const uint16_t* p = &sP[(R * tt + r) * SP + 8 * g];
         const int first = REV ? R * tt / KC : 0, last = REV ? KT : (R * tt + R + KC - 1) / KC;
 #pragma unroll
         for (int kt = first; kt < last; ++kt) {
           o[tt] = M::mma(cv[kt], lds16(p + KC * kt), o[tt]);
-          o[tt] = M::mma(cv[kt], lds16(p + kQ * SP + KC * kt), o[tt]);
+          o[tt] = M::mma(cv[kt], lds16(p + kP2 + KC * kt), o[tt]);
         }
         const int x = R * tt + r;
         if (x >= lo && x < hi) {
@@ -386,7 +393,7 @@ k_attn_sweep_bf16(const AttnSweep s) {
 
   if (!SUM) {
     // Rows behind the sequence's end.
-    for (int64_t t = e + tid / (VD / 4); t < s1; t += 256 / (VD / 4)) {
+    for (int64_t t = e + tid / (VD / 4); t < s1; t += TH / (VD / 4)) {
       O* op = out + t * s.nheads * VD + 4 * (tid % (VD / 4));
 #pragma unroll
       for (int j = 0; j < 4; ++j) io_store(op + j, 0.f);
@@ -410,27 +417,107 @@ k_attn_sweep_bf16(const AttnSweep s) {
   }
 }
 
-template <typename O, bool REV, bool SUM>
-hipError_t by_width(const AttnSweep& s, int64_t kd, int64_t vd, hipStream_t stream) {
-  const unsigned grid = (unsigned)(s.rows * s.n_spans);
-  auto go = [&](auto kern) { return launch(kern, dim3(grid), dim3(256), 0, stream, s); };
-  if (kd == 64)
-    return vd == 64 ? go(k_attn_sweep_bf16<O, 64, 16, REV, SUM>)
-                    : go(k_attn_sweep_bf16<O, 64, 32, REV, SUM>);
-  return vd == 64 ? go(k_attn_sweep_bf16<O, 128, 16, REV, SUM>)
-                  : go(k_attn_sweep_bf16<O, 128, 32, REV, SUM>);
+// A workgroup's part of a launch of `roles` sweeps over the same rows and
+// spans: the sweeps of one row and span are neighbours, so that they find each
+// other's operands in their XCD's L2.
+struct Part {
+  int role;
+  int64_t row, span;
+};
+__device__ __forceinline__ Part part_of(const AttnSweep& s, int roles) {
+  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
+  return Part{(int)(id % roles), id / roles % s.rows, id / roles / s.rows};
+}
+
+template <int KD, int VD, int NW>
+__global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2)))
+k_attn_sweep(const AttnSweep s) {
+  __shared__ __align__(16) uint16_t lds[sweep_lds(KD, VD)];
+  const Part p = part_of(s, 1);
+  sweep_span<uint16_t, KD, VD / NW, NW, false, false>(s, lds, p.row, p.span);
+}
+
+// The spans' own states: of H (role 0) and, in the gradient, of G (role 1).  The
+// last span of a direction has no use for its own.
+template <int KD, int VD>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
+k_attn_span_states(const AttnSweep f, const AttnSweep r, int roles) {
+  __shared__ __align__(16) uint16_t lds[sum_lds(KD, VD)];
+  const Part p = part_of(f, roles);
+  if (p.role == 0) {
+    sweep_span<float, KD, VD / 4, 4, false, true>(f, lds, p.row, p.span);
+  } else {
+    sweep_span<float, KD, VD / 4, 4, true, true>(r, lds, p.row, p.span + 1);
+  }
+}
+
+// dq, dk and dv: three sweeps in one launch.
+template <typename O, int DK, int DV, int NW>
+__global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2)))
+k_attn_sweep_grad(const AttnSweep q, const AttnSweep k, const AttnSweep v) {
+  __shared__ __align__(16) uint16_t lds[larger(sweep_lds(DV, DK), sweep_lds(DK, DV))];
+  const Part p = part_of(q, 3);
+  if (p.role == 0) {
+    sweep_span<uint16_t, DV, DK / NW, NW, false, false>(q, lds, p.row, p.span);
+  } else if (p.role == 1) {
+    sweep_span<O, DV, DK / NW, NW, true, false>(k, lds, p.row, p.span);
+  } else {
+    sweep_span<O, DK, DV / NW, NW, true, false>(v, lds, p.row, p.span);
+  }
+}
+
+// Up to this many workgroups, one a CU: then eight waves of 16 columns each,
+// two a SIMD, instead of four of 32 (operands of 128 columns).
+constexpr int64_t kOneEach = 256;
+
+// Calls f with the widths as constants.
+template <typename F>
+hipError_t by_width(int64_t a, int64_t b, F f) {
+  typedef std::integral_constant<int, 64> W64;
+  typedef std::integral_constant<int, 128> W128;
+  if (a == 64) return b == 64 ? f(W64(), W64()) : f(W64(), W128());
+  return b == 64 ? f(W128(), W64()) : f(W128(), W128());
 }
 
 }  // namespace
 
-hipError_t launch_attn_sweep_bf16(const AttnSweep& s, int64_t kd, int64_t vd, bool rev, bool sum, bool out32,
-                                  hipStream_t stream) {
-  if (sum)
-    return rev ? by_width<float, true, true>(s, kd, vd, stream) : by_width<float, false, true>(s, kd, vd, stream);
-  if (out32)
-    return rev ? by_width<float, true, false>(s, kd, vd, stream) : by_width<float, false, false>(s, kd, vd, stream);
-  return rev ? by_width<uint16_t, true, false>(s, kd, vd, stream)
-             : by_width<uint16_t, false, false>(s, kd, vd, stream);
+hipError_t launch_attn_sweep_bf16(const AttnSweep& s, int64_t kd, int64_t vd, hipStream_t stream) {
+  const int64_t grid = s.rows * s.n_spans;
+  return by_width(kd, vd, [&](auto k, auto v) {
+    constexpr int KD = decltype(k)::value, VD = decltype(v)::value;
+    if constexpr (KD == 128 && VD == 128) {
+      if (grid <= kOneEach)
+        return launch(k_attn_sweep<KD, VD, 8>, dim3((unsigned)grid), dim3(512), 0, stream, s);
+    }
+    return launch(k_attn_sweep<KD, VD, 4>, dim3((unsigned)grid), dim3(256), 0, stream, s);
+  });
+}
+
+hipError_t launch_attn_span_states_bf16(const AttnSweep& f, const AttnSweep* r, int64_t kd, int64_t vd,
+                                        hipStream_t stream) {
+  const int roles = r != nullptr ? 2 : 1;
+  const int64_t grid = f.rows * (f.n_spans - 1) * roles;
+  return by_width(kd, vd, [&](auto k, auto v) {
+    constexpr int KD = decltype(k)::value, VD = decltype(v)::value;
+    return launch(k_attn_span_states<KD, VD>, dim3((unsigned)grid), dim3(256), 0, stream, f, r != nullptr ? *r : f,
+                  roles);
+  });
+}
+
+hipError_t launch_attn_sweep_grad_bf16(const AttnSweep& q, const AttnSweep& k, const AttnSweep& v, int64_t d_k,
+                                       int64_t d_v, bool out32, hipStream_t stream) {
+  const int64_t grid = 3 * q.rows * q.n_spans;
+  return by_width(d_k, d_v, [&](auto a, auto b) {
+    constexpr int DK = decltype(a)::value, DV = decltype(b)::value;
+    auto go = [&](auto kern, int waves) {
+      return launch(kern, dim3((unsigned)grid), dim3(64 * waves), 0, stream, q, k, v);
+    };
+    if constexpr (DK == 128 && DV == 128) {
+      if (grid <= kOneEach)
+        return out32 ? go(k_attn_sweep_grad<float, DK, DV, 8>, 8) : go(k_attn_sweep_grad<uint16_t, DK, DV, 8>, 8);
+    }
+    return out32 ? go(k_attn_sweep_grad<float, DK, DV, 4>, 4) : go(k_attn_sweep_grad<uint16_t, DK, DV, 4>, 4);
+  });
 }
 
 }  // namespace ssm

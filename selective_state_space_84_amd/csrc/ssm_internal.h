@@ -218,7 +218,8 @@ struct LinAttnPlan {
   int64_t span_len;
   int64_t n_spans;
 };
-LinAttnPlan linear_attn_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16);
+LinAttnPlan linear_attn_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16,
+                             bool grad);
 // Floats of workspace; sizes must have been checked for overflow.
 int64_t linear_attn_fwd_floats(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16);
 int64_t linear_attn_bwd_floats(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_kv, int64_t d_k,
