@@ -94,12 +94,14 @@ __device__ __forceinline__ u32x2 lds_tr4(const uint16_t* p) {
 __device__ __forceinline__ u32x4 cat(u32x2 a, u32x2 b) { return u32x4{a[0], a[1], b[0], b[1]}; }
 __device__ __forceinline__ u32x4 lds16(const uint16_t* p) { return *reinterpret_cast<const u32x4*>(p); }
 
-template <typename O>
-__device__ __forceinline__ void put4(gchar* base, uint32_t off, float a, float b, float c, float d) {
-  if constexpr (sizeof(O) == 2) {
-    gstr<u32x2>(base, off, u32x2{pack(a, b), pack(c, d)});
+// Lanes in halves (R = 32) or 16s (R = 16), even ones 2i and odd ones 2i + 1:
+// {a of lane 2i, a of 2i + 1} in even lanes, {b of 2i, b of 2i + 1} in odd ones.
+template <int R>
+__device__ __forceinline__ u32x2 swap_lanes(uint32_t a, uint32_t b) {
+  if constexpr (R == 32) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(a, b, false, false));
   } else {
-    gstr<f32x4>(base, off, f32x4{a, b, c, d});
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a, b, false, false));
   }
 }
 
@@ -227,7 +229,6 @@ __device__ __forceinline__ void sweep_span(const AttnSweep& s, uint16_t* lds, in
   // Pairs of neighbouring 16 x 16 tiles: gamma^|t - i| at j = 3 (j = 0 in
   // reverse), the smallest power of the lane's four (at least 1).
   const float po = hw_exp2(gl * (float)(16 + (REV ? 4 * q4 - r16 : r16 - 4 * q4 - 3))) * s.s_pair;
-  const uint32_t ooff = ((uint32_t)r * (uint32_t)(s.nheads * VD) + R * w + 4 * g) * sizeof(O);
   const float g16 = hw_exp2(gl * 16.f);
 
   Stage<KD, SA, TH> ga;
@@ -240,16 +241,21 @@ __device__ __forceinline__ void sweep_span(const AttnSweep& s, uint16_t* lds, in
     m = (int)min((int64_t)kQ, e - t0);
     tb = REV ? t0 : t0 - (kQ - m);
   };
-  auto fetch = [&](int64_t k) {
+  // Requests rows of block k: a, b or c.
+  auto fetch = [&](int64_t k, int which) {
     int64_t tb;
     int m;
     block(k, tb, m);
     const int lo = REV ? 0 : kQ - m, hi = REV ? m : kQ;
-    if (!SUM) ga.load(A + tb * s.a.stride, s.a.stride, lo, hi);
-    gb.load(B + tb * s.b.stride, s.b.stride, lo, hi);
-    gc.load(C + tb * s.c.stride, s.c.stride, lo, hi);
+    if (!SUM && which == 0) ga.load(A + tb * s.a.stride, s.a.stride, lo, hi);
+    if (which == 1) gb.load(B + tb * s.b.stride, s.b.stride, lo, hi);
+    if (which == 2) gc.load(C + tb * s.c.stride, s.c.stride, lo, hi);
   };
-  if (nblk > 0) fetch(0);
+  if (nblk > 0) {
+    fetch(0, 0);
+    fetch(0, 1);
+    fetch(0, 2);
+  }
   for (int64_t k = 0; k < nblk; ++k) {
     int64_t tb;
     int m;
@@ -259,13 +265,21 @@ __device__ __forceinline__ void sweep_span(const AttnSweep& s, uint16_t* lds, in
     gb.put(sB, lo, hi);
     gc.put(sC, lo, hi);
     __syncthreads();
-    if (k + 1 < nblk) fetch(k + 1);
+    // The next block's rows are requested in two parts, so that the waves do not
+    // stand in line for the memory pipeline (48 KB take it 768 cycles).
+    const bool more = k + 1 < nblk;
+    if (more) fetch(k + 1, 0);
+    if (SUM && more) fetch(k + 1, 1);
+    if (SUM && more) fetch(k + 1, 2);
 
     Acc o[SUM ? 1 : TT];
     if (!SUM) {
       // pairs: the ten tiles (rows i of tile it, steps t of tile tt) on or beside
-      // the diagonal, dealt to the waves.
-      for (int x = w; x < kQ / 16 * (kQ / 16 + 1) / 2; x += NW) {
+      // the diagonal, dealt to the waves; with four waves two at a time, for their
+      // products' sake (with eight the waves of one tile would wait: 256 -> 267 us
+      // on the gradient of 4 x 4096 x 16 x 128).
+      constexpr int kTiles = kQ / 16 * (kQ / 16 + 1) / 2;
+      auto product = [&](int x) {
         const int big = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, small = x - big * (big + 1) / 2;
         const int it = REV ? big : small, tt = REV ? small : big;
         f32x4 p = {0.f, 0.f, 0.f, 0.f};
@@ -273,6 +287,11 @@ __device__ __forceinline__ void sweep_span(const AttnSweep& s, uint16_t* lds, in
         for (int kk = 0; kk < KD / 32; ++kk)
           p = Tile<16>::mma(lds16(&sB[(16 * it + r16) * SB + 32 * kk + 8 * q4]),
                             lds16(&sA[(16 * tt + r16) * SA + 32 * kk + 8 * q4]), p);
+        return p;
+      };
+      auto decayed = [&](int x, const f32x4& p) {
+        const int big = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, small = x - big * (big + 1) / 2;
+        const int it = REV ? big : small, tt = REV ? small : big;
         float v[4];
         if (big == small) {
 #pragma unroll
@@ -289,8 +308,18 @@ __device__ __forceinline__ void sweep_span(const AttnSweep& s, uint16_t* lds, in
         const uint32_t h0 = peel(v[0], v[1]), h1 = peel(v[2], v[3]);
         *reinterpret_cast<u32x2*>(&sP[at]) = u32x2{h0, h1};
         *reinterpret_cast<u32x2*>(&sP[kP2 + at]) = u32x2{pack(v[0], v[1]), pack(v[2], v[3])};
+      };
+      if constexpr (NW == 4) {
+        const f32x4 p0 = product(w), p1 = product(w + 4);
+        decayed(w, p0);
+        decayed(w + 4, p1);
+        if (w < kTiles - 8) decayed(w + 8, product(w + 8));
+      } else {
+        for (int x = w; x < kTiles; x += NW) decayed(x, product(x));
       }
 
+      if (more) fetch(k + 1, 1);
+      if (more) fetch(k + 1, 2);
       __builtin_amdgcn_sched_barrier(0);
       // read
 #pragma unroll
@@ -370,7 +399,7 @@ __device__ __forceinline__ void sweep_span(const AttnSweep& s, uint16_t* lds, in
     __syncthreads();  // P complete; a, b and c no longer read
 
     if (!SUM) {
-      // join, and out.
+      // join
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) {
         const uint16_t* p = &sP[(R * tt + r) * SP + 8 * g];
@@ -380,12 +409,35 @@ __device__ __forceinline__ void sweep_span(const AttnSweep& s, uint16_t* lds, in
           o[tt] = M::mma(cv[kt], lds16(p + KC * kt), o[tt]);
           o[tt] = M::mma(cv[kt], lds16(p + kP2 + KC * kt), o[tt]);
         }
-        const int x = R * tt + r;
-        if (x >= lo && x < hi) {
-          gchar* op = uniform_ptr(out + (tb + R * tt) * s.nheads * VD);
+      }
+      // out.  bf16 outputs change lanes first, so that each stores 16 bytes of a row:
+      // with R = 32 between the halves of the wave (one takes the first, the other
+      // the second of two runs of 8 columns), with R = 16 between neighbouring 16
+      // lanes (one takes the first, the other the second of two tiles).
+      gchar* const ob = uniform_ptr(out + tb * s.nheads * VD);
+      const uint32_t orow = (uint32_t)(s.nheads * VD) * sizeof(O), ocol = R * w * sizeof(O);
+      if constexpr (sizeof(O) == 2) {
+        constexpr int NP = TT * AR / 8;  // 16-byte pieces of a lane
 #pragma unroll
-          for (int q = 0; q < AR / 4; ++q)
-            put4<O>(op, ooff + 4 * NG * q * sizeof(O), o[tt][4 * q], o[tt][4 * q + 1], o[tt][4 * q + 2], o[tt][4 * q + 3]);
+        for (int i = 0; i < NP; ++i) {
+          const int t0 = R == 32 ? i / 2 : 2 * i, t1 = R == 32 ? t0 : t0 + 1;  // tiles and registers
+          const int f0 = R == 32 ? 8 * (i % 2) : 0, f1 = R == 32 ? f0 + 4 : 0;
+          const u32x2 a = swap_lanes<R>(pack(o[t0][f0], o[t0][f0 + 1]), pack(o[t1][f1], o[t1][f1 + 1]));
+          const u32x2 c = swap_lanes<R>(pack(o[t0][f0 + 2], o[t0][f0 + 3]), pack(o[t1][f1 + 2], o[t1][f1 + 3]));
+          const int x = R * (R == 32 ? t0 : t0 + (g & 1)) + r;
+          const int col = R == 32 ? 8 * (2 * (i % 2) + g) : 8 * (g >> 1);
+          if (x >= lo && x < hi) gstr<u32x4>(ob, (uint32_t)x * orow + ocol + 2 * col, u32x4{a[0], c[0], a[1], c[1]});
+        }
+      } else {
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) {
+          const int x = R * tt + r;
+          if (x >= lo && x < hi) {
+#pragma unroll
+            for (int q = 0; q < AR / 4; ++q)
+              gstr<f32x4>(ob, (uint32_t)x * orow + ocol + (4 * NG * q + 4 * g) * 4,
+                          f32x4{o[tt][4 * q], o[tt][4 * q + 1], o[tt][4 * q + 2], o[tt][4 * q + 3]});
+          }
         }
       }
     }
