@@ -354,28 +354,27 @@ def ssm_conv1d_update(state, x_t, w, bias=None, *, y_t=None, silu=True, stream=N
 
 
 def _rows(t, what: str) -> Tuple[Optional[int], int]:
-    """(pointer, elements between steps) of a tensor (..., heads, width) whose
-    leading axes form evenly spaced rows of dense (heads, width) blocks: a
-    dense tensor, or a column range of a wider one."""
+    """(pointer, elements between steps) of a tensor (rows, heads, width) or
+    (batch, steps, heads, width) whose steps are evenly spaced dense (heads,
+    width) blocks: a dense tensor, or a column range of a wider one."""
     if not t.is_cuda:
         raise ValueError("tensor must live on the GPU")
-    heads, width = t.shape[-2:]
+    shape = t.shape
+    heads, width = shape[-2:]
+    dense = heads * width
     if t.is_contiguous():
-        return t.data_ptr() or None, heads * width
-    *lead, s_head, s_elem = t.stride()
-    ok = (width <= 1 or s_elem == 1) and (heads <= 1 or s_head == width)
-    step = None
-    expect = None  # stride of the next axis to the left
-    for n, s in zip(reversed(t.shape[:-2]), reversed(lead)):
-        if n != 1:
-            if step is None:
-                step = s
-            elif s != expect:
-                ok = False
-            expect = s * n
-    if t.numel() > 0 and (not ok or (step is not None and step < heads * width)):
+        return t.data_ptr() or None, dense
+    st = t.stride()
+    ok = (st[-1] == 1 or width <= 1) and (st[-2] == width or heads <= 1)
+    if len(shape) == 3:
+        step = st[0] if shape[0] > 1 else dense
+    else:
+        batch, steps = shape[:2]
+        step = st[1] if steps > 1 else (st[0] if batch > 1 else dense)
+        ok = ok and len(shape) == 4 and (batch <= 1 or st[0] == step * steps)
+    if not ok or step < dense:
         raise ValueError("%s must hold dense (heads, width) blocks at one step apart" % what)
-    return t.data_ptr() or None, (heads * width if step is None else step)
+    return t.data_ptr() or None, step
 
 
 _no_scope = contextlib.nullcontext()
@@ -544,19 +543,25 @@ def ssm_linear_attn_update(h, q, k, v, log_decay, *, slots=None, scale=None, o=N
     the batch in order.
     """
     import torch
-    nheads, nheads_kv, d_k, d_v = _attn_shapes(q, k, v, 1)
-    batch, n_slots = q.shape[0], h.shape[0]
-    dt = _io_dtype(q)
-    f32 = torch.float32
-    _want(h, (n_slots, nheads, d_v, d_k), f32, "h")
-    _want(log_decay, (nheads,), f32, "log_decay")
-    if slots is not None:
+    f32, qt = torch.float32, q.dtype
+    batch, nheads, d_k = q.shape
+    n_slots, nheads_kv, d_v = h.shape[0], v.shape[1], v.shape[-1]
+    # One comparison for the usual case; the checks one by one name what is wrong.
+    if not (k.shape == (batch, nheads_kv, d_k) and v.shape == (batch, nheads_kv, d_v) and
+            h.shape == (n_slots, nheads, d_v, d_k) and log_decay.shape == (nheads,) and k.dtype is qt and
+            v.dtype is qt and h.dtype is f32 and log_decay.dtype is f32 and
+            (slots is None or (slots.shape == (batch,) and slots.dtype is torch.int32)) and
+            (o is None or (o.shape == (batch, nheads, d_v) and o.dtype is qt))):
+        _attn_shapes(q, k, v, 1)
+        _want(h, (n_slots, nheads, d_v, d_k), f32, "h")
+        _want(log_decay, (nheads,), f32, "log_decay")
         _want(slots, (batch,), torch.int32, "slots")
-    if o is not None:
-        _want(o, (batch, nheads, d_v), q.dtype, "o")
+        _want(o, (batch, nheads, d_v), qt, "o")
+        raise ValueError("arguments do not fit together")
+    dt = _io_dtype(q)
     with _scope(stream, q, h, slots, k, v, log_decay, o):
         if o is None:
-            o = torch.empty((batch, nheads, d_v), dtype=q.dtype, device=q.device)
+            o = torch.empty((batch, nheads, d_v), dtype=qt, device=q.device)
         (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
         rc = load_library().ssm_linear_attn_update(
             _dense(h, "h"), _dense(slots, "slots"), qp, kp, vp, _dense(log_decay, "log_decay"), _dense(o, "o"), batch,

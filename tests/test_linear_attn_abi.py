@@ -188,3 +188,33 @@ def test_binding_refuses_rows_that_share_memory():
             bd._rows(Fake(bad), "x")
     with pytest.raises(ValueError):
         bd.ssm_linear_attn_fwd(x, x, x, torch.zeros(4))  # on the CPU
+
+
+def test_binding_refuses_shapes_that_do_not_fit():
+    """Shapes and types are compared before anything is read (tensors on the CPU suffice)."""
+    torch = pytest.importorskip("torch")
+    z = torch.zeros
+    i32 = torch.int32
+
+    def upd(q=z(2, 4, 64), k=z(2, 2, 64), v=z(2, 2, 128), h=z(3, 4, 128, 64), g=z(4), slots=z(2, dtype=i32), o=None):
+        return bd.ssm_linear_attn_update(h, q, k, v, g, slots=slots, o=o)
+    for a in (dict(k=z(2, 2, 32)), dict(v=z(1, 2, 128)), dict(h=z(3, 4, 64, 128)), dict(g=z(2)), dict(slots=z(3, dtype=i32)),
+              dict(slots=z(2, dtype=torch.int64)), dict(o=z(2, 4, 64)), dict(k=z(2, 2, 64, dtype=torch.bfloat16)),
+              dict(h=z(3, 4, 128, 64, dtype=torch.bfloat16)), dict()):
+        with pytest.raises(ValueError):  # the last one: on the CPU
+            upd(**a)
+    q, k, v = z(1, 5, 4, 64), z(1, 5, 2, 64), z(1, 5, 2, 64)
+    for a in (dict(lengths=z(2, dtype=i32)), dict(lengths=z(1, dtype=torch.int64)), dict(h0=z(1, 4, 64, 32)),
+              dict(o=z(1, 5, 2, 64)), dict(h_last=z(1, 4, 64, 64, dtype=torch.float64))):
+        with pytest.raises(ValueError):
+            bd.ssm_linear_attn_fwd(q, k, v, z(4), **a)
+    with pytest.raises(ValueError):
+        bd.ssm_linear_attn_fwd(q, k[:, :4], v, z(4))
+    with pytest.raises(ValueError):
+        bd.ssm_linear_attn_bwd(q, k, v, z(4), do=z(1, 5, 2, 64))
+    with pytest.raises(ValueError):
+        bd.ssm_qk_norm_rope_fwd(q, k, z(32), z(64), z(32))
+    with pytest.raises(ValueError):
+        bd.ssm_qk_norm_rope_fwd(q, k, positions=z(1, 5))
+    with pytest.raises(ValueError):
+        bd.ssm_qk_norm_rope_bwd(q, k, dq_out=q)
