@@ -47,7 +47,7 @@ struct AttnSweep {
   void* out;               // [batch][seqlen][nheads][VD]
   int64_t sn, sp;          // state element (n, p) at n sn + p sp
   int64_t seqlen, span_len, n_spans;
-  int32_t nheads, slices;  // slices of the VD columns, one workgroup each (fp32 sweep)
+  int32_t nheads;
   int64_t rows;            // batch * nheads
   float s_pair, s_read, s_write;
 };
@@ -60,6 +60,15 @@ hipError_t launch_attn_span_states_bf16(const AttnSweep& f, const AttnSweep* r, 
                                         hipStream_t stream);
 hipError_t launch_attn_sweep_grad_bf16(const AttnSweep& q, const AttnSweep& k, const AttnSweep& v, int64_t d_k,
                                        int64_t d_v, bool out32, hipStream_t stream);
+
+// Calls f with the widths (64 or 128) as constants.
+template <typename F>
+hipError_t by_width(int64_t a, int64_t b, F f) {
+  typedef std::integral_constant<int, 64> W64;
+  typedef std::integral_constant<int, 128> W128;
+  if (a == 64) return b == 64 ? f(W64(), W64()) : f(W64(), W128());
+  return b == 64 ? f(W128(), W64()) : f(W128(), W128());
+}
 
 // log2(gamma); -inf is kept finite so that 0 steps of decay give 1 (0 * -inf
 // would be NaN) and one step or more still gives 0.

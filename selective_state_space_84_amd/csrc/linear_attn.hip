@@ -37,28 +37,29 @@ __device__ __forceinline__ void store4(uint16_t* p, const f32x4& v) {
   *reinterpret_cast<u16x4*>(p) = r;
 }
 
-// SUM: only the state of the span from a zero entry (a and out unused).
-template <int KD, bool REV, bool SUM>
-__global__ void __launch_bounds__(256) k_attn_sweep_f32(const AttnSweep s) {
+// LDS of a sweep with operands of KD columns (floats).
+constexpr int sum_lds(int kd) { return kT * (kd + 4 + kSc); }
+constexpr int sweep_lds(int kd) { return sum_lds(kd) + kT * (kd + 4 + kSp); }
+constexpr int larger(int a, int b) { return a > b ? a : b; }
+
+// One slice of one span of one row.  VD: all output columns.  SUM: only the state
+// of the span from a zero entry (a and out unused).
+template <int KD, int VD, bool REV, bool SUM>
+__device__ __forceinline__ void sweep_span_f32(const AttnSweep& s, float* lds, int64_t row, int64_t span, int slice) {
   constexpr int kSa = KD + 4;
   constexpr int NT = KD / 16;          // state tiles
   constexpr int PA = kT * KD / 4 / 256;  // 4-element pieces of a and b per thread
   constexpr int PC = kT * kCols / 4 / 256;
-  __shared__ __align__(16) float sA[SUM ? 1 : kT * kSa];
-  __shared__ __align__(16) float sB[kT * kSa];
-  __shared__ __align__(16) float sC[kT * kSc];
-  __shared__ __align__(16) float sP[SUM ? 1 : kT * kSp];  // decayed pairs [t][i]
+  float* const sB = lds;
+  float* const sC = sB + kT * kSa;
+  float* const sA = sC + kT * kSc;
+  float* const sP = sA + kT * kSa;  // decayed pairs [t][i]
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, q4 = lane >> 4;
-  int64_t id = xcd_remap(blockIdx.x, gridDim.x);
-  const int slice = (int)(id % s.slices);
-  id /= s.slices;
-  const int64_t row = id % s.rows, span = id / s.rows + (SUM && REV ? 1 : 0);
   const int64_t b = row / s.nheads;
   const int h = (int)(row % s.nheads);
-  const int64_t VD = (int64_t)s.slices * kCols;
   const int col0 = slice * kCols;
   const int64_t len = row_length(s.lengths, b, s.seqlen);
   const int64_t s0 = span * s.span_len;
@@ -86,17 +87,17 @@ __global__ void __launch_bounds__(256) k_attn_sweep_f32(const AttnSweep s) {
   f32x4 ra[SUM ? 1 : PA], rb[PA], rc[PC];
   auto fetch = [&](int64_t t0) {
     const int m = (int)min((int64_t)kT, e - t0);
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int r = 0; r < PA; ++r) {
       const int piece = tid + 256 * r, t = piece / (KD / 4), n = piece % (KD / 4) * 4;
-      const f32x4 z = {0.f, 0.f, 0.f, 0.f};
-      if (!SUM) ra[r] = t < m ? load4(A + (t0 + t) * s.a.stride + n) : z;
-      rb[r] = t < m ? load4(B + (t0 + t) * s.b.stride + n) : z;
+      if (!SUM) ra[r] = t < m ? load4(A + (t0 + t) * s.a.stride + n) : zero;
+      rb[r] = t < m ? load4(B + (t0 + t) * s.b.stride + n) : zero;
     }
 #pragma unroll
     for (int r = 0; r < PC; ++r) {
       const int piece = tid + 256 * r, t = piece / (kCols / 4), p = piece % (kCols / 4) * 4;
-      rc[r] = t < m ? load4(C + (t0 + t) * s.c.stride + p) : f32x4{0.f, 0.f, 0.f, 0.f};
+      rc[r] = t < m ? load4(C + (t0 + t) * s.c.stride + p) : zero;
     }
   };
 
@@ -215,6 +216,47 @@ __global__ void __launch_bounds__(256) k_attn_sweep_f32(const AttnSweep s) {
   }
 }
 
+// The forward sweep; the spans' own states (role 0: of H, role 1: of G); and the
+// three gradient sweeps in one launch.  Slices and roles of one row and span are
+// neighbours, and find each other's operands in their XCD's L2.
+template <int KD, int VD>
+__global__ void __launch_bounds__(256) k_attn_sweep_f32(const AttnSweep s) {
+  __shared__ __align__(16) float lds[sweep_lds(KD)];
+  constexpr int N = VD / kCols;
+  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
+  sweep_span_f32<KD, VD, false, false>(s, lds, id / N % s.rows, id / N / s.rows, (int)(id % N));
+}
+
+template <int KD, int VD>
+__global__ void __launch_bounds__(256) k_attn_span_states_f32(const AttnSweep f, const AttnSweep r, int roles) {
+  __shared__ __align__(16) float lds[sum_lds(KD)];
+  const int n = VD / kCols * roles;
+  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
+  const int64_t row = id / n % f.rows, span = id / n / f.rows;
+  const int part = (int)(id % n), slice = part % (VD / kCols);
+  if (part < VD / kCols) {
+    sweep_span_f32<KD, VD, false, true>(f, lds, row, span, slice);
+  } else {
+    sweep_span_f32<KD, VD, true, true>(r, lds, row, span + 1, slice);
+  }
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(256) k_attn_sweep_grad_f32(const AttnSweep q, const AttnSweep k, const AttnSweep v) {
+  __shared__ __align__(16) float lds[larger(sweep_lds(DK), sweep_lds(DV))];
+  constexpr int NK = DK / kCols, N = 2 * NK + DV / kCols;
+  const int64_t id = xcd_remap(blockIdx.x, gridDim.x);
+  const int64_t row = id / N % q.rows, span = id / N / q.rows;
+  const int part = (int)(id % N);
+  if (part < NK) {
+    sweep_span_f32<DV, DK, false, false>(q, lds, row, span, part);
+  } else if (part < 2 * NK) {
+    sweep_span_f32<DV, DK, true, false>(k, lds, row, span, part - NK);
+  } else {
+    sweep_span_f32<DK, DV, true, false>(v, lds, row, span, part - 2 * NK);
+  }
+}
+
 // ---- carries between spans ----------------------------------------------
 // In place: st[span][row][...] holds every span's state from a zero entry (but
 // the last one's) and receives the state that enters the span: E_0 = start,
@@ -287,12 +329,30 @@ __global__ void __launch_bounds__(256) k_attn_sum_heads(const HeadSum k, const H
 
 int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
 
-template <bool REV, bool SUM>
-hipError_t sweep_f32(AttnSweep s, int64_t kd, int64_t vd, hipStream_t stream) {
-  s.slices = (int32_t)(vd / kCols);
-  const unsigned grid = (unsigned)(s.rows * (s.n_spans - (SUM ? 1 : 0)) * s.slices);
-  if (kd == 64) return launch(k_attn_sweep_f32<64, REV, SUM>, dim3(grid), dim3(256), 0, stream, s);
-  return launch(k_attn_sweep_f32<128, REV, SUM>, dim3(grid), dim3(256), 0, stream, s);
+hipError_t launch_attn_sweep_f32(const AttnSweep& s, int64_t kd, int64_t vd, hipStream_t stream) {
+  const unsigned grid = (unsigned)(s.rows * s.n_spans * (vd / kCols));
+  return by_width(kd, vd, [&](auto k, auto v) {
+    return launch(k_attn_sweep_f32<decltype(k)::value, decltype(v)::value>, dim3(grid), dim3(256), 0, stream, s);
+  });
+}
+
+hipError_t launch_attn_span_states_f32(const AttnSweep& f, const AttnSweep* r, int64_t kd, int64_t vd,
+                                       hipStream_t stream) {
+  const int roles = r != nullptr ? 2 : 1;
+  const unsigned grid = (unsigned)(f.rows * (f.n_spans - 1) * (vd / kCols) * roles);
+  return by_width(kd, vd, [&](auto k, auto v) {
+    return launch(k_attn_span_states_f32<decltype(k)::value, decltype(v)::value>, dim3(grid), dim3(256), 0, stream, f,
+                  r != nullptr ? *r : f, roles);
+  });
+}
+
+hipError_t launch_attn_sweep_grad_f32(const AttnSweep& q, const AttnSweep& k, const AttnSweep& v, int64_t d_k,
+                                      int64_t d_v, hipStream_t stream) {
+  const unsigned grid = (unsigned)(q.rows * q.n_spans * ((2 * d_k + d_v) / kCols));
+  return by_width(d_k, d_v, [&](auto a, auto b) {
+    return launch(k_attn_sweep_grad_f32<decltype(a)::value, decltype(b)::value>, dim3(grid), dim3(256), 0, stream, q,
+                  k, v);
+  });
 }
 
 // The states that enter the spans, of H from h0 into hs and (gs not NULL) of G
@@ -302,13 +362,9 @@ hipError_t span_entries(const LinAttnLaunch& p, AttnSweep f, AttnSweep r, float*
   f.sp = r.sp = p.d_k;
   f.exit = hs;
   r.exit = gs;
-  hipError_t rc;
-  if (p.bf16) {
-    rc = launch_attn_span_states_bf16(f, gs != nullptr ? &r : nullptr, p.d_k, p.d_v, p.stream);
-  } else {
-    rc = sweep_f32<false, true>(f, p.d_k, p.d_v, p.stream);
-    if (rc == hipSuccess && gs != nullptr) rc = sweep_f32<true, true>(r, p.d_k, p.d_v, p.stream);
-  }
+  const AttnSweep* const rev = gs != nullptr ? &r : nullptr;
+  const hipError_t rc = p.bf16 ? launch_attn_span_states_bf16(f, rev, p.d_k, p.d_v, p.stream)
+                               : launch_attn_span_states_f32(f, rev, p.d_k, p.d_v, p.stream);
   if (rc != hipSuccess) return rc;
   const int64_t state4 = p.d_k * p.d_v / 4;
   const unsigned grid = (unsigned)((f.rows * state4 + 255) / 256);
@@ -353,8 +409,9 @@ static LinAttnPlan make_plan(int64_t groups, int64_t seqlen) {
 
 LinAttnPlan linear_attn_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16,
                              bool grad) {
-  // Workgroups of a launch per span: the three gradient sweeps share one in bf16.
-  const int64_t each = bf16 ? (grad ? 3 : 1) : (d_k > d_v ? d_k : d_v) / kCols;
+  // Workgroups of a launch per span: the three gradient sweeps share one, and the
+  // fp32 sweep has one for every 64 columns.
+  const int64_t each = bf16 ? (grad ? 3 : 1) : (grad ? 2 * d_k + d_v : d_v) / kCols;
   return make_plan(batch * nheads * each, seqlen);
 }
 
@@ -393,7 +450,7 @@ hipError_t launch_linear_attn_fwd(const LinAttnLaunch& p) {
   s.exit = p.h_last;
   s.out = p.o;
   return p.bf16 ? launch_attn_sweep_bf16(s, p.d_k, p.d_v, p.stream)
-                : sweep_f32<false, false>(s, p.d_k, p.d_v, p.stream);
+                : launch_attn_sweep_f32(s, p.d_k, p.d_v, p.stream);
 }
 
 hipError_t launch_linear_attn_bwd(const LinAttnLaunch& p) {
@@ -442,13 +499,8 @@ hipError_t launch_linear_attn_bwd(const LinAttnLaunch& p) {
     sq.entry = p.workspace;
     sk.entry = sv.entry = p.workspace + states;
   }
-  if (p.bf16) {
-    rc = launch_attn_sweep_grad_bf16(sq, sk, sv, p.d_k, p.d_v, shared, p.stream);
-  } else {
-    rc = sweep_f32<false, false>(sq, p.d_v, p.d_k, p.stream);
-    if (rc == hipSuccess) rc = sweep_f32<true, false>(sk, p.d_v, p.d_k, p.stream);
-    if (rc == hipSuccess) rc = sweep_f32<true, false>(sv, p.d_k, p.d_v, p.stream);
-  }
+  rc = p.bf16 ? launch_attn_sweep_grad_bf16(sq, sk, sv, p.d_k, p.d_v, shared, p.stream)
+              : launch_attn_sweep_grad_f32(sq, sk, sv, p.d_k, p.d_v, p.stream);
   const int64_t heads = p.batch * p.seqlen * p.nheads_kv;
   if (rc != hipSuccess || !shared || heads == 0) return rc;
   const HeadSum hk{pk, p.dk, heads * p.d_k / 4, (int32_t)(p.d_k / 4)}, hv{pv, p.dv, heads * p.d_v / 4,

@@ -522,15 +522,6 @@ k_attn_sweep_grad(const AttnSweep q, const AttnSweep k, const AttnSweep v) {
 // two a SIMD, instead of four of 32 (operands of 128 columns).
 constexpr int64_t kOneEach = 256;
 
-// Calls f with the widths as constants.
-template <typename F>
-hipError_t by_width(int64_t a, int64_t b, F f) {
-  typedef std::integral_constant<int, 64> W64;
-  typedef std::integral_constant<int, 128> W128;
-  if (a == 64) return b == 64 ? f(W64(), W64()) : f(W64(), W128());
-  return b == 64 ? f(W128(), W64()) : f(W128(), W128());
-}
-
 }  // namespace
 
 hipError_t launch_attn_sweep_bf16(const AttnSweep& s, int64_t kd, int64_t vd, hipStream_t stream) {
