@@ -386,19 +386,27 @@ AttnSweep base(const LinAttnLaunch& p, const LinAttnPlan& pl) {
 
 }  // namespace
 
-// When the (row, head) pairs are few, the sequence is cut into spans of at least
-// kMinSpan steps, at the price of a summary sweep that reads b and c once more:
-// as many as make two workgroups a CU (512 in all).  Two spans do not pay: a CU
-// takes two blocks of different workgroups together in ~1.6 times the time of
-// one, and the summary costs 0.4 of a sweep (8 x 2048 steps x 32 heads of 128,
-// 256 pairs: 157 us whole, 202 us in two spans; 1 x 32768 x 32: 417 us in 16
-// spans, 472 us in 8, 440 us in 32).
+// When the (row, head) pairs are few, the sequence is cut into spans, at the
+// price of a pass over b and c for the spans' states: as many spans as make two
+// workgroups a CU (512 in all), or one a CU where they would be shorter than
+// kShortSpan steps; kMaxSpans at most (the carry walks them one after the other),
+// of at least kMinSpan steps.  Two spans do not pay: a CU takes
+// two blocks of different workgroups together in ~1.6 times the time of one, and
+// the states cost 0.4 of a sweep.  Measured (bf16, heads of 128): 8 x 2048 steps x
+// 32 heads 157 us whole, 202 us in two spans; 1 x 32768 x 32 402 us in 16 spans,
+// 433 us in 8, 440 us in 32; 1 x 4096 x 16 50 us in 16 spans, 58 us in 32; 1 x 1000
+// x 4 27 us in spans of 64, 30 us of 128, 46 us of 256, 64 us of 512; 1 x 8000 x 1
+// 38 us in 63 spans, 50 us in 125.
 constexpr int64_t kTargetGroups = 512;
-constexpr int64_t kMinSpan = 128;
+constexpr int64_t kMinSpan = 64;
+constexpr int64_t kShortSpan = 256;
+constexpr int64_t kMaxSpans = 64;
 constexpr int64_t kSpanStep = 64;  // spans start on block boundaries of both sweeps
 
 static LinAttnPlan make_plan(int64_t groups, int64_t seqlen) {
   int64_t n = groups > 0 ? kTargetGroups / groups : 1;
+  if (groups > 0 && n > seqlen / kShortSpan) n = kTargetGroups / 2 / groups;
+  if (n > kMaxSpans) n = kMaxSpans;
   if (n > seqlen / kMinSpan) n = seqlen / kMinSpan;
   if (n < 3) n = 1;
   int64_t len = (seqlen + n - 1) / n;
