@@ -6,7 +6,9 @@
 // Gradient: g = R(p)^T dy,  dw = sum g x r,
 //           dx = r (w g) - x r^3 mean(w g x).
 //
-// Bound by HBM: x is read once and y written once.  A head belongs to G lanes
+// Bound by HBM: x is read once and y written once (8192 steps x 64 heads of 128
+// in bf16: 54-57 us, 4.7-5.0 TB/s; gradient of 16384 steps x 32 heads: 94-96
+// us, 4.2 TB/s, two workgroups a CU by its registers; a copy reaches 5.1 TB/s).  A head belongs to G lanes
 // (the next power of two of headdim / 8), 8 values a lane; the mean closes with
 // log2(G) adds across lanes, and the pairs of the half-split rotation come from
 // the lane rot_dim / 16 away.  A workgroup takes all heads of one or a few
