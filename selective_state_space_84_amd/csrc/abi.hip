@@ -2,6 +2,7 @@
 // dispatch to the gfx950 kernels.  Every check runs on the host before any
 // HIP call, so a rejected call has no side effects.
 #include "ssm_scan.h"
+#include "attn_launch.h"
 #include "ssm_internal.h"
 
 #include <hip/hip_runtime.h>

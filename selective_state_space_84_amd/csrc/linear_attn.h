@@ -24,7 +24,7 @@
 #pragma once
 
 #include "ssm_device.h"
-#include "ssm_internal.h"
+#include "attn_launch.h"
 
 namespace ssm {
 

@@ -18,7 +18,7 @@
 // fraction of a turn before they are rounded to fp32 (an fp32 product at
 // position 10^6 would be off by 0.06 radians).
 #include "ssm_device.h"
-#include "ssm_internal.h"
+#include "attn_launch.h"
 
 namespace ssm {
 namespace {
