@@ -7,8 +7,8 @@
 //           dx = r (w g) - x r^3 mean(w g x).
 //
 // Bound by HBM: x is read once and y written once (8192 steps x 64 heads of 128
-// in bf16: 54-57 us, 4.7-5.0 TB/s; gradient of 16384 steps x 32 heads: 94-96
-// us, 4.2 TB/s, two workgroups a CU by its registers; a copy reaches 5.1 TB/s).  A head belongs to G lanes
+// in bf16: 54-57 us, 4.7-5.0 TB/s; gradient of 16384 steps x 32 heads: 91.5
+// us, 4.4 TB/s, two workgroups a CU by its registers; a copy reaches 5.1 TB/s).  A head belongs to G lanes
 // (the next power of two of headdim / 8), 8 values a lane; the mean closes with
 // log2(G) adds across lanes, and the pairs of the half-split rotation come from
 // the lane rot_dim / 16 away.  A workgroup takes all heads of one or a few
@@ -401,7 +401,10 @@ void set_steps(QkArgs& a, int64_t left) {
 }
 
 constexpr int64_t kFwdGroups = 2048;
-constexpr int64_t kBwdGroups = 1024;  // workgroups (and partial sums) of the gradient
+// Workgroups (and partial sums) of the gradient: the two a CU that its registers
+// allow (16384 steps x 32 heads of 128 in bf16: 91.5 us; 95 us with 1024, 103 us
+// with 2048).
+constexpr int64_t kBwdGroups = 512;
 
 QkArgs args(const QkNormRopeLaunch& p, bool grad) {
   QkArgs a{};
