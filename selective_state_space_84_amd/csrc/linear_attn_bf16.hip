@@ -532,7 +532,11 @@ k_attn_sweep_grad(const AttnSweep q, const AttnSweep k, const AttnSweep v) {
 }
 
 // Up to this many workgroups, one a CU: then eight waves of 16 columns each,
-// two a SIMD, instead of four of 32 (operands of 128 columns).
+// two a SIMD, instead of four of 32 (operands of 128 columns).  Measured, eight
+// against four waves, 1000 steps, heads of 128: 64 (row, head) pairs (256
+// workgroups) 47 against 49 us, 256 pairs 75 against 81, 320 pairs 137 against
+// 116, 512 pairs 159 against 141; gradient of 4 x 4096 x 16 257 against 289, of 7
+// x 1000 x 16 heads (336 workgroups) 129 against 101.
 constexpr int64_t kOneEach = 256;
 
 }  // namespace

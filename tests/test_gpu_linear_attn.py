@@ -380,3 +380,66 @@ def test_graph_capture(lib):
         for a, b in zip(outs, want):
             assert torch.equal(a, b)
         assert torch.equal(h, hw)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,M", [(70000, 1, 1), (1, 32768, 8)])
+def test_many_rows_and_heads(lib, B, H, M, dtype):
+    """More rows than a 16-bit grid axis, and the most heads: prompt of two steps, gradient of v, one token."""
+    import torch
+    from selective_state_space_84_amd import binding
+    print("case", B, H, M, dtype, flush=True)
+    r = np.random.default_rng(21)
+    q, k, v = (_t(r.standard_normal((B, 2, h, 64)), dtype) for h in (H, M, M))
+    dec = _t(-r.random(H))
+    rep = H // M
+    nq, nk, nv = _np(q), np.repeat(_np(k), rep, 2), np.repeat(_np(v), rep, 2)
+    g = np.exp(_np(dec))[None, :, None]
+
+    def pairs(f):  # scale * (q_1 . k_i), i = 0 (decayed) and 1, with f applied to the factors
+        return [64 ** -0.5 * (f(nq[:, 1]) * f(nk[:, i])).sum(-1, keepdims=True) * (g if i == 0 else 1) for i in (0, 1)]
+    a, m = pairs(lambda x: x), pairs(np.abs)
+    ref, mag = (p[0] * f(nv[:, 0]) + p[1] * f(nv[:, 1]) for p, f in ((a, lambda x: x), (m, np.abs)))
+    o, none = binding.ssm_linear_attn_fwd(q, k, v, dec, want_h_last=False)
+    assert none is None
+    _close("o", _np(o[:, 1]), ref, P.attn_tol(ref, mag, 2, 64, dtype))
+    # dv of the last step is its own pair's weight times do, summed over the heads that share v.
+    do = torch.zeros_like(o)
+    do[:, 1] = 1
+    gr = binding.ssm_linear_attn_bwd(q, k, v, dec, do=do, want_dh0=False)
+    dv, dm = (p[1].reshape(B, M, rep, 1).sum(2) * np.ones(64) for p in (a, m))
+    _close("dv", _np(gr["dv"][:, 1]), dv, P.attn_tol(dv, dm, 2, 64, dtype, rep))
+    h = torch.zeros(B, H, 64, 64, device=DEV)
+    binding.ssm_linear_attn_update(h, q[:, 0].contiguous(), k[:, 0].contiguous(), v[:, 0].contiguous(), dec)
+    u = binding.ssm_linear_attn_update(h, q[:, 1].contiguous(), k[:, 1].contiguous(), v[:, 1].contiguous(), dec)
+    _close("u", _np(u), ref, P.attn_tol(ref, mag, 2, 64, dtype))
+
+
+def test_two_at_once(lib):
+    """Calls in flight on two streams, each with its own workspace, and outputs given by the caller."""
+    import torch
+    from selective_state_space_84_amd import binding
+    sets = [_make(22 + i, 1, 2500, 2, 1, 128, 128, "bf16") for i in range(2)]
+    want = []
+    for d, _, do, dh in sets:
+        want.append((binding.ssm_linear_attn_fwd(**d), binding.ssm_linear_attn_bwd(**d, do=do, dh_last=dh)))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    given = [torch.empty_like(d["q"], memory_format=torch.contiguous_format) for d, _, _, _ in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, (d, _, do, dh) in enumerate(sets):
+            got[i].append((binding.ssm_linear_attn_fwd(**d, stream=streams[i]),
+                           binding.ssm_linear_attn_bwd(**d, do=do, dh_last=dh, stream=streams[i],
+                                                       grads={"dq": given[i]})))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for f, g in got[i]:
+            assert g["dq"] is given[i]
+            assert torch.equal(f[0], want[i][0][0]) and torch.equal(f[1], want[i][0][1])
+            assert all(torch.equal(g[name], want[i][1][name]) for name in g)
+    # 0 is the default stream's handle.
+    d = sets[0][0]
+    o, _ = binding.ssm_linear_attn_fwd(**d, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0][0][0])
