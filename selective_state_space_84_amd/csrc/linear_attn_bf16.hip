@@ -33,7 +33,7 @@
 //     worked on.
 //
 // Measured, one MI355X (a copy reaches 5.1 TB/s): 1 x 32768 steps x 32 heads of
-// 128 in 16 spans: 407-418 us (1.07 GB, 2.6 TB/s), a third of it the spans'
+// 128 in 16 spans: 403-418 us (1.07 GB, 2.6 TB/s), a third of it the spans'
 // states; gradient of 4 x 4096 x 16 heads of 128: 257-260 us.  No one resource is
 // full: counted over the long sweep the matrix units are busy 38% of the time, a
 // SIMD issues 53k vector instructions in its 524k cycles (4 to 5 cycles each,
