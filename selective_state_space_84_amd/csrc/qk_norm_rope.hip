@@ -470,7 +470,8 @@ hipError_t launch_qk_norm_rope(const QkNormRopeLaunch& p) {
 
 hipError_t launch_qk_norm_rope_bwd(const QkNormRopeLaunch& p) {
   QkArgs a = args(p, true);
-  int64_t groups = groups_of(a);
+  // Without heads there is no gradient to form (inv_freq may be NULL then): dw alone, a sum over nothing.
+  int64_t groups = p.nheads + p.nheads_k > 0 ? groups_of(a) : 0;
   if (groups > kBwdGroups) groups = kBwdGroups;
   const bool want = p.dwq != nullptr || p.dwk != nullptr;
   a.part = want ? p.workspace : nullptr;
