@@ -426,7 +426,9 @@ int ssm_conv1d_update(float* state, const void* x_t, const float* w, const float
  *                below the dense ones and at most 2^23 elements.
  *   log_decay  : [nheads] fp32, log(gamma); 0 keeps everything, -inf keeps
  *                only the current step.  A constant of the layer: it has no
- *                gradient.  Positive values grow the state without bound.
+ *                gradient.  Positive values grow the state: results follow the
+ *                formula while gamma to the power of the row's steps is an fp32
+ *                number, and are unspecified beyond.
  *   lengths    : [batch] int32 or NULL.  Row b has lengths[b] steps (clamped to
  *                [0, seqlen] on the device); what q, k and v hold behind them
  *                is not used, o is zero there, and h_last is the state after

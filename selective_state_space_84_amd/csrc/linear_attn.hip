@@ -141,7 +141,9 @@ __device__ __forceinline__ void sweep_span_f32(const AttnSweep& s, float* lds, i
       for (int j = 0; j < 4; ++j) {
         const int i = 16 * it + 4 * q4 + j;
         const int d = REV ? i - t : t - i;
-        sc[j] = d >= 0 ? sc[j] * (hw_exp2(g * (float)d) * s.s_pair) : 0.f;
+        // In reverse rows without a step come last: their zeros would meet powers beyond the block's steps
+        // (infinite where gamma is above 1).
+        sc[j] = d >= 0 && (!REV || i < m) ? sc[j] * (hw_exp2(g * (float)d) * s.s_pair) : 0.f;
       }
       *reinterpret_cast<f32x4*>(&sP[t * kSp + 16 * it + 4 * q4]) = sc;
       __syncthreads();

@@ -100,6 +100,10 @@ __device__ __forceinline__ float uniform_f32(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
 }
 
+// Rows of a block without a step hold zeros, but may meet powers of gamma beyond the block's steps.  These are kept
+// finite, and multiplied to the row's value one after the other, so that they leave zeros.
+__device__ __forceinline__ float finite(float w) { return __builtin_amdgcn_fmed3f(w, -__FLT_MAX__, __FLT_MAX__); }
+
 __device__ __forceinline__ u32x2 lds_tr4(const uint16_t* p) {
   return __builtin_bit_cast(u32x2,
                             __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(s16x4*)const_cast<uint16_t*>(p)));
@@ -236,7 +240,7 @@ __device__ __forceinline__ void sweep_span(const AttnSweep& s, uint16_t* lds, in
   const float wg = hw_exp2(gl * (float)(REV ? 8 * g : 8 * (NG - 1 - g))) * s.s_write;
   float wj[8], wk[KT];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) wj[j] = uniform_f32(hw_exp2(gl * (float)(REV ? j + 1 : 7 - j)));
+  for (int j = 0; j < 8; ++j) wj[j] = uniform_f32(finite(hw_exp2(gl * (float)(REV ? j + 1 : 7 - j))));
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt) wk[kt] = uniform_f32(hw_exp2(gl * (float)(REV ? KC * kt : KC * (KT - 1 - kt))));
   // Pairs of neighbouring 16 x 16 tiles: gamma^|t - i| at j = 3 (j = 0 in
@@ -310,12 +314,12 @@ __device__ __forceinline__ void sweep_span(const AttnSweep& s, uint16_t* lds, in
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int d = REV ? 4 * q4 + j - r16 : r16 - 4 * q4 - j;
-            v[j] = d >= 0 ? p[j] * (hw_exp2(gl * (float)d) * s.s_pair) : 0.f;
+            v[j] = d >= 0 ? p[j] * finite(hw_exp2(gl * (float)d)) * s.s_pair : 0.f;
           }
         } else {
-          const float f = po * (big - small == 1 ? 1.f : (big - small == 2 ? g16 : g16 * g16));
+          const float f = finite(po * (big - small == 1 ? 1.f : (big - small == 2 ? g16 : g16 * g16)));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = p[j] * (f * (REV ? (j == 0 ? 1.f : wj[j - 1]) : wj[4 + j]));
+          for (int j = 0; j < 4; ++j) v[j] = p[j] * f * (REV ? (j == 0 ? 1.f : wj[j - 1]) : wj[4 + j]);
         }
         const int at = (16 * tt + r16) * SP + 16 * it + 4 * q4;
         const uint32_t h0 = peel(v[0], v[1]), h1 = peel(v[2], v[3]);
@@ -388,12 +392,11 @@ __device__ __forceinline__ void sweep_span(const AttnSweep& s, uint16_t* lds, in
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
       u32x4 w0, w1, w2;
-      float wl = wg * wk[kt];
-      asm volatile("" : "+v"(wl));  // keeps wl * wj[] from being held in 8 KT registers
+      const float wl = finite(wg * wk[kt]);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        float v0 = lo_f32(cv[kt][q]) * (wl * wj[2 * q]);
-        float v1 = hi_f32(cv[kt][q]) * (wl * wj[2 * q + 1]);
+        float v0 = lo_f32(cv[kt][q]) * wl * wj[2 * q];
+        float v1 = hi_f32(cv[kt][q]) * wl * wj[2 * q + 1];
         w0[q] = peel(v0, v1);
         w1[q] = peel(v0, v1);
         w2[q] = pack(v0, v1);

@@ -1,0 +1,22 @@
+"""Linear attention: decays, sizes and launch shapes beside those of
+test_gpu_linear_attn.py, elementwise within the same bounds of the 64-bit
+definitions (plain64.py)."""
+import pytest
+
+from test_gpu_linear_attn import _check_bwd, _check_fwd, _make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("decay,L,lengths", [(1.5, 1, None), (1.5, 3, None), (1.5, 33, None), (5.0, 1, None),
+                                             (5.0, 3, None), (5.0, 16, None), (1.2, 64, None), (1.2, 65, None),
+                                             (0.05, 300, None), (5.0, 80, [1, 16]), (1.5, 80, [0, 33])])
+def test_growing_states(lib, decay, L, lengths, dtype):
+    """gamma above 1: only powers up to the row's steps count, all of them in fp32's range here; higher ones, of rows of
+    a block that have no step, leave it (1.5 * 63, 5 * 31)."""
+    print("case", decay, L, lengths, dtype, flush=True)
+    d, n, do, dh = _make(L, 2, L, 2, 1, 64, 128, dtype, decay=[decay, decay / 2])
+    for scale in (None, -0.25):
+        _check_fwd(d, n, dtype, lengths, scale)
+        _check_bwd(d, n, do, dh, dtype, lengths, scale)
