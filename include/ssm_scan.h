@@ -450,7 +450,7 @@ int ssm_conv1d_update(float* state, const void* x_t, const float* w, const float
  * reach the outputs of steps that share its block of 64.
  * Sums are taken in a fixed order: results are bitwise reproducible for a
  * given device, sizes and strides.  Same conventions, validation and error
- * codes as the scan; nheads above 32768: SSM_ERR_BAD_DIM.
+ * codes as the scan; nheads or nheads_kv above 32768: SSM_ERR_BAD_DIM.
  */
 int ssm_linear_attn_fwd(const void* q, const void* k, const void* v, const float* log_decay, const int32_t* lengths,
                         const float* h0, void* o, float* h_last, int64_t batch, int64_t seqlen, int64_t nheads,

@@ -601,11 +601,12 @@ constexpr int64_t kMaxElems = (int64_t)1 << 48;
 int check_linear_attn_dims(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_kv, int64_t d_k, int64_t d_v,
                            int32_t io_dtype) {
   if (batch < 0 || seqlen < 0 || nheads < 0 || nheads_kv <= 0 || d_k <= 0 || d_v <= 0) return SSM_ERR_BAD_DIM;
-  if (seqlen > kMaxSeqlen || nheads > kMaxHeads) return SSM_ERR_BAD_DIM;
+  if (seqlen > kMaxSeqlen || nheads > kMaxHeads || nheads_kv > kMaxHeads) return SSM_ERR_BAD_DIM;
   if (io_dtype != SSM_DTYPE_F32 && io_dtype != SSM_DTYPE_BF16) return SSM_ERR_UNSUPPORTED;
   if ((d_k != 64 && d_k != 128) || (d_v != 64 && d_v != 128) || nheads % nheads_kv != 0) return SSM_ERR_UNSUPPORTED;
   int64_t n, st;
-  if (!mul3(batch, seqlen, nheads * 128, &n) || !mul3(batch, nheads, d_k * d_v, &st)) return SSM_ERR_BAD_DIM;
+  const int64_t heads = nheads > 0 ? nheads : nheads_kv;  // k and v have steps where there are no query heads too
+  if (!mul3(batch, seqlen, heads * 128, &n) || !mul3(batch, heads, d_k * d_v, &st)) return SSM_ERR_BAD_DIM;
   if (n > kMaxElems || st > kMaxElems) return SSM_ERR_BAD_DIM;
   // Spans are only cut where pairs are few, so 6 workgroups a pair bound the grids.
   if (batch * nheads * 6 > INT32_MAX || st / 1024 + 1 > INT32_MAX || n / 1024 + 1 > INT32_MAX)
@@ -664,7 +665,8 @@ int linear_attn_impl(ssm::LinAttnLaunch p, int32_t io_dtype, bool grad, size_t w
 int linear_attn_update_impl(ssm::LinAttnUpdateLaunch p, int32_t io_dtype) {
   if (p.batch < 0 || p.n_slots < 0 || p.nheads < 0 || p.nheads_kv <= 0 || p.d_k <= 0 || p.d_v <= 0)
     return SSM_ERR_BAD_DIM;
-  if (p.nheads > kMaxHeads || p.batch > kMaxSeqlen || p.n_slots > kMaxSeqlen) return SSM_ERR_BAD_DIM;
+  if (p.nheads > kMaxHeads || p.nheads_kv > kMaxHeads || p.batch > kMaxSeqlen || p.n_slots > kMaxSeqlen)
+    return SSM_ERR_BAD_DIM;
   if (p.slots == nullptr && p.n_slots != p.batch) return SSM_ERR_BAD_DIM;
   if (io_dtype != SSM_DTYPE_F32 && io_dtype != SSM_DTYPE_BF16) return SSM_ERR_UNSUPPORTED;
   if ((p.d_k != 64 && p.d_k != 128) || (p.d_v != 64 && p.d_v != 128) || p.nheads % p.nheads_kv != 0)
