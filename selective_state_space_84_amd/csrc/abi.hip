@@ -630,8 +630,9 @@ int linear_attn_impl(ssm::LinAttnLaunch p, int32_t io_dtype, bool grad, size_t w
   if (n > 0 && (p.q == nullptr || p.k == nullptr || p.v == nullptr)) return SSM_ERR_NULL_ARG;
   if (p.nheads > 0 && p.batch > 0 && p.log_decay == nullptr) return SSM_ERR_NULL_ARG;
   if (n > 0 && !grad && p.o == nullptr) return SSM_ERR_NULL_ARG;
-  if (n > 0 && grad && (p.d_o == nullptr || p.dq == nullptr || p.dk == nullptr || p.dv == nullptr))
-    return SSM_ERR_NULL_ARG;
+  if (n > 0 && grad && (p.d_o == nullptr || p.dq == nullptr)) return SSM_ERR_NULL_ARG;
+  // Without query heads dk and dv are zeros, and still outputs.
+  if (tokens > 0 && grad && (p.dk == nullptr || p.dv == nullptr)) return SSM_ERR_NULL_ARG;
 
   const void* a16[] = {p.q, p.k, p.v, p.o, p.h0, p.h_last, p.d_o, p.dh_last, p.dq, p.dk, p.dv, p.dh0};
   for (const void* q : a16)
@@ -657,7 +658,7 @@ int linear_attn_impl(ssm::LinAttnLaunch p, int32_t io_dtype, bool grad, size_t w
     if ((rc = check_alias(&ws, 1, ins, 8)) != SSM_OK || (rc = check_alias(&ws, 1, outs, 6)) != SSM_OK) return rc;
     if (overlap(ws, dense(p.h0, b_h))) return SSM_ERR_ALIAS;
   }
-  if (p.batch == 0 || p.nheads == 0) return SSM_OK;
+  if (p.batch == 0 || (p.nheads == 0 && (!grad || tokens == 0))) return SSM_OK;
   const hipError_t err = grad ? ssm::launch_linear_attn_bwd(p) : ssm::launch_linear_attn_fwd(p);
   return err == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }

@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(256) k_attn_carry(const AttnCarry f, const Att
 }
 
 // ---- sums over the heads that share a key/value head --------------------
-// blockIdx.y: dk or dv; part holds [step][nheads][4 d4] fp32.
+// blockIdx.y: dk or dv; part holds [step][nheads][4 d4] fp32 (and is not read without query heads: rep 0, zeros).
 struct HeadSum {
   const float* part;
   void* out;
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(256) k_attn_sum_heads(const HeadSum k, const H
   if (i >= s.n4) return;
   const int64_t head = i / s.d4;
   const f32x4* p = reinterpret_cast<const f32x4*>(s.part) + head * rep * s.d4 + i % s.d4;
-  f32x4 x = p[0];
+  f32x4 x = rep > 0 ? p[0] : f32x4{0.f, 0.f, 0.f, 0.f};
   for (int r = 1; r < rep; ++r) x += p[(int64_t)r * s.d4];
   store4(static_cast<T*>(s.out) + i * 4, x);
 }
@@ -512,8 +512,10 @@ hipError_t launch_linear_attn_bwd(const LinAttnLaunch& p) {
     sq.entry = p.workspace;
     sk.entry = sv.entry = p.workspace + states;
   }
-  rc = p.bf16 ? launch_attn_sweep_grad_bf16(sq, sk, sv, p.d_k, p.d_v, shared, p.stream)
-              : launch_attn_sweep_grad_f32(sq, sk, sv, p.d_k, p.d_v, p.stream);
+  rc = hipSuccess;
+  if (p.nheads > 0)
+    rc = p.bf16 ? launch_attn_sweep_grad_bf16(sq, sk, sv, p.d_k, p.d_v, shared, p.stream)
+                : launch_attn_sweep_grad_f32(sq, sk, sv, p.d_k, p.d_v, p.stream);
   const int64_t heads = p.batch * p.seqlen * p.nheads_kv;
   if (rc != hipSuccess || !shared || heads == 0) return rc;
   const HeadSum hk{pk, p.dk, heads * p.d_k / 4, (int32_t)(p.d_k / 4)}, hv{pv, p.dv, heads * p.d_v / 4,

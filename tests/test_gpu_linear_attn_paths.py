@@ -3,7 +3,7 @@ test_gpu_linear_attn.py, elementwise within the same bounds of the 64-bit
 definitions (plain64.py)."""
 import pytest
 
-from test_gpu_linear_attn import _check_bwd, _check_fwd, _make
+from test_gpu_linear_attn import DEV, _check_bwd, _check_fwd, _make
 
 pytestmark = pytest.mark.gpu
 
@@ -20,3 +20,17 @@ def test_growing_states(lib, decay, L, lengths, dtype):
     for scale in (None, -0.25):
         _check_fwd(d, n, dtype, lengths, scale)
         _check_bwd(d, n, do, dh, dtype, lengths, scale)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradient_without_query_heads(lib, dtype):
+    """dk and dv are sums over no heads: zeros, written over what the buffers held."""
+    import torch
+    from selective_state_space_84_amd import binding
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q, k, v = (torch.ones(2, 70, h, 64, dtype=t, device=DEV) for h in (0, 3, 3))
+    grads = {n: torch.full_like(x, float("nan")) for n, x in (("dk", k), ("dv", v))}
+    g = binding.ssm_linear_attn_bwd(q, k, v, torch.zeros(0, device=DEV), do=q, grads=grads)
+    torch.cuda.synchronize()
+    assert g["dq"].shape == q.shape and g["dh0"].shape == (2, 0, 64, 64)
+    assert not g["dk"].any() and not g["dv"].any()

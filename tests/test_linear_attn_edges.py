@@ -29,3 +29,10 @@ def test_counts_without_heads_stay_in_range(lib):
         assert _attn(lib, 1 << 30, 1 << 30, 0, 1 << 15, grad) == bd.SSM_ERR_BAD_DIM
     assert lib.ssm_linear_attn_update(*[None] * 7, 2, 2, 0, 1 << 60, 64, 64, 0, 0, 0, 0.125, 1, None) == \
         bd.SSM_ERR_BAD_DIM
+
+
+def test_gradient_of_shared_heads_without_query_heads_needs_outputs(lib):
+    """dk and dv of no query heads are zeros, which somebody has to write."""
+    assert _attn(lib, 2, 10, 0, 2, grad=True) == bd.SSM_ERR_NULL_ARG
+    assert _attn(lib, 2, 0, 0, 2, grad=True) == bd.SSM_OK
+    assert _attn(lib, 2, 10, 0, 2) == bd.SSM_OK
