@@ -450,7 +450,9 @@ int ssm_conv1d_update(float* state, const void* x_t, const float* w, const float
  * reach the outputs of steps that share its block of 64.
  * Sums are taken in a fixed order: results are bitwise reproducible for a
  * given device, sizes and strides.  Same conventions, validation and error
- * codes as the scan; nheads or nheads_kv above 32768: SSM_ERR_BAD_DIM.
+ * codes as the scan; nheads or nheads_kv above 32768: SSM_ERR_BAD_DIM, and so
+ * are more workgroups than a launch holds (2^24 - 1: one per row and head with
+ * SSM_DTYPE_BF16, one per row, head and 64 columns of o with SSM_DTYPE_F32).
  */
 int ssm_linear_attn_fwd(const void* q, const void* k, const void* v, const float* log_decay, const int32_t* lengths,
                         const float* h0, void* o, float* h_last, int64_t batch, int64_t seqlen, int64_t nheads,
@@ -479,7 +481,9 @@ size_t ssm_linear_attn_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t
  *             is NULL), or NULL.
  *   workspace : ssm_linear_attn_bwd_workspace_size() bytes, 256-byte aligned.
  * Outputs are overwritten and must not overlap each other, any input or the
- * workspace.
+ * workspace.  A launch has three workgroups per row and head (SSM_DTYPE_F32:
+ * one for every 64 columns of dq, dk and dv); with shared heads the elements of
+ * dk and of dv stay below 2^34.
  */
 int ssm_linear_attn_bwd(const void* q, const void* k, const void* v, const float* log_decay, const int32_t* lengths,
                         const float* h0, const void* d_o, const float* dh_last, void* dq, void* dk, void* dv,
@@ -505,7 +509,7 @@ size_t ssm_linear_attn_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t
  *             [batch][nheads_kv][d_v] io_dtype, rows q_stride, k_stride, v_stride
  *             elements apart (0: dense); alignment as for ssm_linear_attn_fwd.
  *   o       : [batch][nheads][d_v] io_dtype, dense; overlaps nothing.
- *   d_k, d_v: 64 or 128 each.
+ *   d_k, d_v: 64 or 128 each; batch * nheads * d_k * d_v / 2048 below 2^24.
  * Equivalent to ssm_linear_attn_fwd with seqlen 1 and h0 = h_last = h[slots].
  */
 int ssm_linear_attn_update(float* h, const int32_t* slots, const void* q, const void* k, const void* v,
@@ -538,6 +542,8 @@ int ssm_linear_attn_update(float* h, const int32_t* slots, const void* q, const 
  *                anything else.
  *   headdim    : a multiple of 16 up to 256; rot_dim a multiple of 16 up to
  *                headdim; eps >= 0.
+ * More steps than the workgroups of a launch take (2^24 - 1, of a step at
+ * least): SSM_ERR_BAD_DIM.
  */
 int ssm_qk_norm_rope_fwd(const void* q, const void* k, const float* wq, const float* wk, const float* inv_freq,
                          const int64_t* positions, void* q_out, void* k_out, int64_t batch, int64_t seqlen,

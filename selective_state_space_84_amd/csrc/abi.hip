@@ -594,12 +594,14 @@ int check_stride(int64_t* stride, int64_t width, int64_t rows, int64_t es) {
 }
 
 constexpr int64_t kMaxHeads = 1 << 15;
+// Workgroups of 256 threads in a launch: an axis of the grid holds fewer than 2^32 threads.
+constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;
 // Every byte count and grid below stays far inside 64 (and 32) bits when no
 // tensor has more elements than this.
 constexpr int64_t kMaxElems = (int64_t)1 << 48;
 
 int check_linear_attn_dims(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_kv, int64_t d_k, int64_t d_v,
-                           int32_t io_dtype) {
+                           int32_t io_dtype, bool grad) {
   if (batch < 0 || seqlen < 0 || nheads < 0 || nheads_kv <= 0 || d_k <= 0 || d_v <= 0) return SSM_ERR_BAD_DIM;
   if (seqlen > kMaxSeqlen || nheads > kMaxHeads || nheads_kv > kMaxHeads) return SSM_ERR_BAD_DIM;
   if (io_dtype != SSM_DTYPE_F32 && io_dtype != SSM_DTYPE_BF16) return SSM_ERR_UNSUPPORTED;
@@ -608,15 +610,18 @@ int check_linear_attn_dims(int64_t batch, int64_t seqlen, int64_t nheads, int64_
   const int64_t heads = nheads > 0 ? nheads : nheads_kv;  // k and v have steps where there are no query heads too
   if (!mul3(batch, seqlen, heads * 128, &n) || !mul3(batch, heads, d_k * d_v, &st)) return SSM_ERR_BAD_DIM;
   if (n > kMaxElems || st > kMaxElems) return SSM_ERR_BAD_DIM;
-  // Spans are only cut where pairs are few, so 6 workgroups a pair bound the grids.
-  if (batch * nheads * 6 > INT32_MAX || st / 1024 + 1 > INT32_MAX || n / 1024 + 1 > INT32_MAX)
+  // Spans are only cut where pairs are few (kTargetGroups workgroups at most), so a span's workgroups bound the grids.
+  if (ssm::linear_attn_groups(batch, nheads, d_k, d_v, io_dtype == SSM_DTYPE_BF16, grad) > kMaxGroups)
+    return SSM_ERR_BAD_DIM;
+  if (grad && nheads != nheads_kv &&
+      ssm::linear_attn_sum_threads(batch, seqlen, nheads_kv, d_k, d_v) > kMaxGroups * 256)
     return SSM_ERR_BAD_DIM;
   return SSM_OK;
 }
 
 // Forward (d_o NULL and grad false) and gradient share their checks.
 int linear_attn_impl(ssm::LinAttnLaunch p, int32_t io_dtype, bool grad, size_t workspace_bytes) {
-  int rc = check_linear_attn_dims(p.batch, p.seqlen, p.nheads, p.nheads_kv, p.d_k, p.d_v, io_dtype);
+  int rc = check_linear_attn_dims(p.batch, p.seqlen, p.nheads, p.nheads_kv, p.d_k, p.d_v, io_dtype, grad);
   if (rc != SSM_OK) return rc;
   p.bf16 = io_dtype == SSM_DTYPE_BF16;
   const int64_t es = p.bf16 ? 2 : 4;
@@ -672,6 +677,7 @@ int linear_attn_update_impl(ssm::LinAttnUpdateLaunch p, int32_t io_dtype) {
   if (io_dtype != SSM_DTYPE_F32 && io_dtype != SSM_DTYPE_BF16) return SSM_ERR_UNSUPPORTED;
   if ((p.d_k != 64 && p.d_k != 128) || (p.d_v != 64 && p.d_v != 128) || p.nheads % p.nheads_kv != 0)
     return SSM_ERR_UNSUPPORTED;
+  if (ssm::linear_attn_update_blocks(p.batch, p.nheads, p.d_k, p.d_v) > kMaxGroups) return SSM_ERR_BAD_DIM;
   p.bf16 = io_dtype == SSM_DTYPE_BF16;
   const int64_t es = p.bf16 ? 2 : 4;
   const int64_t wq = p.nheads * p.d_k, wk = p.nheads_kv * p.d_k, wv = p.nheads_kv * p.d_v, wo = p.nheads * p.d_v;
@@ -693,7 +699,6 @@ int linear_attn_update_impl(ssm::LinAttnUpdateLaunch p, int32_t io_dtype) {
   const Rows outs[] = {dense(p.h, p.n_slots * p.nheads * p.d_k * p.d_v * 4), dense(p.o, p.batch * wo * es)};
   if ((rc = check_alias(outs, 2, ins, 5)) != SSM_OK) return rc;
   if (n == 0) return SSM_OK;
-  if (ssm::linear_attn_update_blocks(p.batch, p.nheads, p.d_k, p.d_v) > INT32_MAX) return SSM_ERR_BAD_DIM;
   return ssm::launch_linear_attn_update(p) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
@@ -716,6 +721,7 @@ int qk_norm_rope_impl(ssm::QkNormRopeLaunch p, int32_t io_dtype, int32_t interle
   if (p.rot_dim < 0 || p.rot_dim > p.headdim || p.rot_dim % 16 != 0) return SSM_ERR_UNSUPPORTED;
   if (!(p.eps >= 0.f) || (interleaved != 0 && interleaved != 1)) return SSM_ERR_UNSUPPORTED;
   p.bf16 = io_dtype == SSM_DTYPE_BF16;
+  if (!grad && p.nheads + p.nheads_k > 0 && ssm::qk_norm_rope_groups(p) > kMaxGroups) return SSM_ERR_BAD_DIM;
   p.interleaved = interleaved == 1;
   const int64_t es = p.bf16 ? 2 : 4, tokens = p.batch * p.seqlen;
   const int64_t wq = p.nheads * p.headdim, wk = p.nheads_k * p.headdim;
@@ -793,7 +799,7 @@ int ssm_linear_attn_fwd(const void* q, const void* k, const void* v, const float
 
 size_t ssm_linear_attn_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v,
                                           int32_t io_dtype) {
-  if (check_linear_attn_dims(batch, seqlen, nheads, 1, d_k, d_v, io_dtype) != SSM_OK) return (size_t)-1;
+  if (check_linear_attn_dims(batch, seqlen, nheads, 1, d_k, d_v, io_dtype, false) != SSM_OK) return (size_t)-1;
   return (size_t)ssm::linear_attn_fwd_floats(batch, seqlen, nheads, d_k, d_v, io_dtype == SSM_DTYPE_BF16) * 4;
 }
 
@@ -832,7 +838,7 @@ int ssm_linear_attn_bwd(const void* q, const void* k, const void* v, const float
 
 size_t ssm_linear_attn_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_kv,
                                           int64_t d_k, int64_t d_v, int32_t io_dtype) {
-  if (check_linear_attn_dims(batch, seqlen, nheads, nheads_kv, d_k, d_v, io_dtype) != SSM_OK) return (size_t)-1;
+  if (check_linear_attn_dims(batch, seqlen, nheads, nheads_kv, d_k, d_v, io_dtype, true) != SSM_OK) return (size_t)-1;
   return (size_t)ssm::linear_attn_bwd_floats(batch, seqlen, nheads, nheads_kv, d_k, d_v,
                                              io_dtype == SSM_DTYPE_BF16) * 4;
 }

@@ -39,6 +39,9 @@ struct LinAttnPlan {
 };
 LinAttnPlan linear_attn_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16,
                              bool grad);
+// Workgroups of the widest launch for every span, and threads of the sum over shared heads (0: none).
+int64_t linear_attn_groups(int64_t batch, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16, bool grad);
+int64_t linear_attn_sum_threads(int64_t batch, int64_t seqlen, int64_t nheads_kv, int64_t d_k, int64_t d_v);
 // Floats of workspace; sizes must have been checked for overflow.
 int64_t linear_attn_fwd_floats(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16);
 int64_t linear_attn_bwd_floats(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_kv, int64_t d_k,
@@ -87,6 +90,7 @@ struct QkNormRopeLaunch {
   float* workspace;
 };
 int64_t qk_norm_rope_bwd_floats(int64_t tokens, int64_t headdim);
+int64_t qk_norm_rope_groups(const QkNormRopeLaunch& p);  // workgroups of the forward launch
 hipError_t launch_qk_norm_rope(const QkNormRopeLaunch& p);
 hipError_t launch_qk_norm_rope_bwd(const QkNormRopeLaunch& p);
 

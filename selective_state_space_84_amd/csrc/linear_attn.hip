@@ -420,12 +420,19 @@ static LinAttnPlan make_plan(int64_t groups, int64_t seqlen) {
   return LinAttnPlan{len, seqlen > 0 ? (seqlen + len - 1) / len : 1};
 }
 
+// The three gradient sweeps share a launch, and the fp32 sweep has a workgroup for
+// every 64 columns.
+int64_t linear_attn_groups(int64_t batch, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16, bool grad) {
+  return batch * nheads * (bf16 ? (grad ? 3 : 1) : (grad ? 2 * d_k + d_v : d_v) / kCols);
+}
+
+int64_t linear_attn_sum_threads(int64_t batch, int64_t seqlen, int64_t nheads_kv, int64_t d_k, int64_t d_v) {
+  return (batch * seqlen * nheads_kv * (d_k > d_v ? d_k : d_v) / 4 + 255) / 256 * 256;
+}
+
 LinAttnPlan linear_attn_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16,
                              bool grad) {
-  // Workgroups of a launch per span: the three gradient sweeps share one, and the
-  // fp32 sweep has one for every 64 columns.
-  const int64_t each = bf16 ? (grad ? 3 : 1) : (grad ? 2 * d_k + d_v : d_v) / kCols;
-  return make_plan(batch * nheads * each, seqlen);
+  return make_plan(linear_attn_groups(batch, nheads, d_k, d_v, bf16, grad), seqlen);
 }
 
 static int64_t span_floats(int64_t batch, int64_t nheads, int64_t d_k, int64_t d_v, const LinAttnPlan& pl) {
@@ -520,7 +527,8 @@ hipError_t launch_linear_attn_bwd(const LinAttnLaunch& p) {
   if (rc != hipSuccess || !shared || heads == 0) return rc;
   const HeadSum hk{pk, p.dk, heads * p.d_k / 4, (int32_t)(p.d_k / 4)}, hv{pv, p.dv, heads * p.d_v / 4,
                                                                           (int32_t)(p.d_v / 4)};
-  const dim3 grid((unsigned)(((hk.n4 > hv.n4 ? hk.n4 : hv.n4) + 255) / 256), 2);
+  const int64_t threads = linear_attn_sum_threads(p.batch, p.seqlen, p.nheads_kv, p.d_k, p.d_v);
+  const dim3 grid((unsigned)(threads / 256), 2);
   if (p.bf16) return launch(k_attn_sum_heads<uint16_t>, grid, dim3(256), 0, p.stream, hk, hv, rep);
   return launch(k_attn_sum_heads<float>, grid, dim3(256), 0, p.stream, hk, hv, rep);
 }

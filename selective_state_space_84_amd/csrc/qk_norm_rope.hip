@@ -457,6 +457,8 @@ int64_t qk_norm_rope_bwd_floats(int64_t tokens, int64_t headdim) {
   return 2 * (tokens < kBwdGroups ? tokens : kBwdGroups) * headdim;
 }
 
+int64_t qk_norm_rope_groups(const QkNormRopeLaunch& p) { return groups_of(args(p, false)); }
+
 hipError_t launch_qk_norm_rope(const QkNormRopeLaunch& p) {
   const QkArgs a = args(p, false);
   const unsigned grid = (unsigned)groups_of(a);

@@ -1,9 +1,11 @@
 """Linear attention: decays, sizes and launch shapes beside those of
 test_gpu_linear_attn.py, elementwise within the same bounds of the 64-bit
 definitions (plain64.py)."""
+import numpy as np
 import pytest
 
-from test_gpu_linear_attn import DEV, _check_bwd, _check_fwd, _make
+import plain64 as P
+from test_gpu_linear_attn import DEV, _check_bwd, _check_fwd, _close, _make, _np
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +36,36 @@ def test_gradient_without_query_heads(lib, dtype):
     torch.cuda.synchronize()
     assert g["dq"].shape == q.shape and g["dh0"].shape == (2, 0, 64, 64)
     assert not g["dk"].any() and not g["dv"].any()
+
+
+def test_largest_launches(lib):
+    """As many workgroups as an axis of a grid holds: one step of every row, and one token of a batch of mostly unused
+    rows."""
+    import torch
+    from selective_state_space_84_amd import binding
+    gen = torch.Generator(device=DEV).manual_seed(23)
+    B, H = 4097, 4095  # 2^24 - 1 pairs
+    q = torch.randn(B, 1, H, 64, generator=gen, device=DEV, dtype=torch.bfloat16)
+    k, v = (torch.randn(B, 1, 1, 64, generator=gen, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    dec = torch.zeros(H, device=DEV)
+    o, _ = binding.ssm_linear_attn_fwd(q, k, v, dec, want_h_last=False)
+    torch.cuda.synchronize()
+    for b in (0, B // 2, B - 1):  # o = scale (q . k) v
+        n = dict(q=_np(q[b:b + 1]), k=_np(k[b:b + 1]), v=_np(v[b:b + 1]))
+        p, m = ((f(n["q"]) * f(n["k"])).sum(-1, keepdims=True) * 64 ** -0.5 for f in (lambda x: x, np.abs))
+        ref, mag = p * n["v"], m * np.abs(n["v"])
+        _close("o", _np(o[b:b + 1]), ref, P.attn_tol(ref, mag, 1, 64, "bf16"))
+    del q, o
+    B, H = 178481, 47  # 2^23 - 1 pairs of two workgroups
+    q = torch.randn(B, H, 64, generator=gen, device=DEV, dtype=torch.bfloat16)
+    k, v = (torch.randn(B, 1, 64, generator=gen, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    slots = torch.full((B,), -1, dtype=torch.int32, device=DEV)
+    slots[0], slots[B - 1] = 1, 0
+    h = torch.zeros(2, H, 64, 64, device=DEV)
+    u = binding.ssm_linear_attn_update(h, q, k, v, torch.zeros(H, device=DEV), slots=slots)
+    torch.cuda.synchronize()
+    assert not u[1:B - 1].any()
+    for b in (0, B - 1):
+        p, m = ((f(_np(q[b])) * f(_np(k[b]))).sum(-1, keepdims=True) * 64 ** -0.5 for f in (lambda x: x, np.abs))
+        ref, mag = p * _np(v[b]), m * np.abs(_np(v[b]))
+        _close("u", _np(u[b]), ref, P.attn_tol(ref, mag, 1, 64, "bf16"))

@@ -36,3 +36,29 @@ def test_gradient_of_shared_heads_without_query_heads_needs_outputs(lib):
     assert _attn(lib, 2, 10, 0, 2, grad=True) == bd.SSM_ERR_NULL_ARG
     assert _attn(lib, 2, 0, 0, 2, grad=True) == bd.SSM_OK
     assert _attn(lib, 2, 10, 0, 2) == bd.SSM_OK
+
+
+def test_more_workgroups_than_a_launch_holds(lib):
+    """An axis of a grid has fewer than 2^32 threads: refused before anything else is looked at, while what just fits
+    is refused here for its NULL pointers alone."""
+    null, bad = bd.SSM_ERR_NULL_ARG, bd.SSM_ERR_BAD_DIM
+    for b, H, dtype, dv, want in ((4097, 4095, 1, 128, null), (4097, 4096, 1, 64, bad), (4097, 4095, 0, 64, null),
+                                  (4097, 2047, 0, 128, null), (4097, 2048, 0, 128, bad)):
+        assert _attn(lib, b, 1, H, 1, False, 64, dv, dtype) == want, (b, H, dtype, dv)
+    size = lib.ssm_linear_attn_bwd_workspace_size
+    for b, H, dtype, want in ((4097, 1365, 1, null), (4097, 1366, 1, bad), (4097, 1365, 0, null), (4097, 1366, 0, bad)):
+        assert _attn(lib, b, 1, H, H, True, 64, 64, dtype) == want, (b, H, dtype)
+        assert (size(b, 1, H, H, 64, 64, dtype) == 0) == (want == null)
+    # The sum over shared heads has a thread for every 4 elements of dk: 2^31 of them, and 2^32.
+    assert _attn(lib, 1 << 12, 1 << 15, 2, 1, True) == null
+    assert _attn(lib, 1 << 13, 1 << 15, 2, 1, True) == bad
+
+    def update(b, H, d):
+        return lib.ssm_linear_attn_update(*[None] * 7, b, b, H, 1, d, d, 0, 0, 0, 0.125, 1, None)
+    assert update(4097, 2047, 64) == null and update(4097, 2048, 64) == bad
+    assert update(4097, 511, 128) == null and update(4097, 512, 128) == bad
+
+    def norm(L, headdim, rot):
+        return lib.ssm_qk_norm_rope_fwd(*[None] * 8, 1, L, 1, 0, headdim, rot, 0, 0, 0, 0, 1e-6, 0, 1, None)
+    assert norm((1 << 27) - 8, 256, 256) == null and norm(1 << 27, 256, 256) == bad  # 8 steps a workgroup
+    assert norm((1 << 31) - 300, 16, 16) == null  # 128 steps a workgroup
