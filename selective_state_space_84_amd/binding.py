@@ -647,9 +647,9 @@ def ssm_qk_norm_rope_bwd(q, k, wq=None, wk=None, inv_freq=None, *, dq_out, dk_ou
     names = [("dq", q.shape, q.dtype)]
     if want_dw:
         names.append(("dwq", (headdim,), torch.float32))
+    if (k is None) != (dk_out is None):
+        raise ValueError("dk_out is required with k" if dk_out is None else "dk_out given without k")
     if k is not None:
-        if dk_out is None:
-            raise ValueError("dk_out is required with k")
         _want(dk_out, k.shape, q.dtype, "dk_out")
         names.append(("dk", k.shape, q.dtype))
         if want_dw:

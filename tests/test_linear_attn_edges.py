@@ -1,6 +1,8 @@
 """Calls at the edges of what linear attention and the norm with rotation accept:
 no heads, counts that leave 64 bits, more workgroups than a launch holds
 (nothing is launched)."""
+import pytest
+
 from selective_state_space_84_amd import binding as bd
 
 P0 = 0x7F0000000000
@@ -62,3 +64,11 @@ def test_more_workgroups_than_a_launch_holds(lib):
         return lib.ssm_qk_norm_rope_fwd(*[None] * 8, 1, L, 1, 0, headdim, rot, 0, 0, 0, 0, 1e-6, 0, 1, None)
     assert norm((1 << 27) - 8, 256, 256) == null and norm(1 << 27, 256, 256) == bad  # 8 steps a workgroup
     assert norm((1 << 31) - 300, 16, 16) == null  # 128 steps a workgroup
+
+
+def test_binding_refuses_a_key_gradient_without_keys():
+    """As the forward call refuses k_out without k."""
+    torch = pytest.importorskip("torch")
+    q = torch.zeros(1, 5, 4, 64)
+    with pytest.raises(ValueError, match="dk_out"):
+        bd.ssm_qk_norm_rope_bwd(q, None, dq_out=q, dk_out=q)
