@@ -395,29 +395,33 @@ AttnSweep base(const LinAttnLaunch& p, const LinAttnPlan& pl) {
 // price of a pass over b and c for the spans' states: as many spans as make two
 // workgroups a CU (512 in all), or one a CU where they would be shorter than
 // kShortSpan steps; kMaxSpans at most (the carry walks them one after the other),
-// of at least kMinSpan steps.  Two spans do not pay: a CU takes
+// of whole steps of kSpanStep, rounded up.  Two spans do not pay: a CU takes
 // two blocks of different workgroups together in ~1.6 times the time of one, and
 // the states cost 0.4 of a sweep.  Measured (bf16, heads of 128): 8 x 2048 steps x
 // 32 heads 157 us whole, 202 us in two spans; 1 x 32768 x 32 402 us in 16 spans,
-// 433 us in 8, 440 us in 32; 1 x 4096 x 16 50 us in 16 spans, 58 us in 32; 1 x 1000
-// x 4 27 us in spans of 64, 30 us of 128, 46 us of 256, 64 us of 512; 1 x 8000 x 1
-// 38 us in 63 spans, 50 us in 125.
+// 433 us in 8, 440 us in 32; 1 x 4096 x 16 50 us in 16 spans, 58 us in 32; 1 x 8000
+// x 1 38 us in 63 spans, 50 us in 125.  Spans of 64 against 128 steps: 1 x 1000 x 4
+// 24.8 against 26.2 us, 1 x 2500 x 2 29.9 against 29.0, 1 x 3000 x 1 28.9 against
+// 27.3; fp32 36.9 against 45.6 (1 x 1000 x 4) and 38.8 against 45.3 (1 x 2500 x 2).
+// Short sequences stay whole, since three launches cost more than the blocks they
+// save: 1 x 256 steps x 4 heads whole 19.9 us, cut 22.8, 1 x 320 x 4 23.6 and 22.9
+// (gradient of 256 x 2 20.5 and 28.4, 512 x 2 35.2 and 28.3); fp32 192 x 4 31.0 and
+// 32.3, 256 x 4 38.9 and 32.5.
 constexpr int64_t kTargetGroups = 512;
-constexpr int64_t kMinSpan = 64;
 constexpr int64_t kShortSpan = 256;
 constexpr int64_t kMaxSpans = 64;
 constexpr int64_t kSpanStep = 64;  // spans start on block boundaries of both sweeps
+constexpr int64_t kMinCutBf16 = 320, kMinCutF32 = 256;
 
-static LinAttnPlan make_plan(int64_t groups, int64_t seqlen) {
+static LinAttnPlan make_plan(int64_t groups, int64_t seqlen, bool bf16) {
+  const int64_t steps = seqlen > 0 ? (seqlen + kSpanStep - 1) / kSpanStep : 1;  // of kSpanStep, the last one not whole
   int64_t n = groups > 0 ? kTargetGroups / groups : 1;
   if (groups > 0 && n > seqlen / kShortSpan) n = kTargetGroups / 2 / groups;
   if (n > kMaxSpans) n = kMaxSpans;
-  if (n > seqlen / kMinSpan) n = seqlen / kMinSpan;
-  if (n < 3) n = 1;
-  int64_t len = (seqlen + n - 1) / n;
-  len = (len + kSpanStep - 1) / kSpanStep * kSpanStep;
-  if (len < kSpanStep) len = kSpanStep;
-  return LinAttnPlan{len, seqlen > 0 ? (seqlen + len - 1) / len : 1};
+  if (n < 1 || seqlen < (bf16 ? kMinCutBf16 : kMinCutF32)) n = 1;
+  int64_t each = (steps + n - 1) / n;
+  if ((steps + each - 1) / each < 3) each = steps;
+  return LinAttnPlan{each * kSpanStep, (steps + each - 1) / each};
 }
 
 // The three gradient sweeps share a launch, and the fp32 sweep has a workgroup for
@@ -432,7 +436,7 @@ int64_t linear_attn_sum_threads(int64_t batch, int64_t seqlen, int64_t nheads_kv
 
 LinAttnPlan linear_attn_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16,
                              bool grad) {
-  return make_plan(linear_attn_groups(batch, nheads, d_k, d_v, bf16, grad), seqlen);
+  return make_plan(linear_attn_groups(batch, nheads, d_k, d_v, bf16, grad), seqlen, bf16);
 }
 
 static int64_t span_floats(int64_t batch, int64_t nheads, int64_t d_k, int64_t d_v, const LinAttnPlan& pl) {

@@ -72,3 +72,21 @@ def test_binding_refuses_a_key_gradient_without_keys():
     q = torch.zeros(1, 5, 4, 64)
     with pytest.raises(ValueError, match="dk_out"):
         bd.ssm_qk_norm_rope_bwd(q, None, dq_out=q, dk_out=q)
+
+
+@pytest.mark.parametrize("L,H,grad,bf16,f32", [
+    (1000, 4, False, 16, 16), (1024, 4, False, 16, 16), (2500, 2, False, 40, 40), (8000, 1, False, 63, 63),
+    (4096, 16, False, 16, 16), (32768, 32, False, 16, 8), (1511, 8, False, 24, 12), (1300, 4, True, 21, 7),
+    (1000, 64, False, 4, 1),
+    (200, 4, False, 1, 1), (255, 4, False, 1, 1), (256, 4, False, 1, 4), (319, 1, False, 1, 5), (320, 1, False, 5, 5),
+    (1000, 256, False, 1, 1), (1, 1, False, 1, 1), (0, 1, False, 1, 1)])
+def test_spans_of_a_sequence(lib, L, H, grad, bf16, f32):
+    """The spans a sequence is cut into, read off the workspace: one state a head and span (both directions' in the
+    gradient).  Steps that are no multiple of 64 do not double the spans' length, short sequences stay whole, and a
+    cut gives three spans at least."""
+    for dtype, want in ((1, bf16), (0, f32)):
+        if grad:
+            got = lib.ssm_linear_attn_bwd_workspace_size(1, L, H, H, 128, 128, dtype) / 2
+        else:
+            got = lib.ssm_linear_attn_fwd_workspace_size(1, L, H, 128, 128, dtype)
+        assert got == (want * H * 128 * 128 * 4 if want > 1 else 0), dtype
