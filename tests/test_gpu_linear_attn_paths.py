@@ -69,3 +69,37 @@ def test_largest_launches(lib):
         p, m = ((f(_np(q[b])) * f(_np(k[b]))).sum(-1, keepdims=True) * 64 ** -0.5 for f in (lambda x: x, np.abs))
         ref, mag = p * _np(v[b]), m * np.abs(_np(v[b]))
         _close("u", _np(u[b]), ref, P.attn_tol(ref, mag, 1, 64, "bf16"))
+
+
+@pytest.mark.parametrize("M", [32, 8])
+def test_more_pairs_than_compute_units(lib, M):
+    """Heads of 128 in bf16 with more workgroups than compute units: four waves of 32 columns each instead of eight of 16
+    (above 256 workgroups, one a pair in the prompt and three in the gradient)."""
+    lengths = [77, 0, 64, 77, 1, 65, 40, 77, 76]
+    d, n, _, _ = _make(24, 9, 77, 32, M, 128, 128, "bf16", fused=True)
+    _check_fwd(d, n, "bf16", lengths)
+    d, n, do, dh = _make(25, 3, 131, 32, M, 128, 128, "bf16", fused=True)
+    _check_bwd(d, n, do, dh, "bf16", [131, 70, 131])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 64), (128, 128)])
+def test_spans_with_shared_heads(lib, K, V, dtype):
+    """Spans, states at both ends and per-head gradients of shared heads, which lie behind the spans' states in the
+    workspace; a row that ends inside a span."""
+    d, n, do, dh = _make(26, 2, 700, 4, 2, K, V, dtype, fused=True, decay=[-1e-3, -0.02, 0.0, -0.5])
+    for lengths in (None, [700, 413]):
+        _check_fwd(d, n, dtype, lengths)
+        _check_bwd(d, n, do, dh, dtype, lengths)
+
+
+def test_spans_of_more_pairs_than_compute_units(lib):
+    """Spans and the four-wave form together: 96 pairs in five spans of a prompt of 1300 steps, 36 pairs in four of a
+    gradient of 1030."""
+    size = lib.ssm_linear_attn_fwd_workspace_size(3, 1300, 32, 128, 128, 1)
+    assert size == 96 * 5 * 128 * 128 * 4  # 96 pairs in five spans: 480 workgroups
+    d, n, _, _ = _make(27, 3, 1300, 32, 8, 128, 128, "bf16")
+    _check_fwd(d, n, "bf16", [1300, 517, 640])
+    assert lib.ssm_linear_attn_bwd_workspace_size(3, 1030, 12, 12, 128, 128, 1) == 2 * 36 * 4 * 128 * 128 * 4
+    d, n, do, dh = _make(28, 3, 1030, 12, 4, 128, 128, "bf16")
+    _check_bwd(d, n, do, dh, "bf16", [1030, 517, 64])
