@@ -103,3 +103,30 @@ def test_spans_of_more_pairs_than_compute_units(lib):
     assert lib.ssm_linear_attn_bwd_workspace_size(3, 1030, 12, 12, 128, 128, 1) == 2 * 36 * 4 * 128 * 128 * 4
     d, n, do, dh = _make(28, 3, 1030, 12, 4, 128, 128, "bf16")
     _check_bwd(d, n, do, dh, "bf16", [1030, 517, 64])
+
+
+def _off(x, ref):
+    return float(np.linalg.norm(_np(x) - ref) / np.linalg.norm(ref))
+
+
+@pytest.mark.parametrize("B,H,K,V", [(1, 3, 64, 64), (2, 4, 128, 128), (3, 30, 128, 128)])
+def test_bits_kept(lib, B, H, K, V):
+    """bf16 operands: the state keeps fp32's bits (three parts of the decayed values: 2^-24 and the powers' few roundings,
+    random, some 3e-7 in all; two parts would be off by 2^-18 at most, 2e-6 in all), and nothing but the rounding of the
+    outputs shows in them (two parts of the pairs and of the state that is read: 2^-18, in quadrature with 2^-9 less
+    than 1e-5 of it)."""
+    import torch
+    from selective_state_space_84_amd import binding
+    L = 333
+    d, n, do, dh = _make(29, B, L, H, H, K, V, "bf16", decay=-np.exp(np.linspace(-7, -1, H)))
+    o, hl = binding.ssm_linear_attn_fwd(**d)
+    g = binding.ssm_linear_attn_bwd(**d, do=do, dh_last=dh)
+    torch.cuda.synchronize()
+    ro, rh = P.attn_fwd(**n)
+    ref = dict(zip(("dq", "dk", "dv", "dh0"), P.attn_bwd(**n, do=_np(do), dh_last=_np(dh))))
+    print("  h_last %.3g dh0 %.3g" % (_off(hl, rh), _off(g["dh0"], ref["dh0"])), flush=True)
+    assert _off(hl, rh) < 1e-6 and _off(g["dh0"], ref["dh0"]) < 1e-6
+    for name, x, r in [("o", o, ro)] + [(k, g[k], ref[k]) for k in ("dq", "dk", "dv")]:
+        least = _off(torch.as_tensor(r).to(torch.bfloat16), r)
+        print("  %s %.6g, rounded alone %.6g" % (name, _off(x, r), least), flush=True)
+        assert _off(x, r) < 1.01 * least, name
