@@ -521,7 +521,8 @@ int ssm_linear_attn_update(float* h, const int32_t* slots, const void* q, const 
  * RMS norm of every query and key head followed by the rotation of position,
  * in one pass.  For a head x of headdim values at position p:
  *
- *   n = w * x / sqrt(mean(x^2) + eps)
+ *   n = w * x / sqrt(mean(x^2) + eps)     (mean(x^2) in fp32: |x| below 10^18,
+ *                                          and with eps 0 above 10^-18 or 0)
  *   the first rot_dim values of n are turned pair by pair by p * inv_freq[j]:
  *     (a, b) -> (a cos - b sin, a sin + b cos)
  *   with the pair j < rot_dim / 2 at (j, j + rot_dim / 2), or at (2 j, 2 j + 1)

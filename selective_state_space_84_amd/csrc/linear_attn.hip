@@ -23,8 +23,9 @@ typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 // Bound by the fp32 matrix rate (153 TFLOP/s in a large product on this
 // card), an eighth of the bf16 one; 32 steps keep the pair products (which
 // grow with the block) below a fifth of the state products.  1 x 4096 steps x 16
-// heads of 128: 113 us with the spans' states, 38 TFLOP/s counting only the two
-// products of a step with the state.
+// heads of 128: 114 us with the spans' states, 38 TFLOP/s counting only the two
+// products of a step with the state: with one workgroup a CU a SIMD has one wave,
+// whose LDS reads and three barriers a block nothing covers.
 constexpr int kT = 32;        // steps per block
 constexpr int kCols = 64;     // output columns per workgroup
 constexpr int kSc = kCols + 4;  // LDS row strides (floats) with rows 4 apart on different banks

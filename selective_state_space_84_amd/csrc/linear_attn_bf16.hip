@@ -14,7 +14,12 @@
 // between is split: P and the state of `read` into two bf16 values (about 16
 // significant bits, so that the rounding of a bf16 output stays the largest
 // error), w o C into three (24 bits: the state keeps fp32's precision over any
-// number of blocks, since each block adds to it at that precision).
+// number of blocks, since each block adds to it at that precision).  Three parts
+// everywhere leave the error of o, dq, dk and dv against 64 bits as it is (0.00166
+// of their norm, what rounding alone costs) and take the difference from products
+// in 32 bits, which round a few outputs the other way, from 1e-4 to 2e-5..4e-5:
+// long prompt 412 -> 447 us, padded batch 130 -> 155, gradient of 4 x 4096 x 16 x
+// 128 259 -> 301.  Not taken.
 //
 // Mapping.
 //   * The accumulators' layout (lane = column p, four rows n per register
@@ -33,12 +38,17 @@
 //     worked on.
 //
 // Measured, one MI355X (a copy reaches 5.1 TB/s): 1 x 32768 steps x 32 heads of
-// 128 in 16 spans: 403-418 us (1.07 GB, 2.6 TB/s), a third of it the spans'
-// states; gradient of 4 x 4096 x 16 heads of 128: 257-260 us.  No one resource is
-// full: counted over the long sweep the matrix units are busy 38% of the time, a
-// SIMD issues 53k vector instructions in its 524k cycles (4 to 5 cycles each,
-// measured alone), and waves wait a third of theirs; a block is a chain of load,
-// stage, pairs, barrier, join.  Against 427 us at the time: rows loaded straight
+// 128 in 16 spans: 407-413 us (1.07 GB, 2.6 TB/s), a third of it the spans'
+// states; gradient of 4 x 4096 x 16 heads of 128: 258-260 us.  In units of a 64 x
+// 128 x 128 product a block takes 0.31 (pairs) + 2 (read) + 3 (update) + 0.75
+// (join), and 3 more for its span's state: the splits and the second update make
+// 305 GFLOP of the long prompt, 251 us at the rate of a large product.  The rest is
+// not one resource: over the long sweep the matrix units are busy 38% of the time,
+// a SIMD issues 54k vector instructions in its 523k cycles (4 to 5 cycles each,
+// measured alone), 37% of the LDS cycles (13% of a CU's) are bank conflicts of rows
+// that lie 8 dwords (modulo 64) apart, and waves wait a third of their cycles; a
+// block is a chain of load, stage, pairs, barrier, join.  Against 427 us at the
+// time: rows loaded straight
 // to LDS, four waves a SIMD 447 us; the splits interleaved with the products by
 // hand 447 us; 32-step blocks 418 us, taken as the noise between runs and
 // not pursued; the update in two parts (16 bits) 398 us, but
@@ -519,7 +529,9 @@ k_attn_span_states(const AttnSweep f, const AttnSweep r, int roles) {
   }
 }
 
-// dq, dk and dv: three sweeps in one launch.
+// dq, dk and dv: three sweeps in one launch.  The three inlined roles hold three
+// launch descriptions: 77 to 93 of their scalars lie in lanes of vector registers
+// (8 at most in a sweep alone).
 template <typename O, int DK, int DV, int NW>
 __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2)))
 k_attn_sweep_grad(const AttnSweep q, const AttnSweep k, const AttnSweep v) {
@@ -539,7 +551,9 @@ k_attn_sweep_grad(const AttnSweep q, const AttnSweep k, const AttnSweep v) {
 // against four waves, 1000 steps, heads of 128: 64 (row, head) pairs (256
 // workgroups) 47 against 49 us, 256 pairs 75 against 81, 320 pairs 137 against
 // 116, 512 pairs 159 against 141; gradient of 4 x 4096 x 16 257 against 289, of 7
-// x 1000 x 16 heads (336 workgroups) 129 against 101.
+// x 1000 x 16 heads (336 workgroups) 129 against 101.  Heads of 64 by 128 have the
+// four-wave form alone: eight waves of 16 columns would take 5% off 8 x 1000 steps x
+// 32 of them (54 against 57 us).
 constexpr int64_t kOneEach = 256;
 
 }  // namespace

@@ -3,9 +3,10 @@
 //
 // Bound by HBM: 8 bytes of state move per state element against ~3 vector
 // instructions (233 requests x 32 heads of 128 x 128: 183 us, 5.3 TB/s, where a
-// copy reaches 5.1 to 5.3; one request x 16 heads: 3.2 us).  A state row (d_k floats) belongs to
-// d_k / 8 lanes, 8 elements (two 16-byte accesses) a lane, so that the row's dot
-// product with q closes with 3 or 4 adds across lanes.  One row a lane: four,
+// copy reaches 5.1 to 5.3; one request x 16 heads: 3.2 us; with fp32
+// operands 196 us).  A state row (d_k floats) belongs to d_k / 8 lanes, 8
+// elements (two 16-byte accesses) a lane, so that the row's dot product with q
+// closes with 3 or 4 adds across lanes.  One row a lane: four,
 // with k and q kept in registers over them, took 196 us there and no less at any
 // size tried (1 to 256 requests).
 #include "linear_attn.h"

@@ -7,9 +7,9 @@
 //           dx = r (w g) - x r^3 mean(w g x).
 //
 // Bound by HBM: x is read once and y written once (8192 steps x 64 heads of 128
-// in bf16: 54-57 us, 4.7-5.0 TB/s; gradient of 16384 steps x 32 heads: 91.5
-// us, 4.4 TB/s, two workgroups a CU by its registers; a copy reaches 5.1 TB/s).  A head belongs to G lanes
-// (the next power of two of headdim / 8), 8 values a lane; the mean closes with
+// in bf16: 54-58 us, 4.7-5.0 TB/s, in fp32 106 us, 5.1 TB/s; gradient of 16384
+// steps x 32 heads: 91 us, 4.4 TB/s, two workgroups a CU by its registers; a copy
+// reaches 5.1 TB/s).  A head belongs to G lanes (the next power of two of headdim / 8), 8 values a lane; the mean closes with
 // log2(G) adds across lanes, and the pairs of the half-split rotation come from
 // the lane rot_dim / 16 away.  A workgroup takes all heads of one or a few
 // steps, so that a step's angles are formed once, by one lane each, and shared
@@ -403,7 +403,9 @@ void set_steps(QkArgs& a, int64_t left) {
 constexpr int64_t kFwdGroups = 2048;
 // Workgroups (and partial sums) of the gradient: the two a CU that its registers
 // allow (16384 steps x 32 heads of 128 in bf16: 91.5 us; 95 us with 1024, 103 us
-// with 2048).
+// with 2048).  Their turns, of a power of two of steps, come out even where it
+// divides the steps; else the longest workgroup walks up to twice what others do (40
+// heads of 128: 6000 steps in 750 turns take 69 us, 8192 in 512 take 77).
 constexpr int64_t kBwdGroups = 512;
 
 QkArgs args(const QkNormRopeLaunch& p, bool grad) {
