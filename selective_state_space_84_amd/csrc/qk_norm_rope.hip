@@ -9,8 +9,8 @@
 // Bound by HBM: x is read once and y written once (8192 steps x 64 heads of 128
 // in bf16: 54-58 us, 4.7-5.0 TB/s, in fp32 106 us, 5.1 TB/s; gradient of 16384
 // steps x 32 heads: 91 us, 4.4 TB/s, two workgroups a CU by its registers; a copy
-// reaches 5.1 TB/s).  A head belongs to G lanes (the next power of two of headdim / 8), 8 values a lane; the mean closes with
-// log2(G) adds across lanes, and the pairs of the half-split rotation come from
+// reaches 5.1 TB/s).  A head belongs to G lanes (the next power of two of headdim
+// / 8), 8 values a lane; the mean closes with log2(G) adds across lanes, and the pairs of the half-split rotation come from
 // the lane rot_dim / 16 away.  A workgroup takes all heads of one or a few
 // steps, so that a step's angles are formed once, by one lane each, and shared
 // through LDS by its heads; the first heads' loads are on their way

@@ -73,8 +73,8 @@ def test_largest_launches(lib):
 
 @pytest.mark.parametrize("M", [32, 8])
 def test_more_pairs_than_compute_units(lib, M):
-    """Heads of 128 in bf16 with more workgroups than compute units: four waves of 32 columns each instead of eight of 16
-    (above 256 workgroups, one a pair in the prompt and three in the gradient)."""
+    """Heads of 128 in bf16 with more workgroups than compute units: four waves of 32 columns each instead of eight of
+    16 (above 256 workgroups, one a pair in the prompt and three in the gradient)."""
     lengths = [77, 0, 64, 77, 1, 65, 40, 77, 76]
     d, n, _, _ = _make(24, 9, 77, 32, M, 128, 128, "bf16", fused=True)
     _check_fwd(d, n, "bf16", lengths)
@@ -111,8 +111,8 @@ def _off(x, ref):
 
 @pytest.mark.parametrize("B,H,K,V", [(1, 3, 64, 64), (2, 4, 128, 128), (3, 30, 128, 128)])
 def test_bits_kept(lib, B, H, K, V):
-    """bf16 operands: the state keeps fp32's bits (three parts of the decayed values: 2^-24 and the powers' few roundings,
-    random, some 3e-7 in all; two parts would be off by 2^-18 at most, 2e-6 in all), and nothing but the rounding of the
+    """bf16 operands: the state keeps fp32's bits (three parts of the decayed values: 2^-24 and the powers' few
+    roundings, random, some 3e-7 in all; two parts would be off by 2^-18 at most, 2e-6 in all), and nothing but the rounding of the
     outputs shows in them (two parts of the pairs and of the state that is read: 2^-18, in quadrature with 2^-9 less
     than 1e-5 of it)."""
     import torch

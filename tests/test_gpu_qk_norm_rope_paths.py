@@ -31,7 +31,7 @@ def test_gradient_of_no_heads(lib):
 @pytest.mark.parametrize("B,L,H,M,D,R", [
     (1, 4101, 9, 8, 256, 256),    # forward 2 rounds of one step; gradient 8, and 513 turns on 512 workgroups
     (3, 2801, 40, 24, 64, 32),    # forward 2 rounds of 2 steps; gradient 8 of 2
-    (1, 32771, 1, 0, 256, 64),    # 2 rounds of 8 steps, the last turn of 3 steps; gradient 4 turns a workgroup and a fifth
+    (1, 32771, 1, 0, 256, 64),    # 2 rounds of 8 steps, the last turn of 3; gradient 4 or 5 turns a workgroup
     (1, 3001, 20, 4, 80, 48)])    # gradient 2 of 2 steps, 751 turns: 239 workgroups walk two
 def test_several_rounds(lib, B, L, H, M, D, R, inter, dtype):
     """Several rounds a workgroup on one set of angles, several turns a workgroup in the gradient, as long prompts and
@@ -43,8 +43,8 @@ def test_several_rounds(lib, B, L, H, M, D, R, inter, dtype):
 @pytest.mark.parametrize("B,L,H,M,D,R", [(1, 4101, 9, 8, 256, 256), (3, 2801, 4, 2, 64, 32), (1, 32771, 1, 1, 64, 64),
                                          (1, 3001, 20, 4, 80, 48), (1, 511, 3, 1, 128, 128), (1, 513, 3, 1, 128, 0)])
 def test_weight_gradients_take_every_step_once(lib, B, L, H, M, D, R):
-    """dw over all steps, by its norm: a step left out or taken twice shows as 1 / sqrt(steps), 5e-3 at least, where sums
-    of at most 170 roundings one after the other are off by 170 * 2^-24 = 1e-5 if all of them go one way."""
+    """dw over all steps, by its norm: a step left out or taken twice shows as 1 / sqrt(steps), 5e-3 at least, where
+    sums of at most 170 roundings one after the other are off by 170 * 2^-24 = 1e-5 if all of them go one way."""
     import torch
     from selective_state_space_84_amd import binding
     q, k, wq, wk, f, pos, dq, dk = _make(B + L + 1, B, L, H, M, D, R, "bf16")

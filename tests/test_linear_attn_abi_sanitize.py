@@ -33,8 +33,8 @@ def test_linear_attn_abi_clean_under_sanitizers(lib, tmp_path):
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
     out = str(tmp_path / "libssm_scan_sanitized.so")
-    subprocess.run([build_lib.HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *SAN, "-shared-libsan", "-o", out, *objs,
-                    build_lib.LIB, "-Wl,-rpath," + os.path.dirname(build_lib.LIB)],
+    subprocess.run([build_lib.HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *SAN, "-shared-libsan", "-o", out,
+                    *objs, build_lib.LIB, "-Wl,-rpath," + os.path.dirname(build_lib.LIB)],
                    check=True, capture_output=True, timeout=300)
     pre = os.environ.get("LD_PRELOAD", "")
     env = dict(os.environ, SSM_TEST_LIBRARY=out, LD_PRELOAD=(_runtime() + (" " + pre if pre else "")),

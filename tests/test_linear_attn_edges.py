@@ -11,8 +11,7 @@ MB = 1 << 20
 
 def test_norm_gradient_of_no_heads_reads_nothing(lib):
     """Without heads no frequencies are needed, and without weight gradients nothing is left to launch."""
-    rc = lib.ssm_qk_norm_rope_bwd(None, None, None, None, None, None, None, None, None, None, None, None, 2, 10, 0, 0, 64,
-                                  64, 0, 0, 1e-6, 0, 1, None, 0, None)
+    rc = lib.ssm_qk_norm_rope_bwd(*[None] * 12, 2, 10, 0, 0, 64, 64, 0, 0, 1e-6, 0, 1, None, 0, None)
     assert rc == bd.SSM_OK
 
 
