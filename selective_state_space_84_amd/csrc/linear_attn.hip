@@ -401,9 +401,16 @@ AttnSweep base(const LinAttnLaunch& p, const LinAttnPlan& pl) {
 // the states cost 0.4 of a sweep.  Measured (bf16, heads of 128): 8 x 2048 steps x
 // 32 heads 157 us whole, 202 us in two spans; 1 x 32768 x 32 402 us in 16 spans,
 // 433 us in 8, 440 us in 32; 1 x 4096 x 16 50 us in 16 spans, 58 us in 32; 1 x 8000
-// x 1 38 us in 63 spans, 50 us in 125.  Spans of 64 against 128 steps: 1 x 1000 x 4
-// 24.8 against 26.2 us, 1 x 2500 x 2 29.9 against 29.0, 1 x 3000 x 1 28.9 against
-// 27.3; fp32 36.9 against 45.6 (1 x 1000 x 4) and 38.8 against 45.3 (1 x 2500 x 2).
+// x 1 38 us in 63 spans, 50 us in 125.
+// In bf16 spans of one block (64 steps) pay against two where they and their states
+// (of both directions in the gradient), which the carry moves, are few, and again
+// where they give nearly every CU a workgroup: 1 x 1000 x 4 24.1 and 26.5 us, 1500 x 4
+// (96 states) 27.5 and 28.5, 2000 x 1 (32 spans) 25.0 and 26.9; 896 x 16 (224 states)
+// 31.5 and 32.2, 1000 x 16 30.2 and 33.4, 2000 x 8 (256) 32.1 and 34.1; not between:
+// 1700 x 4 (108) 29.8 and 27.8, 1500 x 8 (192) 33.7 and 31.9, gradient of 1300 x 4 (168)
+// 32.0 and 31.1; nor in more than 32 spans: 2500 x 4 35.9 and 32.1, 3500 x 1 31.1 and
+// 28.7 (2500 x 1 27.1 and 28.1).  In fp32, whose blocks take longer, they pay
+// throughout: 1000 x 4 36.9 and 45.6, 4000 x 1 42.3 and 46.7.
 // Short sequences stay whole, since three launches cost more than the blocks they
 // save: 1 x 256 steps x 4 heads whole 19.9 us, cut 22.8, 1 x 320 x 4 23.6 and 22.9
 // (gradient of 256 x 2 20.5 and 28.4, 512 x 2 35.2 and 28.3); fp32 192 x 4 31.0 and
@@ -413,14 +420,18 @@ constexpr int64_t kShortSpan = 256;
 constexpr int64_t kMaxSpans = 64;
 constexpr int64_t kSpanStep = 64;  // spans start on block boundaries of both sweeps
 constexpr int64_t kMinCutBf16 = 320, kMinCutF32 = 256;
+constexpr int64_t kOneBlockSpans = 32, kOneBlockFew = 96, kOneBlockMany = 200;
 
-static LinAttnPlan make_plan(int64_t groups, int64_t seqlen, bool bf16) {
+// states: of one span, in both directions for the gradient.
+static LinAttnPlan make_plan(int64_t groups, int64_t states, int64_t seqlen, bool bf16) {
   const int64_t steps = seqlen > 0 ? (seqlen + kSpanStep - 1) / kSpanStep : 1;  // of kSpanStep, the last one not whole
   int64_t n = groups > 0 ? kTargetGroups / groups : 1;
   if (groups > 0 && n > seqlen / kShortSpan) n = kTargetGroups / 2 / groups;
   if (n > kMaxSpans) n = kMaxSpans;
   if (n < 1 || seqlen < (bf16 ? kMinCutBf16 : kMinCutF32)) n = 1;
   int64_t each = (steps + n - 1) / n;
+  const bool between = steps * states > kOneBlockFew && steps * states < kOneBlockMany;
+  if (bf16 && each == 1 && (steps > kOneBlockSpans || between)) each = 2;
   if ((steps + each - 1) / each < 3) each = steps;
   return LinAttnPlan{each * kSpanStep, (steps + each - 1) / each};
 }
@@ -437,7 +448,8 @@ int64_t linear_attn_sum_threads(int64_t batch, int64_t seqlen, int64_t nheads_kv
 
 LinAttnPlan linear_attn_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t d_k, int64_t d_v, bool bf16,
                              bool grad) {
-  return make_plan(linear_attn_groups(batch, nheads, d_k, d_v, bf16, grad), seqlen, bf16);
+  return make_plan(linear_attn_groups(batch, nheads, d_k, d_v, bf16, grad), batch * nheads * (grad ? 2 : 1), seqlen,
+                   bf16);
 }
 
 static int64_t span_floats(int64_t batch, int64_t nheads, int64_t d_k, int64_t d_v, const LinAttnPlan& pl) {

@@ -74,8 +74,10 @@ def test_binding_refuses_a_key_gradient_without_keys():
 
 
 @pytest.mark.parametrize("L,H,grad,bf16,f32", [
-    (1000, 4, False, 16, 16), (1024, 4, False, 16, 16), (2500, 2, False, 40, 40), (8000, 1, False, 63, 63),
-    (4096, 16, False, 16, 16), (32768, 32, False, 16, 8), (1511, 8, False, 24, 12), (1300, 4, True, 21, 7),
+    (1000, 4, False, 16, 16), (1024, 4, False, 16, 16), (2500, 2, False, 20, 40), (8000, 1, False, 63, 63),
+    (1500, 4, False, 24, 24), (1700, 4, False, 14, 27), (2000, 1, False, 32, 32), (2049, 1, False, 17, 33),
+    (1000, 16, False, 16, 8), (1500, 8, False, 12, 12),
+    (4096, 16, False, 16, 16), (32768, 32, False, 16, 8), (1511, 8, False, 12, 12), (1300, 4, True, 11, 7), (1000, 2, True, 16, 16),
     (1000, 64, False, 4, 1),
     (200, 4, False, 1, 1), (255, 4, False, 1, 1), (256, 4, False, 1, 4), (319, 1, False, 1, 5), (320, 1, False, 5, 5),
     (1000, 256, False, 1, 1), (1, 1, False, 1, 1), (0, 1, False, 1, 1)])
