@@ -38,7 +38,7 @@
 //     worked on.
 //
 // Measured, one MI355X (a copy reaches 5.1 TB/s): 1 x 32768 steps x 32 heads of
-// 128 in 16 spans: 407-413 us (1.07 GB, 2.6 TB/s), a third of it the spans'
+// 128 in 16 spans: 407-422 us (1.07 GB, 2.6 TB/s), a third of it the spans'
 // states; gradient of 4 x 4096 x 16 heads of 128: 258-260 us.  In units of a 64 x
 // 128 x 128 product a block takes 0.31 (pairs) + 2 (read) + 3 (update) + 0.75
 // (join), and 3 more for its span's state: the splits and the second update make
