@@ -16,6 +16,15 @@
  *   ssm_qk_norm_rope_fwd / ssm_qk_norm_rope_bwd
  *                     per-head norm and position rotation of the queries and
  *                     keys that feed it, and their gradient
+ *   ssm_gated_scan_fwd / ssm_gated_scan_bwd / ssm_gated_scan_update
+ *                     gated linear recurrence with one state per channel: whole
+ *                     sequences, their gradient, and one recurrent step
+ *   ssm_gated_norm_fwd / ssm_gated_norm_bwd
+ *                     group norm of a mixer's output with its gate, and the
+ *                     gradient
+ *   ssm_residual_norm_fwd / ssm_residual_norm_bwd
+ *                     residual update between two blocks with the norms behind
+ *                     the one and before the other, and the gradient
  *
  * Per batch row b, channel d and state n (A diagonal, B and C shared by all
  * channels of a row):
@@ -572,6 +581,189 @@ int ssm_qk_norm_rope_bwd(const void* q, const void* k, const float* wq, const fl
 /* Workspace bytes of ssm_qk_norm_rope_bwd.  (size_t)-1 for invalid sizes. */
 size_t ssm_qk_norm_rope_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nheads_k,
                                            int64_t headdim);
+
+/*
+ * Gated linear recurrence.  Per batch row b and channel d, with one state h and
+ * gates that depend on the step:
+ *
+ *   a_t = exp(log_a[d] * sigmoid(ga[b,t,d]))
+ *   h_t = a_t * h_{t-1} + sqrt(1 - a_t^2) * sigmoid(gx[b,t,d]) * x[b,t,d]
+ *   y[b,t,d] = h_t * silu(z[b,t,d])
+ *
+ *   x, ga, gx, z : [batch][seqlen][width] io_dtype; z NULL for no output gate.
+ *                Consecutive steps (and the rows of the batch, seqlen steps
+ *                apart) are x_stride, ga_stride, gx_stride, z_stride elements
+ *                apart, so that each may be a column range of one projection's
+ *                output; 0 stands for width.  Aligned to their elements; faster
+ *                where widths, strides and addresses are multiples of 4 bytes.
+ *                Strides not below width and at most 2^40.
+ *   log_a      : [width] fp32, <= 0 and finite: the log of the strongest decay.
+ *                Where 1 - a^2 is below fp32's normal range (and for log_a > 0)
+ *                the input counts as nothing.
+ *   lengths    : [batch] int32 or NULL.  Row b has lengths[b] steps (clamped to
+ *                [0, seqlen] on the device); what the inputs hold behind them is
+ *                not used, y is zero there, and h_last is the state after
+ *                lengths[b] steps.
+ *   h0, h_last : [batch][width] fp32, or NULL (zeros / not written); h_last may
+ *                be the h0 buffer.
+ *   y          : [batch][seqlen][width] io_dtype, dense; overlaps no input.
+ *   ckpt       : ssm_gated_scan_ckpt_bytes() bytes, 4-byte aligned, or NULL:
+ *                receives states on the way, which spare the gradient a pass
+ *                over x, ga and gx.  Only ssm_gated_scan_bwd of the same sizes
+ *                reads them.
+ *   workspace  : ssm_gated_scan_fwd_workspace_size() bytes, 256-byte aligned
+ *                (may be NULL when that is 0); contents on entry ignored.
+ *                Calls that may run at the same time need one each, and so do
+ *                two captured graphs that may be replayed at the same time.
+ * The state is fp32 and y is rounded once.  Sums are taken in a fixed order:
+ * results are bitwise reproducible for given sizes and strides.  Same
+ * conventions, validation and error codes as the scan; width above 2^23, more
+ * than 2^31 states or more than 2^31 pieces of 64 steps and 64 channels:
+ * SSM_ERR_BAD_DIM.
+ */
+int ssm_gated_scan_fwd(const void* x, const void* ga, const void* gx, const float* log_a, const void* z,
+                       const int32_t* lengths, const float* h0, void* y, float* h_last, float* ckpt, int64_t batch,
+                       int64_t seqlen, int64_t width, int64_t x_stride, int64_t ga_stride, int64_t gx_stride,
+                       int64_t z_stride, int32_t io_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of ssm_gated_scan_fwd, and bytes of the states it can save.
+ * (size_t)-1 for invalid sizes.  Pure host computation. */
+size_t ssm_gated_scan_fwd_workspace_size(int64_t batch, int64_t seqlen, int64_t width, int32_t io_dtype);
+size_t ssm_gated_scan_ckpt_bytes(int64_t batch, int64_t seqlen, int64_t width);
+
+/*
+ * Gradient of ssm_gated_scan_fwd for L = sum(dy * y) + sum(dh_last * h_last).
+ *
+ *   x, ga, gx, log_a, z, lengths, h0, strides, io_dtype : as in the forward call.
+ *   dy      : [batch][seqlen][width] io_dtype, dense (unused behind a row's
+ *             length).
+ *   dh_last : [batch][width] fp32, or NULL for 0.
+ *   ckpt    : what the forward call saved, or NULL (recomputed).
+ *   dx, dga, dgx : io_dtype, dense; zero behind a row's length.
+ *   dz      : the same; given exactly when z is.
+ *   dlog_a  : [width] fp32, summed over rows and steps in a fixed order, or
+ *             NULL.  (Where the input counts as nothing, so does the derivative
+ *             of sqrt(1 - a^2).)
+ *   dh0     : [batch][width] fp32 (of zeros when h0 is NULL), or NULL.
+ *   workspace : ssm_gated_scan_bwd_workspace_size() bytes (ckpt_given: 1 when
+ *             ckpt is not NULL, else 0), 256-byte aligned.
+ * Outputs are overwritten and must not overlap each other, any input or the
+ * workspace.
+ */
+int ssm_gated_scan_bwd(const void* x, const void* ga, const void* gx, const float* log_a, const void* z,
+                       const int32_t* lengths, const float* h0, const void* dy, const float* dh_last,
+                       const float* ckpt, void* dx, void* dga, void* dgx, void* dz, float* dlog_a, float* dh0,
+                       int64_t batch, int64_t seqlen, int64_t width, int64_t x_stride, int64_t ga_stride,
+                       int64_t gx_stride, int64_t z_stride, int32_t io_dtype, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* Workspace bytes of ssm_gated_scan_bwd.  (size_t)-1 for invalid sizes. */
+size_t ssm_gated_scan_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t width, int32_t io_dtype,
+                                         int32_t ckpt_given);
+
+/*
+ * One recurrent step (decode) of the same operator, in place on the state.
+ *
+ *   h       : [n_slots][width] fp32.
+ *   slots   : [batch] int32 or NULL.  Request b's state is h[slots[b]]; NULL
+ *             stands for slots[b] = b (n_slots must then be batch).  A value
+ *             outside [0, n_slots) marks an unused row: no state is touched and
+ *             its y is zero.  The used values must differ: of two requests with
+ *             one slot, that slot's state and both outputs are unspecified.
+ *   x, ga, gx, z : [batch][width] io_dtype, rows x_stride, ... elements apart
+ *             (0: dense); z NULL for no output gate.
+ *   y       : [batch][width] io_dtype, dense; overlaps nothing.
+ * batch * width / 256 (each row rounded up) below 2^24.  Equivalent to
+ * ssm_gated_scan_fwd with seqlen 1 and h0 = h_last = h[slots].
+ */
+int ssm_gated_scan_update(float* h, const int32_t* slots, const void* x, const void* ga, const void* gx,
+                          const float* log_a, const void* z, void* y, int64_t batch, int64_t n_slots, int64_t width,
+                          int64_t x_stride, int64_t ga_stride, int64_t gx_stride, int64_t z_stride, int32_t io_dtype,
+                          void* stream);
+
+/*
+ * RMS norm of a mixer's output over groups of channels, with its SiLU gate.  Per
+ * row and group of width / groups values:
+ *
+ *   gate_first 1:  t = x * silu(z),  y = w * t / sqrt(mean(t^2) + eps)
+ *   gate_first 0:  y = w * x / sqrt(mean(x^2) + eps) * silu(z)
+ *
+ *   x, z    : [rows][width] io_dtype, rows x_stride and z_stride elements apart
+ *             (0: dense; at most 2^40); z NULL for no gate (a norm alone).
+ *             Aligned to their elements; faster where groups, strides and all
+ *             addresses are multiples of 8 values and 16 bytes.
+ *   w       : [width] fp32, or NULL for ones.
+ *   y       : [rows][width] io_dtype, dense.  It may be x itself (dense, in
+ *             place) and overlaps nothing else.
+ *   eps >= 0.  groups divides width, with at most 16384 values in a group.
+ * Means are fp32: |t| below 10^18; a group of zeros with eps 0 gives NaN.
+ */
+int ssm_gated_norm_fwd(const void* x, const void* z, const float* w, void* y, int64_t rows, int64_t width,
+                       int64_t groups, int64_t x_stride, int64_t z_stride, float eps, int32_t gate_first,
+                       int32_t io_dtype, void* stream);
+
+/*
+ * Gradient of ssm_gated_norm_fwd, from x and z as the forward call read them and
+ * dy [rows][width] (dense):
+ *   dx, dz  : io_dtype, dense; dz given exactly when z is.
+ *   dw      : [width] fp32, summed over the rows in a fixed order, or NULL when
+ *             not wanted (also valid for w NULL).
+ *   workspace : ssm_gated_norm_bwd_workspace_size() bytes, 256-byte aligned
+ *             (unused, may be NULL, when dw is not wanted).
+ * Outputs must not overlap each other, any input or the workspace.
+ */
+int ssm_gated_norm_bwd(const void* x, const void* z, const float* w, const void* dy, void* dx, void* dz, float* dw,
+                       int64_t rows, int64_t width, int64_t groups, int64_t x_stride, int64_t z_stride, float eps,
+                       int32_t gate_first, int32_t io_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of ssm_gated_norm_bwd.  (size_t)-1 for invalid sizes. */
+size_t ssm_gated_norm_bwd_workspace_size(int64_t rows, int64_t width, int64_t groups);
+
+/*
+ * Residual update between two blocks: x, the output of the one, is normed,
+ * scaled and added to the stream, and the sum is normed for the other.
+ *
+ *   n       = w_post * x / sqrt(mean(x^2) + eps)   (post_norm 1)
+ *           = w_post * x                           (post_norm 0)
+ *   res_out = residual + alpha * n
+ *   y       = w_pre * res_out / sqrt(mean(res_out^2) + eps)
+ *
+ *   x, y    : [rows][width] io_dtype; x's rows x_stride elements apart (0:
+ *             dense), y dense.
+ *   residual, res_out : [rows][width] res_dtype, dense: SSM_DTYPE_F32, or
+ *             SSM_DTYPE_BF16 with bf16 io.  residual NULL stands for zeros;
+ *             res_out may be residual itself.  y is the norm of the sum before it
+ *             is rounded to res_dtype.
+ *   w_pre, w_post : [width] fp32, or NULL for ones.
+ *   eps >= 0; width at most 16384.  Alignment as for ssm_gated_norm_fwd; y and
+ *   res_out overlap nothing else.  Means are fp32, as there.
+ */
+int ssm_residual_norm_fwd(const void* x, const void* residual, const float* w_pre, const float* w_post, void* res_out,
+                          void* y, int64_t rows, int64_t width, int64_t x_stride, float alpha, float eps,
+                          int32_t post_norm, int32_t io_dtype, int32_t res_dtype, void* stream);
+
+/*
+ * Gradient of ssm_residual_norm_fwd, from x and res_out as the forward call read
+ * and wrote them:
+ *   dy       : [rows][width] io_dtype, dense: the gradient of y.
+ *   dres_out : [rows][width] res_dtype, or NULL for 0: what reaches res_out
+ *              from behind.
+ *   dx       : io_dtype, dense.
+ *   dres     : res_dtype, dense: the gradient of residual, or NULL.
+ *   dw_pre, dw_post : [width] fp32, summed over the rows in a fixed order, or
+ *              NULL when not wanted (also valid for NULL weights).
+ *   x may be NULL with post_norm 0 and without dw_post.
+ *   workspace : ssm_residual_norm_bwd_workspace_size() bytes, 256-byte aligned
+ *              (unused, may be NULL, when neither sum is wanted).
+ * Outputs must not overlap each other, any input or the workspace.
+ */
+int ssm_residual_norm_bwd(const void* x, const void* res_out, const float* w_pre, const float* w_post, const void* dy,
+                          const void* dres_out, void* dx, void* dres, float* dw_pre, float* dw_post, int64_t rows,
+                          int64_t width, int64_t x_stride, float alpha, float eps, int32_t post_norm, int32_t io_dtype,
+                          int32_t res_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of ssm_residual_norm_bwd.  (size_t)-1 for invalid sizes. */
+size_t ssm_residual_norm_bwd_workspace_size(int64_t rows, int64_t width);
 
 #ifdef __cplusplus
 }

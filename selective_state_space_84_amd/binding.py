@@ -75,6 +75,18 @@ SIGNATURES = {
     "ssm_qk_norm_rope_fwd": ([_P] * 8 + [_I64] * 10 + [_F32, _I32, _I32, _P], ctypes.c_int),
     "ssm_qk_norm_rope_bwd": ([_P] * 12 + [_I64] * 8 + [_F32, _I32, _I32, _P, _SZ, _P], ctypes.c_int),
     "ssm_qk_norm_rope_bwd_workspace_size": ([_I64] * 5, _SZ),
+    "ssm_gated_scan_fwd": ([_P] * 10 + [_I64] * 7 + [_I32, _P, _SZ, _P], ctypes.c_int),
+    "ssm_gated_scan_fwd_workspace_size": ([_I64] * 3 + [_I32], _SZ),
+    "ssm_gated_scan_ckpt_bytes": ([_I64] * 3, _SZ),
+    "ssm_gated_scan_bwd": ([_P] * 16 + [_I64] * 7 + [_I32, _P, _SZ, _P], ctypes.c_int),
+    "ssm_gated_scan_bwd_workspace_size": ([_I64] * 3 + [_I32] * 2, _SZ),
+    "ssm_gated_scan_update": ([_P] * 8 + [_I64] * 7 + [_I32, _P], ctypes.c_int),
+    "ssm_gated_norm_fwd": ([_P] * 4 + [_I64] * 5 + [_F32, _I32, _I32, _P], ctypes.c_int),
+    "ssm_gated_norm_bwd": ([_P] * 7 + [_I64] * 5 + [_F32, _I32, _I32, _P, _SZ, _P], ctypes.c_int),
+    "ssm_gated_norm_bwd_workspace_size": ([_I64] * 3, _SZ),
+    "ssm_residual_norm_fwd": ([_P] * 6 + [_I64] * 3 + [_F32, _F32, _I32, _I32, _I32, _P], ctypes.c_int),
+    "ssm_residual_norm_bwd": ([_P] * 10 + [_I64] * 3 + [_F32, _F32, _I32, _I32, _I32, _P, _SZ, _P], ctypes.c_int),
+    "ssm_residual_norm_bwd_workspace_size": ([_I64] * 2, _SZ),
 }
 
 _lib = None
@@ -670,4 +682,315 @@ def ssm_qk_norm_rope_bwd(q, k, wq=None, wk=None, inv_freq=None, *, dq_out, dk_ou
             _io_dtype(q), _ptr(workspace), have, _here(q))
     if rc != SSM_OK:
         raise SsmError(rc, "ssm_qk_norm_rope_bwd")
+    return g
+
+
+def _steps(t, what: str) -> Tuple[Optional[int], int]:
+    """(pointer, elements between rows) of a tensor (..., width) whose rows are
+    evenly spaced: a dense tensor, or a column range of a wider one."""
+    if not t.is_cuda:
+        raise ValueError("tensor must live on the GPU")
+    shape = t.shape
+    width = shape[-1]
+    if t.is_contiguous():
+        return t.data_ptr() or None, width
+    st = t.stride()
+    ok = st[-1] == 1 or width <= 1
+    step = rows = None
+    for n, s in zip(reversed(shape[:-1]), reversed(st[:-1])):
+        if n == 1:
+            continue
+        if step is None:
+            step, rows = s, n
+        else:
+            ok = ok and s == step * rows
+            rows *= n
+    step = width if step is None else step
+    if not ok or step < width:
+        raise ValueError("%s must hold dense rows at one distance" % what)
+    return t.data_ptr() or None, step
+
+
+def _gated_shapes(x, ga, gx, log_a, z, lead):
+    import torch
+    if x.dim() != lead + 1:
+        raise ValueError("x must have %d axes, got %s" % (lead + 1, tuple(x.shape)))
+    _want(ga, x.shape, x.dtype, "ga")
+    _want(gx, x.shape, x.dtype, "gx")
+    _want(z, x.shape, x.dtype, "z")
+    _want(log_a, x.shape[-1:], torch.float32, "log_a")
+
+
+def _ckpt_floats(lib, batch, seqlen, width, what):
+    n = lib.ssm_gated_scan_ckpt_bytes(batch, seqlen, width)
+    if n == ctypes.c_size_t(-1).value:
+        raise SsmError(SSM_ERR_BAD_DIM, what)
+    return n // 4
+
+
+def ssm_gated_scan_fwd(x, ga, gx, log_a, z=None, *, lengths=None, h0=None, y=None, h_last=None, want_h_last=True,
+                       want_ckpt=False, workspace=None, stream=None):
+    """Gated linear recurrence; returns (y, h_last, ckpt).
+
+    h_t = a_t h_(t-1) + sqrt(1 - a_t^2) sigmoid(gx_t) x_t with
+    a_t = exp(log_a sigmoid(ga_t)); y = h silu(z).  x, ga, gx, z: (batch, seqlen,
+    width), all bfloat16 or all float32, dense or column ranges of a wider
+    tensor; log_a: (width,) fp32, not positive; lengths: (batch,) int32 steps of
+    each row; h0, h_last: (batch, width) fp32.  ckpt (None unless want_ckpt)
+    holds states on the way for ssm_gated_scan_bwd.
+    """
+    import torch
+    _gated_shapes(x, ga, gx, log_a, z, 2)
+    batch, seqlen, width = x.shape
+    dt, f32 = _io_dtype(x), torch.float32
+    st = (batch, width)
+    _want(lengths, (batch,), torch.int32, "lengths")
+    _want(h0, st, f32, "h0")
+    _want(y, x.shape, x.dtype, "y")
+    _want(h_last, st, f32, "h_last")
+    lib = load_library()
+    with _scope(stream, x, ga, gx, log_a, z, lengths, h0, y, h_last, workspace):
+        dev = x.device
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        if h_last is None and want_h_last:
+            h_last = torch.empty(st, dtype=f32, device=dev)
+        ckpt = None
+        if want_ckpt:
+            ckpt = torch.empty(_ckpt_floats(lib, batch, seqlen, width, "ssm_gated_scan_fwd"), dtype=f32, device=dev)
+        need = lib.ssm_gated_scan_fwd_workspace_size(batch, seqlen, width, dt)
+        workspace, have = _workspace(workspace, need, dev, "ssm_gated_scan_fwd")
+        (xp, xs), (ap, as_), (ip, is_) = _steps(x, "x"), _steps(ga, "ga"), _steps(gx, "gx")
+        zp, zs = (None, 0) if z is None else _steps(z, "z")
+        rc = lib.ssm_gated_scan_fwd(xp, ap, ip, _dense(log_a, "log_a"), zp, _dense(lengths, "lengths"),
+                                    _dense(h0, "h0"), _dense(y, "y"), _dense(h_last, "h_last"), _dense(ckpt, "ckpt"),
+                                    batch, seqlen, width, xs, as_, is_, zs, dt, _dense(workspace, "workspace"), have,
+                                    _here(x))
+    if rc != SSM_OK:
+        raise SsmError(rc, "ssm_gated_scan_fwd")
+    return y, h_last, ckpt
+
+
+def ssm_gated_scan_bwd(x, ga, gx, log_a, z=None, *, dy, lengths=None, h0=None, dh_last=None, ckpt=None, want_dh0=True,
+                       want_dlog_a=True, grads=None, workspace=None, stream=None):
+    """Gradient of ssm_gated_scan_fwd for L = sum(dy * y) + sum(dh_last * h_last).
+
+    Returns a dict with dx, dga, dgx, with z dz (io dtype, dense), and when wanted
+    dlog_a and dh0 (fp32).  ckpt: what the forward call returned for it, or None
+    (recomputed).  Outputs are allocated unless given in ``grads``.
+    """
+    import torch
+    _gated_shapes(x, ga, gx, log_a, z, 2)
+    batch, seqlen, width = x.shape
+    dt, f32 = _io_dtype(x), torch.float32
+    st = (batch, width)
+    _want(lengths, (batch,), torch.int32, "lengths")
+    _want(h0, st, f32, "h0")
+    _want(dy, x.shape, x.dtype, "dy")
+    _want(dh_last, st, f32, "dh_last")
+    g = dict(grads or {})
+    names = [("dx", x.shape, x.dtype), ("dga", x.shape, x.dtype), ("dgx", x.shape, x.dtype)]
+    if z is not None:
+        names.append(("dz", x.shape, x.dtype))
+    if want_dlog_a or "dlog_a" in g:
+        names.append(("dlog_a", (width,), f32))
+    if want_dh0 or "dh0" in g:
+        names.append(("dh0", st, f32))
+    lib = load_library()
+    if ckpt is not None:
+        _want(ckpt, (_ckpt_floats(lib, batch, seqlen, width, "ssm_gated_scan_bwd"),), f32, "ckpt")
+    with _scope(stream, x, ga, gx, log_a, z, lengths, h0, dy, dh_last, ckpt, workspace, *g.values()):
+        _fill(g, names, x.device)
+        # Saved states of no steps are no pointer: the recomputation of none costs nothing.
+        cp = _dense(ckpt, "ckpt")
+        need = lib.ssm_gated_scan_bwd_workspace_size(batch, seqlen, width, dt, 0 if cp is None else 1)
+        workspace, have = _workspace(workspace, need, x.device, "ssm_gated_scan_bwd")
+        (xp, xs), (ap, as_), (ip, is_) = _steps(x, "x"), _steps(ga, "ga"), _steps(gx, "gx")
+        zp, zs = (None, 0) if z is None else _steps(z, "z")
+        rc = lib.ssm_gated_scan_bwd(
+            xp, ap, ip, _dense(log_a, "log_a"), zp, _dense(lengths, "lengths"), _dense(h0, "h0"), _dense(dy, "dy"),
+            _dense(dh_last, "dh_last"), cp, _dense(g["dx"], "dx"), _dense(g["dga"], "dga"), _dense(g["dgx"], "dgx"),
+            _dense(g.get("dz"), "dz"), _dense(g.get("dlog_a"), "dlog_a"), _dense(g.get("dh0"), "dh0"), batch, seqlen,
+            width, xs, as_, is_, zs, dt, _dense(workspace, "workspace"), have, _here(x))
+    if rc != SSM_OK:
+        raise SsmError(rc, "ssm_gated_scan_bwd")
+    return g
+
+
+def ssm_gated_scan_update(h, x, ga, gx, log_a, z=None, *, slots=None, y=None, stream=None):
+    """One decode step of the gated recurrence, in place on h (n_slots, width) fp32; returns y (batch, width).
+
+    x, ga, gx, z: (batch, width); slots: (batch,) int32 places of the requests'
+    states in h (values outside h mark unused rows; used values must differ), or
+    None when h holds the batch in order.
+    """
+    import torch
+    _gated_shapes(x, ga, gx, log_a, z, 1)
+    batch, width = x.shape
+    n_slots = h.shape[0]
+    _want(h, (n_slots, width), torch.float32, "h")
+    _want(slots, (batch,), torch.int32, "slots")
+    _want(y, x.shape, x.dtype, "y")
+    dt = _io_dtype(x)
+    with _scope(stream, x, h, slots, ga, gx, log_a, z, y):
+        if y is None:
+            y = torch.empty((batch, width), dtype=x.dtype, device=x.device)
+        (xp, xs), (ap, as_), (ip, is_) = _steps(x, "x"), _steps(ga, "ga"), _steps(gx, "gx")
+        zp, zs = (None, 0) if z is None else _steps(z, "z")
+        rc = load_library().ssm_gated_scan_update(
+            _dense(h, "h"), _dense(slots, "slots"), xp, ap, ip, _dense(log_a, "log_a"), zp, _dense(y, "y"), batch,
+            n_slots, width, xs, as_, is_, zs, dt, _here(x))
+    if rc != SSM_OK:
+        raise SsmError(rc, "ssm_gated_scan_update")
+    return y
+
+
+def _norm_rows(x, what):
+    if x.dim() < 1:
+        raise ValueError("%s must have an axis" % what)
+    width = x.shape[-1]
+    return (x.numel() // width if width else 0), width
+
+
+def ssm_gated_norm_fwd(x, z=None, w=None, *, groups=1, gate_first=True, eps=1e-6, y=None, stream=None):
+    """RMS norm of x (..., width) over ``groups`` groups of its channels, with the
+    gate silu(z) on its input (gate_first) or on its output; returns y.
+
+    x, z: bfloat16 or float32, dense or column ranges of a wider tensor; w:
+    (width,) fp32 or None for ones.  y may be x itself (in place).
+    """
+    import torch
+    rows, width = _norm_rows(x, "x")
+    _want(z, x.shape, x.dtype, "z")
+    _want(w, (width,), torch.float32, "w")
+    _want(y, x.shape, x.dtype, "y")
+    dt = _io_dtype(x)
+    with _scope(stream, x, z, w, y):
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        xp, xs = _steps(x, "x")
+        zp, zs = (None, 0) if z is None else _steps(z, "z")
+        rc = load_library().ssm_gated_norm_fwd(xp, zp, _dense(w, "w"), _dense(y, "y"), rows, width, groups, xs, zs,
+                                               eps, 1 if gate_first else 0, dt, _here(x))
+    if rc != SSM_OK:
+        raise SsmError(rc, "ssm_gated_norm_fwd")
+    return y
+
+
+def ssm_gated_norm_bwd(x, z=None, w=None, *, dy, groups=1, gate_first=True, eps=1e-6, want_dw=True, grads=None,
+                       workspace=None, stream=None):
+    """Gradient of ssm_gated_norm_fwd: a dict with dx, with z dz (dense), and when
+    want_dw dw (fp32).  Outputs are allocated unless given in ``grads``."""
+    import torch
+    rows, width = _norm_rows(x, "x")
+    _want(z, x.shape, x.dtype, "z")
+    _want(w, (width,), torch.float32, "w")
+    _want(dy, x.shape, x.dtype, "dy")
+    dt = _io_dtype(x)
+    g = dict(grads or {})
+    names = [("dx", x.shape, x.dtype)]
+    if z is not None:
+        names.append(("dz", x.shape, x.dtype))
+    if want_dw or "dw" in g:
+        names.append(("dw", (width,), torch.float32))
+    lib = load_library()
+    with _scope(stream, x, z, w, dy, workspace, *g.values()):
+        _fill(g, names, x.device)
+        need = lib.ssm_gated_norm_bwd_workspace_size(rows, width, groups) if "dw" in g else 0
+        workspace, have = _workspace(workspace, need, x.device, "ssm_gated_norm_bwd")
+        xp, xs = _steps(x, "x")
+        zp, zs = (None, 0) if z is None else _steps(z, "z")
+        rc = lib.ssm_gated_norm_bwd(xp, zp, _dense(w, "w"), _dense(dy, "dy"), _dense(g["dx"], "dx"),
+                                    _dense(g.get("dz"), "dz"), _dense(g.get("dw"), "dw"), rows, width, groups, xs, zs,
+                                    eps, 1 if gate_first else 0, dt, _dense(workspace, "workspace"), have, _here(x))
+    if rc != SSM_OK:
+        raise SsmError(rc, "ssm_gated_norm_bwd")
+    return g
+
+
+def ssm_residual_norm_fwd(x, residual, w_pre=None, w_post=None, *, alpha=1.0, post_norm=False, eps=1e-6, res_out=None,
+                          y=None, res_dtype=None, stream=None):
+    """Residual update between two blocks; returns (res_out, y).
+
+    res_out = residual + alpha n with n = w_post x (rms-normed first when
+    post_norm), y = w_pre times the rms-normed res_out.  x: (..., width) bfloat16
+    or float32, dense or a column range of a wider tensor; residual, res_out:
+    the same shape, dense, float32 or x's dtype (residual None: zeros, in
+    res_dtype, by default x's); w_pre, w_post: (width,) fp32 or None for ones.  res_out may
+    be residual itself (in place).
+    """
+    import torch
+    rows, width = _norm_rows(x, "x")
+    rt = residual.dtype if residual is not None else (
+        res_out.dtype if res_out is not None else (x.dtype if res_dtype is None else res_dtype))
+    if res_dtype is not None and rt != res_dtype:
+        raise ValueError("residual must be %s, got %s" % (res_dtype, rt))
+    _want(residual, x.shape, rt, "residual")
+    _want(res_out, x.shape, rt, "res_out")
+    _want(y, x.shape, x.dtype, "y")
+    _want(w_pre, (width,), torch.float32, "w_pre")
+    _want(w_post, (width,), torch.float32, "w_post")
+    dt, rd = _io_dtype(x), _res_dtype(rt)
+    with _scope(stream, x, residual, w_pre, w_post, res_out, y):
+        if res_out is None:
+            res_out = torch.empty(x.shape, dtype=rt, device=x.device)
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        xp, xs = _steps(x, "x")
+        rc = load_library().ssm_residual_norm_fwd(
+            xp, _dense(residual, "residual"), _dense(w_pre, "w_pre"), _dense(w_post, "w_post"),
+            _dense(res_out, "res_out"), _dense(y, "y"), rows, width, xs, alpha, eps, 1 if post_norm else 0, dt, rd,
+            _here(x))
+    if rc != SSM_OK:
+        raise SsmError(rc, "ssm_residual_norm_fwd")
+    return res_out, y
+
+
+def _res_dtype(rt) -> int:
+    import torch
+    if rt == torch.float32:
+        return SSM_DTYPE_F32
+    if rt == torch.bfloat16:
+        return SSM_DTYPE_BF16
+    raise ValueError("the residual must be bfloat16 or float32, got %s" % rt)
+
+
+def ssm_residual_norm_bwd(x, res_out, w_pre=None, w_post=None, *, dy, dres_out=None, alpha=1.0, post_norm=False,
+                          eps=1e-6, want_dres=True, want_dw=True, grads=None, workspace=None, stream=None):
+    """Gradient of ssm_residual_norm_fwd from x and the res_out it returned: a dict
+    with dx, when want_dres dres, and when want_dw dw_pre and dw_post (fp32).
+
+    dy, dres_out (or None): gradients of y and res_out.  x may be None without
+    post_norm and want_dw.  Outputs are allocated unless given in ``grads``.
+    """
+    import torch
+    rows, width = _norm_rows(res_out, "res_out")
+    _want(x, res_out.shape, dy.dtype, "x")
+    _want(dy, res_out.shape, dy.dtype, "dy")
+    _want(dres_out, res_out.shape, res_out.dtype, "dres_out")
+    _want(w_pre, (width,), torch.float32, "w_pre")
+    _want(w_post, (width,), torch.float32, "w_post")
+    dt, rd = _io_dtype(dy), _res_dtype(res_out.dtype)
+    g = dict(grads or {})
+    names = [("dx", res_out.shape, dy.dtype)]
+    if want_dres or "dres" in g:
+        names.append(("dres", res_out.shape, res_out.dtype))
+    for n in ("dw_pre", "dw_post"):
+        if want_dw or n in g:
+            names.append((n, (width,), torch.float32))
+    lib = load_library()
+    with _scope(stream, res_out, x, w_pre, w_post, dy, dres_out, workspace, *g.values()):
+        _fill(g, names, res_out.device)
+        need = 0
+        if "dw_pre" in g or "dw_post" in g:
+            need = lib.ssm_residual_norm_bwd_workspace_size(rows, width)
+        workspace, have = _workspace(workspace, need, res_out.device, "ssm_residual_norm_bwd")
+        xp, xs = (None, 0) if x is None else _steps(x, "x")
+        rc = lib.ssm_residual_norm_bwd(
+            xp, _dense(res_out, "res_out"), _dense(w_pre, "w_pre"), _dense(w_post, "w_post"), _dense(dy, "dy"),
+            _dense(dres_out, "dres_out"), _dense(g["dx"], "dx"), _dense(g.get("dres"), "dres"),
+            _dense(g.get("dw_pre"), "dw_pre"), _dense(g.get("dw_post"), "dw_post"), rows, width, xs, alpha, eps,
+            1 if post_norm else 0, dt, rd, _dense(workspace, "workspace"), have, _here(res_out))
+    if rc != SSM_OK:
+        raise SsmError(rc, "ssm_residual_norm_bwd")
     return g

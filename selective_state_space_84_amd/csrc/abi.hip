@@ -2,6 +2,7 @@
 // dispatch to the gfx950 kernels.  Every check runs on the host before any
 // HIP call, so a rejected call has no side effects.
 #include "ssm_scan.h"
+#include "abi_checks.h"
 #include "attn_launch.h"
 #include "ssm_internal.h"
 
@@ -31,27 +32,9 @@ constexpr int64_t kTargetWaves = 2048;
 constexpr int64_t kChunkTargetWaves = 16384;
 // Shortest chunk the automatic plan will cut a sequence into.
 constexpr int64_t kMinAutoChunk = 64;
-// Workspace alignment the library asks for.
-constexpr uintptr_t kWorkspaceAlign = 256;
 constexpr uint32_t kKnownFlags = SSM_FLAG_DELTA_SOFTPLUS | SSM_FLAG_EXACT_ZOH | SSM_FLAG_A_LINEAR_N;
 
-bool mul3(int64_t a, int64_t b, int64_t c, int64_t* out) {
-  int64_t t;
-  if (__builtin_mul_overflow(a, b, &t)) return false;
-  if (__builtin_mul_overflow(t, c, out)) return false;
-  return true;
-}
-
 bool is_pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// Byte ranges [p, p+n) and [q, q+m) overlap (empty ranges never overlap).
-bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
-  if (p == nullptr || q == nullptr || n <= 0 || m <= 0) return false;
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + (uintptr_t)m && b < a + (uintptr_t)n;
-}
 
 struct Plan {
   int32_t n_split;
@@ -547,38 +530,6 @@ int conv_impl(const void* x, const float* w, const float* bias, const float* sta
 }
 
 // ---- linear attention and the query/key norm with rotation ---------------
-
-// Rows of a tensor read in place from a wider one: `rows` rows of `width`
-// bytes, `stride` bytes apart.
-struct Rows {
-  const void* p;
-  int64_t rows, width, stride;
-};
-
-// Some byte of x is also one of y.  Two tensors of the same stride may be
-// column ranges of one buffer, whose extents overlap although their rows do not.
-bool overlap(const Rows& x, const Rows& y) {
-  if (x.p == nullptr || y.p == nullptr || x.rows <= 0 || y.rows <= 0 || x.width <= 0 || y.width <= 0) return false;
-  if (!overlap(x.p, (x.rows - 1) * x.stride + x.width, y.p, (y.rows - 1) * y.stride + y.width)) return false;
-  if (x.stride != y.stride || x.rows == 1 || y.rows == 1) return true;
-  const int64_t s = x.stride;
-  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(y.p) - reinterpret_cast<uintptr_t>(x.p)) % s;
-  const int64_t off = d < 0 ? d + s : d;  // y's first byte within x's rows
-  return off < x.width || off + y.width > s;
-}
-
-Rows dense(const void* p, int64_t bytes) { return Rows{p, 1, bytes, bytes}; }
-
-// Outputs against the inputs, each other and the workspace.
-int check_alias(const Rows* outs, int n_out, const Rows* ins, int n_in) {
-  for (int o = 0; o < n_out; ++o) {
-    for (int k = 0; k < n_in; ++k)
-      if (overlap(outs[o], ins[k])) return SSM_ERR_ALIAS;
-    for (int k = o + 1; k < n_out; ++k)
-      if (overlap(outs[o], outs[k])) return SSM_ERR_ALIAS;
-  }
-  return SSM_OK;
-}
 
 // A block of 64 rows is addressed with 32-bit byte offsets.
 constexpr int64_t kMaxStride = (int64_t)1 << 23;

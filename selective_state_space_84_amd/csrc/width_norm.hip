@@ -1,0 +1,684 @@
+// Norms over a layer's width: the gated norm behind a mixer, the residual update
+// with the norms before and after a block, and their gradients.
+//
+//   gated norm:    t = x s(z), y = w t r;  or t = x, y = w t r s(z)
+//   residual norm: n = w_post x r_x (or w_post x), R = residual + alpha n, y = w_pre R r_R
+// with s(z) = z / (1 + e^-z) and r = 1 / sqrt(mean(t^2) + eps) over a group.
+// Gradient of n = w t r:  dt = r (w g) - t r^3 mean(w g t),  dw = sum g t r.
+//
+// A group of values belongs to a team of lanes that holds it in registers: 8, 16,
+// 32 or 64 lanes of a wave, or a whole workgroup whose size follows the group.
+// Every value is read once.
+#include "gated_launch.h"
+#include "ssm_device.h"
+
+namespace ssm {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Eight values of one lane.  VEC: neighbours, in 16-byte accesses.  Else: one by one,
+// `step` apart, so that the lanes of a team read neighbours; those from `left`
+// on do not exist.
+template <typename T, bool VEC>
+struct Eight;
+template <>
+struct Eight<float, true> {
+  u32x4 a[2];
+  __device__ __forceinline__ void zero() { a[0] = a[1] = u32x4{0, 0, 0, 0}; }
+  __device__ __forceinline__ void load(const float* p, int, int) {
+    a[0] = *reinterpret_cast<const u32x4*>(p);
+    a[1] = *reinterpret_cast<const u32x4*>(p + 4);
+  }
+  __device__ __forceinline__ float get(int j) const {
+    const uint32_t v = a[j / 4][j % 4];
+    return __builtin_bit_cast(float, v);
+  }
+};
+template <>
+struct Eight<uint16_t, true> {
+  u32x4 a;
+  __device__ __forceinline__ void zero() { a = u32x4{0, 0, 0, 0}; }
+  __device__ __forceinline__ void load(const uint16_t* p, int, int) { a = *reinterpret_cast<const u32x4*>(p); }
+  __device__ __forceinline__ float get(int j) const {
+    const uint32_t v = a[j / 2];
+    return __builtin_bit_cast(float, j % 2 ? v & 0xffff0000u : v << 16);
+  }
+};
+template <typename T>
+struct Eight<T, false> {
+  T a[8];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = T(0);
+  }
+  __device__ __forceinline__ void load(const T* p, int step, int left) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = j * step < left ? p[j * step] : T(0);
+  }
+  __device__ __forceinline__ float get(int j) const { return io_to_f32(a[j]); }
+};
+
+template <bool VEC>
+__device__ __forceinline__ void put8(float* p, const float* v, int step, int left) {
+  if constexpr (VEC) {
+    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j * step < left) p[j * step] = v[j];
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void put8(uint16_t* p, const float* v, int step, int left) {
+  if constexpr (VEC) {
+    u32x4 r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      r[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2 * k], v[2 * k + 1]}, bf16x2));
+    *reinterpret_cast<u32x4*>(p) = r;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j * step < left) io_store(p + j * step, v[j]);
+  }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+
+// Sum over aligned groups of G lanes (8 at least), in every lane.
+template <int G>
+__device__ __forceinline__ float lane_sum(float v) {
+  v += dpp<0xB1>(v);              // quad_perm 1 0 3 2
+  v += dpp<0x4E>(v);              // quad_perm 2 3 0 1
+  v += dpp<0x141>(v);             // row_half_mirror
+  if (G > 8) v += dpp<0x140>(v);  // row_mirror
+  if (G > 16) v += __shfl_xor(v, 16);
+  if (G > 32) v += __shfl_xor(v, 32);
+  return v;
+}
+
+// A lane's place: TEAM lanes a group (0: the whole workgroup), NV pieces of 8
+// values a lane.  Team q of all takes group q % groups of rows q / groups,
+// q / groups + dr, ...
+constexpr int kMaxWaves = 16;
+template <int TEAM, int NV, bool VEC>
+struct Place {
+  int lanes, ln, dim;  // lanes of the team, this one, values of a group
+  int64_t team, row, dr, col;  // col: the group's first value in its row
+  int phase = 0;
+  float (*red)[2][kMaxWaves];
+  __device__ __forceinline__ Place(int dim_, int64_t groups, float (*red_)[2][kMaxWaves]) : dim(dim_), red(red_) {
+    lanes = TEAM > 0 ? TEAM : (int)blockDim.x;
+    ln = TEAM > 0 ? (int)threadIdx.x % (TEAM > 0 ? TEAM : 1) : (int)threadIdx.x;
+    const int per = TEAM > 0 ? (int)blockDim.x / (TEAM > 0 ? TEAM : 1) : 1;
+    team = (int64_t)blockIdx.x * per + (TEAM > 0 ? (int)threadIdx.x / (TEAM > 0 ? TEAM : 1) : 0);
+    row = team / groups;
+    col = (team % groups) * dim;
+    dr = (int64_t)gridDim.x * per / groups;
+  }
+  // Piece v: its first value within the group, the values' distance, and how many of the group are left from there.
+  __device__ __forceinline__ int at(int v) const { return VEC ? (v * lanes + ln) * 8 : v * 8 * lanes + ln; }
+  __device__ __forceinline__ int step() const { return VEC ? 1 : lanes; }
+  __device__ __forceinline__ int left(int v) const { return dim - at(v); }
+  template <typename E, typename T>
+  __device__ __forceinline__ void load(E& e, const T* p, int v) const {
+    if (left(v) > 0)
+      e.load(p + at(v), step(), left(v));
+    else
+      e.zero();
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* p, const float* x, int v) const {
+    if (left(v) > 0) put8<VEC>(p + at(v), x, step(), left(v));
+  }
+  __device__ __forceinline__ void weights(float (&w)[NV][8], const float* p) const {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      Eight<float, VEC> e;
+      if (p != nullptr) load(e, p + col, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[v][j] = p != nullptr ? e.get(j) : 1.0f;
+    }
+  }
+  // Sums over the team, in every lane of it.  The waves' sums change places between two
+  // halves, so that one barrier a sum is enough.
+  __device__ __forceinline__ void sum(float& x, float& y, bool two) {
+    constexpr int W = TEAM > 0 ? TEAM : 64;
+    x = lane_sum<W>(x);
+    if (two) y = lane_sum<W>(y);
+    if constexpr (TEAM == 0) {
+      const int waves = (int)blockDim.x / 64;
+      float(*const r)[kMaxWaves] = red[phase];
+      phase ^= 1;
+      if (threadIdx.x % 64 == 0) {
+        r[0][threadIdx.x / 64] = x;
+        if (two) r[1][threadIdx.x / 64] = y;
+      }
+      __syncthreads();
+      x = 0.0f;
+      y = two ? 0.0f : y;
+      for (int i = 0; i < waves; ++i) {
+        x += r[0][i];
+        if (two) y += r[1][i];
+      }
+    }
+  }
+  __device__ __forceinline__ float sum(float x) {
+    float y = 0.0f;
+    sum(x, y, false);
+    return x;
+  }
+};
+
+struct NormArgs {
+  const void* x;
+  const void* z;
+  const float* w;
+  void* y;
+  int64_t rows, width, groups, xs, zs;
+  float eps;
+  const void* dy;
+  void* dz;
+  float* part;
+};
+
+template <typename T, bool VEC, int TEAM, int NV, bool Z, bool FIRST>
+__global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_gated_norm(const NormArgs a) {
+  __shared__ float red[2][2][kMaxWaves];
+  Place<TEAM, NV, VEC> at((int)(a.width / a.groups), a.groups, red);
+  const float inv = 1.0f / (float)at.dim;
+  float w[NV][8];
+  at.weights(w, a.w);
+  for (int64_t r = at.row; r < a.rows; r += at.dr) {
+    const T* const xp = static_cast<const T*>(a.x) + r * a.xs + at.col;
+    const T* const zp = static_cast<const T*>(a.z) + r * a.zs + at.col;
+    Eight<T, VEC> x[NV], z[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      at.load(x[v], xp, v);
+      if (Z) at.load(z[v], zp, v);
+    }
+    float t[NV][8], ss = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        t[v][j] = x[v].get(j);
+        if (Z && FIRST) t[v][j] *= silu(z[v].get(j));
+        ss = __builtin_fmaf(t[v][j], t[v][j], ss);
+      }
+    const float rs = __builtin_amdgcn_rsqf(__builtin_fmaf(at.sum(ss), inv, a.eps));
+    T* const yp = static_cast<T*>(a.y) + r * a.width + at.col;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        t[v][j] *= rs * w[v][j];
+        if (Z && !FIRST) t[v][j] *= silu(z[v].get(j));
+      }
+      at.store(yp, t[v], v);
+    }
+  }
+}
+
+// Adds g t r to the sums of dw, turns g into the gradient of t.
+template <int NV>
+struct NormGrad {
+  float rs, c;
+  __device__ __forceinline__ void take(float ss, float sg, float inv, float eps) {
+    rs = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, inv, eps));
+    c = sg * inv * rs * rs;
+  }
+  __device__ __forceinline__ float operator()(float t, float wg) const { return rs * __builtin_fmaf(-t, c, wg); }
+};
+
+template <typename T, bool VEC, int TEAM, int NV, bool Z, bool FIRST>
+__global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_gated_norm_bwd(const NormArgs a) {
+  __shared__ float red[2][2][kMaxWaves];
+  Place<TEAM, NV, VEC> at((int)(a.width / a.groups), a.groups, red);
+  const float inv = 1.0f / (float)at.dim;
+  float w[NV][8], dw[NV][8] = {};
+  at.weights(w, a.w);
+  for (int64_t r = at.row; r < a.rows; r += at.dr) {
+    Eight<T, VEC> x[NV], z[NV], dy[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      at.load(x[v], static_cast<const T*>(a.x) + r * a.xs + at.col, v);
+      if (Z) at.load(z[v], static_cast<const T*>(a.z) + r * a.zs + at.col, v);
+      at.load(dy[v], static_cast<const T*>(a.dy) + r * a.width + at.col, v);
+    }
+    float ss = 0.0f, sg = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float t = x[v].get(j), g = dy[v].get(j);
+        if (Z) {
+          const float s = silu(z[v].get(j));
+          (FIRST ? t : g) *= s;
+        }
+        ss = __builtin_fmaf(t, t, ss);
+        sg = __builtin_fmaf(w[v][j] * g, t, sg);
+      }
+    at.sum(ss, sg, true);
+    NormGrad<NV> n;
+    n.take(ss, sg, inv, a.eps);
+    T* const dx = static_cast<T*>(a.y) + r * a.width + at.col;
+    T* const dz = static_cast<T*>(a.dz) + r * a.width + at.col;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float ox[8], oz[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float xv = x[v].get(j), dv = dy[v].get(j);
+        if (Z) {
+          const float zv = z[v].get(j), q = hw_rcp(1.0f + hw_exp2(-zv * kLog2e));
+          const float s = zv * q, slope = q * __builtin_fmaf(zv, 1.0f - q, 1.0f);
+          const float t = FIRST ? xv * s : xv, g = FIRST ? dv : dv * s;
+          const float dt = n(t, w[v][j] * g);
+          dw[v][j] = __builtin_fmaf(g * t, n.rs, dw[v][j]);
+          ox[j] = FIRST ? dt * s : dt;
+          oz[j] = (FIRST ? dt * xv : dv * (w[v][j] * (t * n.rs))) * slope;
+        } else {
+          dw[v][j] = __builtin_fmaf(dv * xv, n.rs, dw[v][j]);
+          ox[j] = n(xv, w[v][j] * dv);
+        }
+      }
+      at.store(dx, ox, v);
+      if (Z) at.store(dz, oz, v);
+    }
+  }
+  if (a.part == nullptr || at.row >= a.rows) return;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) at.store(a.part + at.team * at.dim, dw[v], v);
+}
+
+struct ResArgs {
+  const void* x;
+  const void* res;
+  const float* w_pre;
+  const float* w_post;
+  void* res_out;
+  void* y;
+  int64_t rows, width, xs;
+  float alpha, eps;
+  const void* dy;
+  const void* dres_out;
+  void* dx;
+  void* dres;
+  float* part;
+  int64_t part_post;  // floats before the sums of dw_post
+};
+
+template <typename T, typename R, bool VEC, int TEAM, int NV, bool POST>
+__global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_residual_norm(const ResArgs a) {
+  __shared__ float red[2][2][kMaxWaves];
+  Place<TEAM, NV, VEC> at((int)a.width, 1, red);
+  const float inv = 1.0f / (float)at.dim;
+  float wo[NV][8], wp[NV][8];
+  at.weights(wo, a.w_post);
+  at.weights(wp, a.w_pre);
+  for (int64_t r = at.row; r < a.rows; r += at.dr) {
+    Eight<T, VEC> x[NV];
+    Eight<R, VEC> e[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      at.load(x[v], static_cast<const T*>(a.x) + r * a.xs, v);
+      if (a.res != nullptr)
+        at.load(e[v], static_cast<const R*>(a.res) + r * a.width, v);
+      else
+        e[v].zero();
+    }
+    float c = a.alpha;
+    if (POST) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(x[v].get(j), x[v].get(j), ss);
+      c *= __builtin_amdgcn_rsqf(__builtin_fmaf(at.sum(ss), inv, a.eps));
+    }
+    float t[NV][8], ss = 0.0f;
+    R* const rp = static_cast<R*>(a.res_out) + r * a.width;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        t[v][j] = __builtin_fmaf(c * x[v].get(j), wo[v][j], e[v].get(j));
+        // Behind the group there are only zeros (with weights of 1): they add nothing.
+        ss = __builtin_fmaf(t[v][j], t[v][j], ss);
+      }
+      at.store(rp, t[v], v);
+    }
+    const float rs = __builtin_amdgcn_rsqf(__builtin_fmaf(at.sum(ss), inv, a.eps));
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[v][j] *= rs * wp[v][j];
+      at.store(static_cast<T*>(a.y) + r * a.width, t[v], v);
+    }
+  }
+}
+
+template <typename T, typename R, bool VEC, int TEAM, int NV, bool POST>
+__global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_residual_norm_bwd(const ResArgs a) {
+  __shared__ float red[2][2][kMaxWaves];
+  Place<TEAM, NV, VEC> at((int)a.width, 1, red);
+  const float inv = 1.0f / (float)at.dim;
+  float wo[NV][8], wp[NV][8], dwo[NV][8] = {}, dwp[NV][8] = {};
+  at.weights(wo, a.w_post);
+  at.weights(wp, a.w_pre);
+  for (int64_t r = at.row; r < a.rows; r += at.dr) {
+    Eight<T, VEC> x[NV], dy[NV];
+    Eight<R, VEC> e[NV], de[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (a.x != nullptr)
+        at.load(x[v], static_cast<const T*>(a.x) + r * a.xs, v);
+      else
+        x[v].zero();
+      at.load(dy[v], static_cast<const T*>(a.dy) + r * a.width, v);
+      at.load(e[v], static_cast<const R*>(a.res) + r * a.width, v);
+      if (a.dres_out != nullptr)
+        at.load(de[v], static_cast<const R*>(a.dres_out) + r * a.width, v);
+      else
+        de[v].zero();
+    }
+    float ss = 0.0f, sg = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float t = e[v].get(j);
+        ss = __builtin_fmaf(t, t, ss);
+        sg = __builtin_fmaf(wp[v][j] * dy[v].get(j), t, sg);
+      }
+    at.sum(ss, sg, true);
+    NormGrad<NV> n;
+    n.take(ss, sg, inv, a.eps);
+    // The gradient of the sum, then of what was added.
+    float g[NV][8], sx = 0.0f, sp = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float t = e[v].get(j), d = dy[v].get(j);
+        dwp[v][j] = __builtin_fmaf(d * t, n.rs, dwp[v][j]);
+        g[v][j] = n(t, wp[v][j] * d) + de[v].get(j);
+      }
+      if (a.dres != nullptr) at.store(static_cast<R*>(a.dres) + r * a.width, g[v], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        g[v][j] *= a.alpha;
+        if (POST) {
+          const float t = x[v].get(j);
+          sx = __builtin_fmaf(t, t, sx);
+          sp = __builtin_fmaf(wo[v][j] * g[v][j], t, sp);
+        }
+      }
+    }
+    NormGrad<NV> m;
+    m.rs = 1.0f;
+    m.c = 0.0f;
+    if (POST) {
+      at.sum(sx, sp, true);
+      m.take(sx, sp, inv, a.eps);
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float t = x[v].get(j);
+        dwo[v][j] = __builtin_fmaf(g[v][j] * t, m.rs, dwo[v][j]);
+        g[v][j] = POST ? m(t, wo[v][j] * g[v][j]) : wo[v][j] * g[v][j];
+      }
+      at.store(static_cast<T*>(a.dx) + r * a.width, g[v], v);
+    }
+  }
+  if (a.part == nullptr || at.row >= a.rows) return;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    at.store(a.part + at.team * at.dim, dwp[v], v);
+    at.store(a.part + a.part_post + at.team * at.dim, dwo[v], v);
+  }
+}
+
+// dw[c] = sum over the teams' rows of part, in a fixed order: 16 columns a workgroup, 64
+// interleaved sums a column (eight loads of each on their way), joined pairwise.
+__global__ void __launch_bounds__(1024) k_norm_sum(const float* part, float* dw0, float* dw1, int64_t second,
+                                                   int32_t n, int64_t width) {
+  __shared__ float s[64][17];
+  float* const dw = blockIdx.y == 0 ? dw0 : dw1;
+  if (dw == nullptr) return;
+  const int c = threadIdx.x & 15, k0 = threadIdx.x >> 4;
+  const int64_t col = (int64_t)blockIdx.x * 16 + c;
+  const float* const p = part + (blockIdx.y == 0 ? 0 : second) + col;
+  float v = 0.0f;
+  if (col < width)
+    for (int k = k0; k < n; k += 8 * 64) {
+      float q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = k + 64 * i < n ? p[(int64_t)(k + 64 * i) * width] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v += q[i];
+    }
+  for (int d = 32; d > 0; d /= 2) {
+    s[k0][c] = v;
+    __syncthreads();
+    if (k0 < d) v += s[k0 + d][c];
+    __syncthreads();
+  }
+  if (k0 == 0 && col < width) dw[col] = v;
+}
+
+// The shape of a launch: lanes a team (0: the workgroup), pieces a lane, threads and
+// workgroups.
+struct Shape {
+  int team, nv, threads;
+  int64_t teams;  // a multiple of the groups
+  unsigned grid;
+};
+
+constexpr int64_t kThreads = 256 * 1024;  // lanes in flight
+
+// rows x groups teams of work; most: teams that may be launched at most per group.
+Shape shape_of(int64_t rows, int64_t dim, int64_t groups) {
+  Shape s{};
+  const int64_t pieces = (dim + 7) / 8;
+  if (pieces <= 64) {
+    s.team = pieces <= 8 ? 8 : pieces <= 16 ? 16 : pieces <= 32 ? 32 : 64;
+    s.nv = 1;
+    s.threads = 256;
+  } else {
+    s.team = 0;
+    s.nv = pieces <= 1024 ? 1 : 2;
+    s.threads = (int)((pieces + 64 * s.nv - 1) / (64 * s.nv) * 64);
+  }
+  const int per = s.team > 0 ? s.threads / s.team : 1;
+  // Teams: what the chip holds, no more than there is work, whole workgroups and whole rows of groups.
+  int64_t rows_at_once = kThreads / s.threads * per / groups;
+  if (rows_at_once > rows) rows_at_once = rows;
+  if (rows_at_once < 1) rows_at_once = 1;
+  while (rows_at_once * groups % per != 0) ++rows_at_once;
+  s.teams = rows_at_once * groups;
+  s.grid = (unsigned)(s.teams / per);
+  return s;
+}
+
+// f(team, pieces) with both as constants.
+template <typename F>
+hipError_t by_shape(const Shape& s, F f) {
+  using std::integral_constant;
+  switch (s.team) {
+    case 8: return f(integral_constant<int, 8>(), integral_constant<int, 1>());
+    case 16: return f(integral_constant<int, 16>(), integral_constant<int, 1>());
+    case 32: return f(integral_constant<int, 32>(), integral_constant<int, 1>());
+    case 64: return f(integral_constant<int, 64>(), integral_constant<int, 1>());
+    default:
+      return s.nv == 1 ? f(integral_constant<int, 0>(), integral_constant<int, 1>())
+                       : f(integral_constant<int, 0>(), integral_constant<int, 2>());
+  }
+}
+
+bool at16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+bool whole(const GatedNormLaunch& p) {
+  const int64_t es = p.bf16 ? 2 : 4;
+  return p.width / p.groups % 8 == 0 && p.x_stride * es % 16 == 0 && (p.z == nullptr || p.z_stride * es % 16 == 0) &&
+         at16(p.x) && at16(p.z) && at16(p.w) && at16(p.y) && at16(p.dy) && at16(p.dz);
+}
+bool whole(const ResidualNormLaunch& p) {
+  const int64_t es = p.bf16 ? 2 : 4;
+  return p.width % 8 == 0 && p.x_stride * es % 16 == 0 && at16(p.x) && at16(p.residual) && at16(p.w_pre) &&
+         at16(p.w_post) && at16(p.res_out) && at16(p.y) && at16(p.dy) && at16(p.dres_out) && at16(p.dx) &&
+         at16(p.dres);
+}
+
+template <typename F>
+hipError_t by_bool(bool v, F f) {
+  return v ? f(std::true_type()) : f(std::false_type());
+}
+
+NormArgs args(const GatedNormLaunch& p) {
+  NormArgs a{};
+  a.x = p.x;
+  a.z = p.z;
+  a.w = p.w;
+  a.y = p.y;
+  a.rows = p.rows;
+  a.width = p.width;
+  a.groups = p.groups;
+  a.xs = p.x_stride;
+  a.zs = p.z_stride;
+  a.eps = p.eps;
+  a.dy = p.dy;
+  a.dz = p.dz;
+  return a;
+}
+ResArgs args(const ResidualNormLaunch& p) {
+  ResArgs a{};
+  a.x = p.x;
+  a.res = p.residual;
+  a.w_pre = p.w_pre;
+  a.w_post = p.w_post;
+  a.res_out = p.res_out;
+  a.y = p.y;
+  a.rows = p.rows;
+  a.width = p.width;
+  a.xs = p.x_stride;
+  a.alpha = p.alpha;
+  a.eps = p.eps;
+  a.dy = p.dy;
+  a.dres_out = p.dres_out;
+  a.dx = p.dx;
+  a.dres = p.dres;
+  return a;
+}
+
+template <bool GRAD, typename T>
+hipError_t go_gated(const GatedNormLaunch& p, const NormArgs& a, const Shape& s) {
+  return by_shape(s, [&](auto team, auto nv) {
+    return by_bool(whole(p), [&](auto vec) {
+      return by_bool(p.z != nullptr, [&](auto z) {
+        return by_bool(p.gate_first, [&](auto first) {
+          constexpr int TEAM = decltype(team)::value, NV = decltype(nv)::value;
+          constexpr bool VEC = decltype(vec)::value, Z = decltype(z)::value, FIRST = decltype(first)::value || !Z;
+          if constexpr (GRAD)
+            return launch(k_gated_norm_bwd<T, VEC, TEAM, NV, Z, FIRST>, dim3(s.grid), dim3(s.threads), 0, p.stream, a);
+          else
+            return launch(k_gated_norm<T, VEC, TEAM, NV, Z, FIRST>, dim3(s.grid), dim3(s.threads), 0, p.stream, a);
+        });
+      });
+    });
+  });
+}
+
+template <bool GRAD, typename T, typename R>
+hipError_t go_residual(const ResidualNormLaunch& p, const ResArgs& a, const Shape& s) {
+  return by_shape(s, [&](auto team, auto nv) {
+    return by_bool(whole(p), [&](auto vec) {
+      return by_bool(p.post_norm, [&](auto post) {
+        constexpr int TEAM = decltype(team)::value, NV = decltype(nv)::value;
+        constexpr bool VEC = decltype(vec)::value, POST = decltype(post)::value;
+        if constexpr (GRAD)
+          return launch(k_residual_norm_bwd<T, R, VEC, TEAM, NV, POST>, dim3(s.grid), dim3(s.threads), 0, p.stream, a);
+        else
+          return launch(k_residual_norm<T, R, VEC, TEAM, NV, POST>, dim3(s.grid), dim3(s.threads), 0, p.stream, a);
+      });
+    });
+  });
+}
+
+hipError_t sum_parts(const float* part, float* dw0, float* dw1, int64_t second, int64_t n, int64_t width,
+                     hipStream_t stream) {
+  return launch(k_norm_sum, dim3((unsigned)((width + 15) / 16), 2), dim3(1024), 0, stream, part, dw0, dw1, second,
+                (int32_t)n, width);
+}
+
+// Rows of sums: the teams of one group, those without a row left out.
+int64_t parts_of(const Shape& s, int64_t rows, int64_t groups) {
+  const int64_t n = s.teams / groups;
+  return n < rows ? n : rows;
+}
+
+}  // namespace
+
+int64_t gated_norm_bwd_floats(int64_t rows, int64_t width, int64_t groups) {
+  return rows == 0 ? 0 : parts_of(shape_of(rows, width / groups, groups), rows, groups) * width;
+}
+int64_t residual_norm_bwd_floats(int64_t rows, int64_t width) {
+  return rows == 0 ? 0 : 2 * parts_of(shape_of(rows, width, 1), rows, 1) * width;
+}
+
+hipError_t launch_gated_norm(const GatedNormLaunch& p) {
+  const Shape s = shape_of(p.rows, p.width / p.groups, p.groups);
+  const NormArgs a = args(p);
+  return p.bf16 ? go_gated<false, uint16_t>(p, a, s) : go_gated<false, float>(p, a, s);
+}
+
+hipError_t launch_gated_norm_bwd(const GatedNormLaunch& p) {
+  int64_t n = 0;
+  if (p.rows > 0) {
+    const Shape s = shape_of(p.rows, p.width / p.groups, p.groups);
+    NormArgs a = args(p);
+    a.part = p.dw != nullptr ? p.workspace : nullptr;
+    n = parts_of(s, p.rows, p.groups);
+    const hipError_t rc = p.bf16 ? go_gated<true, uint16_t>(p, a, s) : go_gated<true, float>(p, a, s);
+    if (rc != hipSuccess) return rc;
+  }
+  return p.dw == nullptr ? hipSuccess : sum_parts(p.workspace, p.dw, nullptr, 0, n, p.width, p.stream);
+}
+
+hipError_t launch_residual_norm(const ResidualNormLaunch& p) {
+  const Shape s = shape_of(p.rows, p.width, 1);
+  const ResArgs a = args(p);
+  if (!p.bf16) return go_residual<false, float, float>(p, a, s);
+  return p.res_bf16 ? go_residual<false, uint16_t, uint16_t>(p, a, s) : go_residual<false, uint16_t, float>(p, a, s);
+}
+
+hipError_t launch_residual_norm_bwd(const ResidualNormLaunch& p) {
+  const bool want = p.dw_pre != nullptr || p.dw_post != nullptr;
+  int64_t n = 0, second = 0;
+  if (p.rows > 0) {
+    const Shape s = shape_of(p.rows, p.width, 1);
+    ResArgs a = args(p);
+    a.part = want ? p.workspace : nullptr;
+    n = parts_of(s, p.rows, 1);
+    a.part_post = second = n * p.width;
+    const hipError_t rc = !p.bf16 ? go_residual<true, float, float>(p, a, s)
+                          : p.res_bf16 ? go_residual<true, uint16_t, uint16_t>(p, a, s)
+                                       : go_residual<true, uint16_t, float>(p, a, s);
+    if (rc != hipSuccess) return rc;
+  }
+  return want ? sum_parts(p.workspace, p.dw_pre, p.dw_post, second, n, p.width, p.stream) : hipSuccess;
+}
+
+}  // namespace ssm
