@@ -596,7 +596,7 @@ size_t ssm_qk_norm_rope_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_
  *                apart, so that each may be a column range of one projection's
  *                output; 0 stands for width.  Aligned to their elements; faster
  *                where widths, strides and addresses are multiples of 4 bytes.
- *                Strides not below width and at most 2^40.
+ *                Strides not below width and at most 2^25.
  *   log_a      : [width] fp32, <= 0 and finite: the log of the strongest decay.
  *                Where 1 - a^2 is below fp32's normal range (and for log_a > 0)
  *                the input counts as nothing.
@@ -671,7 +671,7 @@ size_t ssm_gated_scan_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t 
  *             its y is zero.  The used values must differ: of two requests with
  *             one slot, that slot's state and both outputs are unspecified.
  *   x, ga, gx, z : [batch][width] io_dtype, rows x_stride, ... elements apart
- *             (0: dense); z NULL for no output gate.
+ *             (0: dense; at most 2^40); z NULL for no output gate.
  *   y       : [batch][width] io_dtype, dense; overlaps nothing.
  * batch * width / 256 (each row rounded up) below 2^24.  Equivalent to
  * ssm_gated_scan_fwd with seqlen 1 and h0 = h_last = h[slots].

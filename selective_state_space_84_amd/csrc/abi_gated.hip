@@ -13,7 +13,8 @@ namespace {
 
 constexpr int64_t kMaxSteps = INT32_MAX - 256;
 constexpr int64_t kMaxWidth = (int64_t)1 << 23;
-constexpr int64_t kMaxStep = (int64_t)1 << 40;  // elements between steps
+constexpr int64_t kMaxStep = (int64_t)1 << 40;      // elements between rows
+constexpr int64_t kMaxScanStep = (int64_t)1 << 25;  // and between steps of a scan, which addresses 16 with 32-bit offsets
 constexpr int64_t kMaxStates = (int64_t)1 << 31;
 // Every byte count below stays far inside 64 bits when no tensor has more elements than this.
 constexpr int64_t kMaxElems = (int64_t)1 << 48;
@@ -23,9 +24,9 @@ constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;
 bool dtype_ok(int32_t d) { return d == SSM_DTYPE_F32 || d == SSM_DTYPE_BF16; }
 
 // The distance between steps (0: dense), which must keep `rows` of them in range.
-int check_step(int64_t* stride, int64_t width, int64_t rows) {
+int check_step(int64_t* stride, int64_t width, int64_t rows, int64_t most = kMaxStep) {
   if (*stride == 0) *stride = width;
-  if (*stride < width || *stride > kMaxStep) return SSM_ERR_BAD_DIM;
+  if (*stride < width || *stride > most) return SSM_ERR_BAD_DIM;
   int64_t n;
   if (__builtin_mul_overflow(rows, *stride, &n) || n > kMaxElems * 16) return SSM_ERR_BAD_DIM;
   return SSM_OK;
@@ -39,6 +40,7 @@ int check_scan_dims(int64_t batch, int64_t seqlen, int64_t width) {
     return SSM_ERR_BAD_DIM;
   int64_t tokens;
   if (!mul3(batch, seqlen, 1, &tokens) || tokens > kMaxElems) return SSM_ERR_BAD_DIM;
+  if (ssm::gated_scan_items(batch, seqlen, width) > INT32_MAX) return SSM_ERR_BAD_DIM;
   return SSM_OK;
 }
 
@@ -59,10 +61,10 @@ int gated_scan_impl(ssm::GatedScanLaunch p, int32_t io_dtype, bool grad, size_t 
   if (!dtype_ok(io_dtype)) return SSM_ERR_UNSUPPORTED;
   p.bf16 = io_dtype == SSM_DTYPE_BF16;
   const int64_t es = p.bf16 ? 2 : 4, tokens = p.batch * p.seqlen, n = tokens * p.width, states = p.batch * p.width;
-  if ((rc = check_step(&p.x_stride, p.width, tokens)) != SSM_OK) return rc;
-  if ((rc = check_step(&p.ga_stride, p.width, tokens)) != SSM_OK) return rc;
-  if ((rc = check_step(&p.gx_stride, p.width, tokens)) != SSM_OK) return rc;
-  if (p.z != nullptr && (rc = check_step(&p.z_stride, p.width, tokens)) != SSM_OK) return rc;
+  if ((rc = check_step(&p.x_stride, p.width, tokens, kMaxScanStep)) != SSM_OK) return rc;
+  if ((rc = check_step(&p.ga_stride, p.width, tokens, kMaxScanStep)) != SSM_OK) return rc;
+  if ((rc = check_step(&p.gx_stride, p.width, tokens, kMaxScanStep)) != SSM_OK) return rc;
+  if (p.z != nullptr && (rc = check_step(&p.z_stride, p.width, tokens, kMaxScanStep)) != SSM_OK) return rc;
 
   if (n > 0 && (p.x == nullptr || p.ga == nullptr || p.gx == nullptr)) return SSM_ERR_NULL_ARG;
   if (states > 0 && p.log_a == nullptr) return SSM_ERR_NULL_ARG;

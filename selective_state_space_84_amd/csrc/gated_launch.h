@@ -34,6 +34,7 @@ struct GatedScanLaunch {
 };
 constexpr int kGatedCkpt = 64;  // steps between saved states, [batch][steps / kGatedCkpt, rounded up][width]
 // Floats of workspace and of saved states; sizes must have been checked for overflow.
+int64_t gated_scan_items(int64_t batch, int64_t seqlen, int64_t width);  // pieces of work, at most
 int64_t gated_scan_ckpt_floats(int64_t batch, int64_t seqlen, int64_t width);
 int64_t gated_scan_fwd_floats(int64_t batch, int64_t seqlen, int64_t width, bool bf16);
 int64_t gated_scan_bwd_floats(int64_t batch, int64_t seqlen, int64_t width, bool bf16, bool ckpt_given);

@@ -1,4 +1,26 @@
 // Gated linear recurrence over whole sequences and its gradient.
+//
+// One pass over the data.  A workgroup takes a piece of the sequence, W waves of
+// TS steps each, for 64 V channels (V a lane).  A wave loads its steps at once,
+// forms decays and inputs and folds them to h_out = A h_in + S; the waves' folds
+// meet in LDS, and the piece's fold is published.  The state that enters the
+// piece comes from the pieces before it: pieces are grouped in blocks of
+// kBlock, a block's last piece publishes the state behind the block, and the
+// others fold the (A, S) of the pieces before them in the block onto the state
+// in front of it.  So a sequence's chain is one hop a block long, its sums have a
+// fixed order, and every input is read once.
+//
+// Published words carry their own validity: a word is all ones until it is
+// written, and no (A, S) or state is stored as that pattern.  Relaxed 64 and 32
+// bit atomics at agent scope are therefore enough.  Pieces are handed out by a
+// counter, earlier ones first: who waits for a piece waits for a workgroup that is
+// running, whatever else the device runs.  A wait gives up after kPolls reads (the
+// outputs are NaN then): a workspace that two calls share by mistake cannot hang.
+//
+// The gradient runs the same way from the last piece to the first, on
+// P_t = a_t (e_t + P_{t+1}), e = dy silu(z): what reaches the state before step
+// t.  The states inside a piece are formed again from the state at its
+// start, saved by the forward call or by a forward pass without outputs.
 #include "gated_launch.h"
 #include "gated_math.h"
 
@@ -17,115 +39,531 @@ struct GatedArgs {
   float* h_last;
   float* ckpt;
   int64_t batch, seqlen, width;
-  int64_t xs, as, is, zs;
+  int64_t xs, as, is, zs;  // bytes between steps
   const void* dy;
   const float* dh_last;
   void* dx;
   void* dga;
   void* dgx;
   void* dz;
-  float* part;
+  float* part;  // [batch][pieces][width] sums of dlog_a
   float* dh0;
+  uint32_t* ticket;  // all ones at first
+  uint64_t* folds;   // [batch][pieces][width] (A, S)
+  uint32_t* states;  // [batch][blocks][width]
+  int32_t pieces, tiles, items;
 };
 
-__device__ __forceinline__ int64_t steps_of(const GatedArgs& a, int64_t b) {
-  if (a.lengths == nullptr) return a.seqlen;
-  const int64_t n = a.lengths[b];
-  return n < 0 ? 0 : n > a.seqlen ? a.seqlen : n;
+constexpr int kBlock = 8;  // pieces
+constexpr int kPolls = 1 << 20;
+constexpr uint64_t kNoFold = ~0ull;
+constexpr uint32_t kNoState = ~0u;
+
+__device__ __forceinline__ int steps_of(const GatedArgs& a, int64_t b) {
+  if (a.lengths == nullptr) return (int)a.seqlen;
+  const int n = a.lengths[b];
+  return n < 0 ? 0 : n > (int)a.seqlen ? (int)a.seqlen : n;
 }
 
-template <typename T>
-__device__ __forceinline__ float get(const void* p, int64_t i) {
-  return io_to_f32(static_cast<const T*>(p)[i]);
-}
-template <typename T>
-__device__ __forceinline__ void put(void* p, int64_t i, float v) {
-  io_store(static_cast<T*>(p) + i, v);
-}
-
-// One channel of one row a lane.
-template <typename T>
-__global__ void __launch_bounds__(256) k_gated_fwd(const GatedArgs a) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= a.batch * a.width) return;
-  const int64_t b = id / a.width, d = id % a.width;
-  const int64_t n = steps_of(a, b), nck = (a.seqlen + kGatedCkpt - 1) / kGatedCkpt;
-  const float c2 = a.log_a[d] * kLog2e;
-  float h = a.h0 != nullptr ? a.h0[id] : 0.0f;
-  for (int64_t t = 0; t < a.seqlen; ++t) {
-    const int64_t r = b * a.seqlen + t;
-    if (a.ckpt != nullptr && t % kGatedCkpt == 0) a.ckpt[(b * nck + t / kGatedCkpt) * a.width + d] = h;
-    if (t < n) {
-      const GatedStep s = gated_step(get<T>(a.ga, r * a.as + d), get<T>(a.gx, r * a.is + d), c2);
-      h = __builtin_fmaf(s.a, h, s.m * s.sx * get<T>(a.x, r * a.xs + d));
-      const float gate = a.z != nullptr ? silu(get<T>(a.z, r * a.zs + d)) : 1.0f;
-      if (a.y != nullptr) put<T>(a.y, r * a.width + d, h * gate);
-    } else if (a.y != nullptr) {
-      put<T>(a.y, r * a.width + d, 0.0f);
-    }
+// V values of one lane as loaded.
+template <typename T, int V>
+struct Io {
+  typedef T raw __attribute__((ext_vector_type(V)));
+  raw r;
+  __device__ __forceinline__ void load(const gchar* p, uint32_t off) { r = gldr<raw>(p, off); }
+  __device__ __forceinline__ float get(int v) const { return io_to_f32(r[v]); }
+};
+template <>
+struct Io<uint16_t, 2> {
+  uint32_t r;
+  __device__ __forceinline__ void load(const gchar* p, uint32_t off) { r = gldr<uint32_t>(p, off); }
+  __device__ __forceinline__ float get(int v) const {
+    return __builtin_bit_cast(float, v ? r & 0xffff0000u : r << 16);
   }
-  if (a.h_last != nullptr) a.h_last[id] = h;
+};
+template <int V>
+__device__ __forceinline__ void put(gchar* p, uint32_t off, const float (&v)[V], const float*) {
+  typedef float raw __attribute__((ext_vector_type(V)));
+  raw r;
+#pragma unroll
+  for (int k = 0; k < V; ++k) r[k] = v[k];
+  gstr(p, off, r);
+}
+template <int V>
+__device__ __forceinline__ void put(gchar* p, uint32_t off, const float (&v)[V], const uint16_t*) {
+  if constexpr (V == 1) {
+    gstr(p, off, __builtin_bit_cast(uint16_t, (__bf16)v[0]));
+  } else {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    gstr(p, off, __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[0], v[1]}, b2)));
+  }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_gated_bwd(const GatedArgs a) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= a.batch * a.width) return;
-  const int64_t b = id / a.width, d = id % a.width;
-  const int64_t n = steps_of(a, b), nck = (a.seqlen + kGatedCkpt - 1) / kGatedCkpt;
-  const float la = a.log_a[d], c2 = la * kLog2e;
-  float p = a.dh_last != nullptr ? a.dh_last[id] : 0.0f, sum = 0.0f;
-  for (int64_t c = nck - 1; c >= 0; --c) {
-    const int64_t t0 = c * kGatedCkpt, t1 = min(t0 + kGatedCkpt, a.seqlen);
-    float before[kGatedCkpt];
-    float h = a.ckpt[(b * nck + c) * a.width + d];
-    for (int64_t t = t0; t < min(t1, n); ++t) {
-      const int64_t r = b * a.seqlen + t;
-      before[t - t0] = h;
-      const GatedStep s = gated_step(get<T>(a.ga, r * a.as + d), get<T>(a.gx, r * a.is + d), c2);
-      h = __builtin_fmaf(s.a, h, s.m * s.sx * get<T>(a.x, r * a.xs + d));
-    }
-    for (int64_t t = t1 - 1; t >= t0; --t) {
-      const int64_t r = b * a.seqlen + t, o = r * a.width + d;
-      float dx = 0.0f, dga = 0.0f, dgx = 0.0f, dz = 0.0f;
-      if (t < n) {
-        const GatedStep s = gated_step(get<T>(a.ga, r * a.as + d), get<T>(a.gx, r * a.is + d), c2);
-        const float x = get<T>(a.x, r * a.xs + d), w = s.sx * x;
-        float e = get<T>(a.dy, o);
-        if (a.z != nullptr) {
-          const float z = get<T>(a.z, r * a.zs + d), q = sigmoid(z);
-          const float after = __builtin_fmaf(s.a, before[t - t0], s.m * w);
-          dz = e * after * q * __builtin_fmaf(z, 1.0f - q, 1.0f);
-          e *= z * q;
-        }
-        const float g = e + p;
-        const float gm = g * s.m;
-        const float dla = g * __builtin_fmaf(s.a, before[t - t0], -(s.a * s.a * s.inv_m) * w);
-        dx = gm * s.sx;
-        dgx = dx * x * (1.0f - s.sx);
-        dga = dla * la * s.sa * (1.0f - s.sa);
-        sum = __builtin_fmaf(dla, s.sa, sum);
-        p = s.a * g;
+// Fold of a piece, or of what lies behind it: h_out = a h + s.
+struct Fold {
+  float a, s;
+};
+
+__device__ __forceinline__ float quiet(float v) { return v != v ? __builtin_nanf("") : v; }
+__device__ __forceinline__ void publish(uint64_t* p, Fold f) {
+  const uint64_t w = ((uint64_t)__builtin_bit_cast(uint32_t, quiet(f.s)) << 32) | __builtin_bit_cast(uint32_t, f.a);
+  __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void publish(uint32_t* p, float h) {
+  __hip_atomic_store(p, __builtin_bit_cast(uint32_t, quiet(h)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename W>
+__device__ __forceinline__ W read_word(const W* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// The word when it is there (`first`: what was read before).  Given up, it is all ones, which reads as NaN.
+template <typename W>
+__device__ __forceinline__ W wait_word(const W* p, W first) {
+  W w = first;
+  for (int k = 0; w == (W)~(W)0 && k < kPolls; ++k) {
+    __builtin_amdgcn_s_sleep(1);
+    w = read_word(p);
+  }
+  return w;
+}
+
+// What enters piece q of a chain (counted in the chain's direction, its first piece q0) whose first entry is `first`; fold: this
+// piece's.  Publishes the fold, and behind a block's last piece the state.  folds, states: of piece 0 and
+// block 0 for this lane's channels; fs, ss: words from piece to piece and from block to block.
+template <int V>
+__device__ __forceinline__ void chain(int q, int q0, int last, const float (&first)[V], const Fold (&fold)[V],
+                                      uint64_t* folds, uint32_t* states, int64_t fs, int64_t ss, float (&in)[V]) {
+  const int blk = q / kBlock, j0 = blk * kBlock < q0 ? q0 : blk * kBlock;
+  const bool closes = q % kBlock == kBlock - 1;
+  if (q < last && !closes)
+#pragma unroll
+    for (int v = 0; v < V; ++v) publish(folds + q * fs + v, fold[v]);
+  // All words are asked for at once; most are there.
+  uint64_t w[kBlock - 1][V];
+  uint32_t h[V];
+#pragma unroll
+  for (int k = 0; k < kBlock - 1; ++k)
+    if (j0 + k < q)
+#pragma unroll
+      for (int v = 0; v < V; ++v) w[k][v] = read_word(folds + (j0 + k) * fs + v);
+  if (j0 != q0)
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = read_word(states + (blk - 1) * ss + v);
+#pragma unroll
+  for (int v = 0; v < V; ++v) in[v] = first[v];
+  if (j0 != q0)
+#pragma unroll
+    for (int v = 0; v < V; ++v) in[v] = __builtin_bit_cast(float, wait_word(states + (blk - 1) * ss + v, h[v]));
+#pragma unroll
+  for (int k = 0; k < kBlock - 1; ++k)
+    if (j0 + k < q)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const uint64_t f = wait_word(folds + (j0 + k) * fs + v, w[k][v]);
+        in[v] = __builtin_fmaf(__builtin_bit_cast(float, (uint32_t)f), in[v],
+                               __builtin_bit_cast(float, (uint32_t)(f >> 32)));
       }
-      put<T>(a.dx, o, dx);
-      put<T>(a.dga, o, dga);
-      put<T>(a.dgx, o, dgx);
-      if (a.dz != nullptr) put<T>(a.dz, o, dz);
-    }
+  if (q < last && closes)
+#pragma unroll
+    for (int v = 0; v < V; ++v) publish(states + blk * ss + v, __builtin_fmaf(fold[v].a, in[v], fold[v].s));
+}
+
+// The next piece of work of this workgroup: from the counter where pieces wait for
+// each other, else every gridDim.x-th.
+__device__ __forceinline__ int next_item(const GatedArgs& a, int before, int* shared) {
+  if (a.pieces == 1) return before < 0 ? (int)blockIdx.x : before + (int)gridDim.x;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    *shared = (int)(__hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u);
+  __syncthreads();
+  return *shared;
+}
+
+// Where a lane works: channels d .. d + V - 1 of row b (clamped into the row; `on`: they exist).
+template <int V>
+struct Spot {
+  int64_t b, d;
+  int q;
+  bool on;
+  __device__ __forceinline__ Spot(const GatedArgs& a, int item) {
+    const int per = a.tiles * (int)a.batch;  // earlier pieces of every row first
+    q = item / per;
+    const int rt = item % per;
+    b = rt / a.tiles;
+    d = ((int64_t)(rt % a.tiles) * 64 + (threadIdx.x & 63)) * V;
+    on = d < a.width;
+    if (!on) d = a.width - V;
   }
-  if (a.dh0 != nullptr) a.dh0[id] = p;
-  if (a.part != nullptr) a.part[id] = sum;
+};
+
+// Steps t0 .. t0 + m - 1 (1 <= m <= TS) of one input; what lies behind them repeats the last.
+// One base a wave and 32-bit offsets (TS steps lie within 2^31 bytes): bases of their own for every
+// step do not fit the scalar registers.
+template <typename T, int V, int TS>
+__device__ __forceinline__ void load_steps(Io<T, V> (&r)[TS], const void* base, int64_t row, int64_t stride, int64_t d,
+                                           int m) {
+  const gchar* const p = uniform_ptr(static_cast<const char*>(base) + row * stride);
+  const uint32_t off = (uint32_t)(d * sizeof(T)), st = (uint32_t)stride;
+#pragma unroll
+  for (int i = 0; i < TS; ++i) r[i].load(p, off + (uint32_t)min(i, m - 1) * st);
 }
 
-__global__ void __launch_bounds__(256) k_gated_sum(const float* part, float* out, int64_t rows, int64_t width) {
-  const int64_t d = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (d >= width) return;
-  float s = 0.0f;
-  for (int64_t r = 0; r < rows; ++r) s += part[r * width + d];
-  out[d] = s;
+template <typename T, int V, int TS, int W, bool Z, bool OUT>
+__global__ void __launch_bounds__(64 * W) k_gated_fwd(const GatedArgs a) {
+  __shared__ Fold folds[W][64 * V];
+  __shared__ float enters[64 * V];
+  __shared__ int shared;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  for (int item = next_item(a, -1, &shared); item < a.items; item = next_item(a, item, &shared)) {
+    const Spot<V> at(a, item);
+    const int n = steps_of(a, at.b), seqlen = (int)a.seqlen;
+    const int c0 = at.q * (W * TS), t0 = c0 + wave * TS;
+    const int m = min(max(n - t0, 0), TS);
+    const int64_t row = at.b * a.seqlen + t0, st = at.b * a.width + at.d;
+    const bool first = at.q == 0;
+    float h[V];
+    if (c0 < n || first) {
+      float dec[TS][V], u[TS][V];
+      Fold f[V];
+      Io<T, V> z[TS];
+      if (m > 0) {
+        Io<T, V> x[TS], ga[TS], gx[TS];
+        load_steps(ga, a.ga, row, a.as, at.d, m);
+        load_steps(gx, a.gx, row, a.is, at.d, m);
+        load_steps(x, a.x, row, a.xs, at.d, m);
+        float c2[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) c2[v] = a.log_a[at.d + v] * kLog2e;
+#pragma unroll
+        for (int i = 0; i < TS; ++i)
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const GatedStep s = gated_step(ga[i].get(v), gx[i].get(v), c2[v]);
+            dec[i][v] = s.a;
+            u[i][v] = s.m * s.sx * x[i].get(v);
+          }
+        if (Z && OUT) load_steps(z, a.z, row, a.zs, at.d, m);
+      }
+      if (m < TS)
+#pragma unroll
+        for (int i = 0; i < TS; ++i)
+          if (i >= m)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+              dec[i][v] = 1.0f;
+              u[i][v] = 0.0f;
+            }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        f[v] = Fold{dec[0][v], u[0][v]};
+#pragma unroll
+        for (int i = 1; i < TS; ++i) f[v] = Fold{f[v].a * dec[i][v], __builtin_fmaf(dec[i][v], f[v].s, u[i][v])};
+        folds[wave][lane * V + v] = f[v];
+      }
+      __syncthreads();
+      if (wave == 0) {
+        float start[V], in[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          start[v] = a.h0 != nullptr ? a.h0[st + v] : 0.0f;
+          for (int k = 1; k < W; ++k) {
+            const Fold g = folds[k][lane * V + v];
+            f[v] = Fold{f[v].a * g.a, __builtin_fmaf(g.a, f[v].s, g.s)};
+          }
+        }
+        if (a.pieces > 1) {
+          const int last = n > 0 ? (n - 1) / (W * TS) : 0;
+          const int blocks = (a.pieces + kBlock - 1) / kBlock;
+          chain<V>(at.q, 0, last, start, f, a.folds + at.b * a.pieces * a.width + at.d,
+                   a.states + at.b * blocks * a.width + at.d, a.width, a.width, in);
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; ++v) in[v] = start[v];
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) enters[lane * V + v] = in[v];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        h[v] = enters[lane * V + v];
+        for (int k = 0; k < wave; ++k) {
+          const Fold g = folds[k][lane * V + v];
+          h[v] = __builtin_fmaf(g.a, h[v], g.s);
+        }
+      }
+      if (a.ckpt != nullptr && t0 % kGatedCkpt == 0 && t0 < seqlen && at.on) {
+        const int64_t nck = (a.seqlen + kGatedCkpt - 1) / kGatedCkpt;
+        float* const ck = a.ckpt + (at.b * nck + t0 / kGatedCkpt) * a.width + at.d;
+#pragma unroll
+        for (int v = 0; v < V; ++v) ck[v] = h[v];
+      }
+      gchar* const p = uniform_ptr(static_cast<const char*>(a.y) + row * (a.width * sizeof(T)));
+      const uint32_t off = (uint32_t)(at.d * sizeof(T)), ws = (uint32_t)(a.width * sizeof(T));
+#pragma unroll
+      for (int i = 0; i < TS; ++i) {
+        float o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          h[v] = __builtin_fmaf(dec[i][v], h[v], u[i][v]);
+          o[v] = Z && OUT ? h[v] * silu(z[i].get(v)) : h[v];
+          if (i >= m) o[v] = 0.0f;
+        }
+        if (OUT && t0 + i < seqlen && at.on) put<V>(p, off + i * ws, o, static_cast<const T*>(nullptr));
+      }
+      // The last wave carries the state behind the row's last step to the end of its piece.
+      if (a.h_last != nullptr && wave == W - 1 && at.on && (n - 1) / (W * TS) == at.q)
+#pragma unroll
+        for (int v = 0; v < V; ++v) a.h_last[st + v] = h[v];
+    } else if (OUT) {
+      gchar* const p = uniform_ptr(static_cast<const char*>(a.y) + row * (a.width * sizeof(T)));
+      const uint32_t off = (uint32_t)(at.d * sizeof(T)), ws = (uint32_t)(a.width * sizeof(T));
+      const float o[V] = {};
+      for (int i = 0; i < TS && t0 + i < seqlen; ++i)
+        if (at.on) put<V>(p, off + i * ws, o, static_cast<const T*>(nullptr));
+    }
+    __syncthreads();
+  }
 }
 
-GatedArgs args(const GatedScanLaunch& p) {
+template <typename T, int V, int TS, int W, bool Z>
+__global__ void __launch_bounds__(64 * W) k_gated_bwd(const GatedArgs a) {
+  __shared__ Fold fwd[W][64 * V];
+  __shared__ Fold rev[W][64 * V];
+  __shared__ float enters[64 * V];
+  __shared__ int shared;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  for (int item = next_item(a, -1, &shared); item < a.items; item = next_item(a, item, &shared)) {
+    const Spot<V> at(a, item);  // q counts from the sequence's end
+    const int n = steps_of(a, at.b), seqlen = (int)a.seqlen;
+    const int c = a.pieces - 1 - at.q, c0 = c * (W * TS), t0 = c0 + wave * TS;
+    const int m = min(max(n - t0, 0), TS);
+    const int64_t row = at.b * a.seqlen + t0, st = at.b * a.width + at.d;
+    const int64_t ws = a.width * (int64_t)sizeof(T);
+    const uint32_t off = (uint32_t)(at.d * sizeof(T));
+    gchar* const px = uniform_ptr(static_cast<const char*>(a.dx) + row * ws);
+    gchar* const pa = uniform_ptr(static_cast<const char*>(a.dga) + row * ws);
+    gchar* const pi = uniform_ptr(static_cast<const char*>(a.dgx) + row * ws);
+    gchar* const pz = uniform_ptr(static_cast<const char*>(a.dz) + row * ws);
+    const T* const tag = nullptr;
+    float sum[V] = {};
+    if (c0 < n) {
+      Io<T, V> x[TS], dy[TS], z[TS];
+      float sa[TS][V], sx[TS][V], dec[TS][V], mm[TS][V], before[TS][V];
+      float la[V], h[V];
+      Fold f[V], r[V];
+      if (m > 0) {
+        Io<T, V> ga[TS], gx[TS];
+        load_steps(ga, a.ga, row, a.as, at.d, m);
+        load_steps(gx, a.gx, row, a.is, at.d, m);
+        load_steps(x, a.x, row, a.xs, at.d, m);
+        load_steps(dy, a.dy, row, ws, at.d, m);
+        if (Z) load_steps(z, a.z, row, a.zs, at.d, m);
+#pragma unroll
+        for (int v = 0; v < V; ++v) la[v] = a.log_a[at.d + v];
+#pragma unroll
+        for (int i = 0; i < TS; ++i)
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const GatedStep s = gated_step(ga[i].get(v), gx[i].get(v), la[v] * kLog2e);
+            sa[i][v] = s.sa;
+            sx[i][v] = s.sx;
+            dec[i][v] = s.a;
+            mm[i][v] = s.m;
+          }
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        f[v] = r[v] = Fold{1.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < TS; ++i)
+          if (i < m) f[v] = Fold{f[v].a * dec[i][v], __builtin_fmaf(dec[i][v], f[v].s, mm[i][v] * sx[i][v] * x[i].get(v))};
+#pragma unroll
+        for (int i = TS - 1; i >= 0; --i)
+          if (i < m) {
+            const float e = Z ? dy[i].get(v) * silu(z[i].get(v)) : dy[i].get(v);
+            r[v].s = dec[i][v] * (e + r[v].s);
+          }
+        r[v].a = f[v].a;
+        fwd[wave][lane * V + v] = f[v];
+        rev[wave][lane * V + v] = r[v];
+      }
+      __syncthreads();
+      if (wave == W - 1) {
+        // The piece's fold from its last wave to its first.
+        float start[V], in[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          start[v] = a.dh_last != nullptr ? a.dh_last[st + v] : 0.0f;
+          for (int k = W - 2; k >= 0; --k) {
+            const Fold g = rev[k][lane * V + v];
+            r[v] = Fold{r[v].a * g.a, __builtin_fmaf(g.a, r[v].s, g.s)};
+          }
+        }
+        if (a.pieces > 1) {
+          const int q0 = a.pieces - 1 - (n - 1) / (W * TS);
+          const int blocks = (a.pieces + kBlock - 1) / kBlock;
+          chain<V>(at.q, q0, a.pieces - 1, start, r, a.folds + at.b * a.pieces * a.width + at.d,
+                   a.states + at.b * blocks * a.width + at.d, a.width, a.width, in);
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; ++v) in[v] = start[v];
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) enters[lane * V + v] = in[v];
+      }
+      // Meanwhile the states before each step.
+      const int64_t nck = (a.seqlen + kGatedCkpt - 1) / kGatedCkpt;
+      const float* const ck = a.ckpt + (at.b * nck + c0 / kGatedCkpt) * a.width + at.d;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        h[v] = ck[v];
+        for (int k = 0; k < wave; ++k) {
+          const Fold g = fwd[k][lane * V + v];
+          h[v] = __builtin_fmaf(g.a, h[v], g.s);
+        }
+#pragma unroll
+        for (int i = 0; i < TS; ++i) {
+          before[i][v] = h[v];
+          if (i < m) h[v] = __builtin_fmaf(dec[i][v], h[v], mm[i][v] * sx[i][v] * x[i].get(v));
+        }
+      }
+      __syncthreads();
+      float p[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        p[v] = enters[lane * V + v];
+        for (int k = W - 1; k > wave; --k) {
+          const Fold g = rev[k][lane * V + v];
+          p[v] = __builtin_fmaf(g.a, p[v], g.s);
+        }
+      }
+#pragma unroll
+      for (int i = TS - 1; i >= 0; --i) {
+        float dx[V] = {}, da[V] = {}, di[V] = {}, dz[V] = {};
+        if (i < m)
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const float xv = x[i].get(v), s = sa[i][v], t = sx[i][v], ac = dec[i][v], mv = mm[i][v];
+            const float w = t * xv, hb = before[i][v];
+            float e = dy[i].get(v);
+            if (Z) {
+              const float zv = z[i].get(v), q = sigmoid(zv);
+              dz[v] = e * __builtin_fmaf(ac, hb, mv * w) * q * __builtin_fmaf(zv, 1.0f - q, 1.0f);
+              e *= zv * q;
+            }
+            const float g = e + p[v];
+            const float inv = mv > 0.0f ? hw_rcp(mv) : 0.0f;
+            const float dla = g * __builtin_fmaf(ac, hb, -(ac * ac * inv) * w);
+            dx[v] = g * mv * t;
+            di[v] = dx[v] * xv * (1.0f - t);
+            da[v] = dla * la[v] * s * (1.0f - s);
+            sum[v] = __builtin_fmaf(dla, s, sum[v]);
+            p[v] = ac * g;
+          }
+        const uint32_t o = off + (uint32_t)i * (uint32_t)ws;
+        if (t0 + i < seqlen && at.on) {
+          put<V>(px, o, dx, tag);
+          put<V>(pa, o, da, tag);
+          put<V>(pi, o, di, tag);
+          if (Z) put<V>(pz, o, dz, tag);
+        }
+      }
+      if (a.dh0 != nullptr && c == 0 && wave == 0 && at.on)
+#pragma unroll
+        for (int v = 0; v < V; ++v) a.dh0[st + v] = p[v];
+    } else {
+      const float o[V] = {};
+      for (int i = 0; i < TS && t0 + i < seqlen; ++i) {
+        const uint32_t to = off + (uint32_t)i * (uint32_t)ws;
+        if (at.on) {
+          put<V>(px, to, o, tag);
+          put<V>(pa, to, o, tag);
+          put<V>(pi, to, o, tag);
+          if (Z) put<V>(pz, to, o, tag);
+        }
+      }
+      if (a.dh0 != nullptr && c == 0 && wave == 0 && at.on)
+#pragma unroll
+        for (int v = 0; v < V; ++v) a.dh0[st + v] = a.dh_last != nullptr ? a.dh_last[st + v] : 0.0f;
+    }
+    if (a.part != nullptr) {
+      // The waves' sums in their order.
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < V; ++v) fwd[wave][lane * V + v].a = sum[v];
+      __syncthreads();
+      if (wave == 0 && at.on)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float t = 0.0f;
+          for (int k = 0; k < W; ++k) t += fwd[k][lane * V + v].a;
+          a.part[(at.b * a.pieces + c) * a.width + at.d + v] = t;
+        }
+    }
+    __syncthreads();
+  }
+}
+
+// All ones into n 16-byte words.
+__global__ void __launch_bounds__(256) k_gated_clear(uint4* p, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) p[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+}
+
+// out[d] = sum of part's rows in a fixed order: 16 columns a workgroup, 64 interleaved sums a column,
+// joined pairwise.
+__global__ void __launch_bounds__(1024) k_gated_sum(const float* part, float* out, int64_t rows, int64_t width) {
+  __shared__ float s[64][17];
+  const int c = threadIdx.x & 15, k0 = threadIdx.x >> 4;
+  const int64_t col = (int64_t)blockIdx.x * 16 + c;
+  float v = 0.0f;
+  if (col < width)
+    for (int64_t k = k0; k < rows; k += 8 * 64) {
+      float q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = k + 64 * i < rows ? part[(k + 64 * i) * width + col] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v += q[i];
+    }
+  for (int d = 32; d > 0; d /= 2) {
+    s[k0][c] = v;
+    __syncthreads();
+    if (k0 < d) v += s[k0 + d][c];
+    __syncthreads();
+  }
+  if (k0 == 0 && col < width) out[col] = v;
+}
+
+constexpr int kFwdSteps = 16, kFwdWaves = 8;  // 128 steps a piece
+constexpr int kBwdSteps = 8, kBwdWaves = 8;   // 64: every piece starts at a saved state
+static_assert(kBwdSteps * kBwdWaves % kGatedCkpt == 0 && kGatedCkpt % kFwdSteps == 0, "pieces start at saved states");
+constexpr int64_t kMaxGrid = 1 << 20;
+
+int64_t pieces_of(int64_t seqlen, int64_t len) { return seqlen <= len ? 1 : (seqlen + len - 1) / len; }
+int64_t blocks_of(int64_t pieces) { return (pieces + kBlock - 1) / kBlock; }
+// Words of 4 bytes that a chain uses: the counter, the folds, the states.
+constexpr int64_t kTicketWords = 64;
+int64_t chain_words(int64_t batch, int64_t width, int64_t pieces) {
+  if (pieces <= 1) return 0;
+  const int64_t n = kTicketWords + batch * width * (2 * pieces + blocks_of(pieces));
+  return (n + 63) / 64 * 64;
+}
+
+// Two bf16 channels a lane where every row allows 4-byte accesses.
+bool pairs(const GatedScanLaunch& p) {
+  if (!p.bf16 || p.width % 2 != 0) return false;
+  const int64_t strides = p.x_stride | p.ga_stride | p.gx_stride | (p.z != nullptr ? p.z_stride : 0);
+  uintptr_t at = 0;
+  for (const void* q : {p.x, p.ga, p.gx, p.z, (const void*)p.y, p.dy, (const void*)p.dx, (const void*)p.dga,
+                        (const void*)p.dgx, (const void*)p.dz})
+    at |= reinterpret_cast<uintptr_t>(q);
+  return strides % 2 == 0 && at % 4 == 0;
+}
+
+GatedArgs args(const GatedScanLaunch& p, int64_t pieces, uint32_t* chain) {
+  const int64_t es = p.bf16 ? 2 : 4;
   GatedArgs a{};
   a.x = p.x;
   a.ga = p.ga;
@@ -140,10 +578,10 @@ GatedArgs args(const GatedScanLaunch& p) {
   a.batch = p.batch;
   a.seqlen = p.seqlen;
   a.width = p.width;
-  a.xs = p.x_stride;
-  a.as = p.ga_stride;
-  a.is = p.gx_stride;
-  a.zs = p.z_stride;
+  a.xs = p.x_stride * es;
+  a.as = p.ga_stride * es;
+  a.is = p.gx_stride * es;
+  a.zs = p.z_stride * es;
   a.dy = p.dy;
   a.dh_last = p.dh_last;
   a.dx = p.dx;
@@ -151,46 +589,97 @@ GatedArgs args(const GatedScanLaunch& p) {
   a.dgx = p.dgx;
   a.dz = p.dz;
   a.dh0 = p.dh0;
+  a.pieces = (int32_t)pieces;
+  const int64_t lanes = pairs(p) ? 128 : 64;
+  a.tiles = (int32_t)((p.width + lanes - 1) / lanes);
+  a.items = (int32_t)(p.batch * a.tiles * pieces);
+  a.ticket = chain;
+  a.folds = reinterpret_cast<uint64_t*>(chain + kTicketWords);
+  a.states = chain + kTicketWords + 2 * p.batch * p.width * pieces;
   return a;
 }
 
-unsigned groups(int64_t n) { return (unsigned)((n + 255) / 256); }
+hipError_t clear(uint32_t* p, int64_t words, hipStream_t stream) {
+  if (words == 0) return hipSuccess;
+  const int64_t n = words / 4;
+  return launch(k_gated_clear, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, reinterpret_cast<uint4*>(p), n);
+}
+
+unsigned grid_of(const GatedArgs& a) { return (unsigned)(a.items < kMaxGrid ? a.items : kMaxGrid); }
+
+template <typename T, int V, bool Z, bool OUT>
+hipError_t go_fwd(const GatedArgs& a, hipStream_t stream) {
+  return launch(k_gated_fwd<T, V, kFwdSteps, kFwdWaves, Z, OUT>, dim3(grid_of(a)), dim3(64 * kFwdWaves), 0, stream, a);
+}
+template <typename T, int V, bool OUT>
+hipError_t go_fwd_z(const GatedArgs& a, hipStream_t stream) {
+  return a.z != nullptr && OUT ? go_fwd<T, V, OUT, OUT>(a, stream) : go_fwd<T, V, false, OUT>(a, stream);
+}
+template <bool OUT>
+hipError_t fwd(const GatedScanLaunch& p, const GatedArgs& a) {
+  if (!p.bf16) return go_fwd_z<float, 1, OUT>(a, p.stream);
+  return pairs(p) ? go_fwd_z<uint16_t, 2, OUT>(a, p.stream) : go_fwd_z<uint16_t, 1, OUT>(a, p.stream);
+}
+template <typename T, int V>
+hipError_t go_bwd(const GatedArgs& a, hipStream_t stream) {
+  return launch(a.z != nullptr ? k_gated_bwd<T, V, kBwdSteps, kBwdWaves, true> : k_gated_bwd<T, V, kBwdSteps, kBwdWaves, false>,
+                dim3(grid_of(a)), dim3(64 * kBwdWaves), 0, stream, a);
+}
+
+constexpr int64_t kFwdLen = kFwdSteps * kFwdWaves, kBwdLen = kBwdSteps * kBwdWaves;
 
 }  // namespace
 
+int64_t gated_scan_items(int64_t batch, int64_t seqlen, int64_t width) {
+  return batch * ((width + 63) / 64) * pieces_of(seqlen, kBwdLen);
+}
 int64_t gated_scan_ckpt_floats(int64_t batch, int64_t seqlen, int64_t width) {
   return batch * ((seqlen + kGatedCkpt - 1) / kGatedCkpt) * width;
 }
-int64_t gated_scan_fwd_floats(int64_t, int64_t, int64_t, bool) { return 0; }
+int64_t gated_scan_fwd_floats(int64_t batch, int64_t seqlen, int64_t width, bool) {
+  return chain_words(batch, width, pieces_of(seqlen, kFwdLen));
+}
 int64_t gated_scan_bwd_floats(int64_t batch, int64_t seqlen, int64_t width, bool, bool ckpt_given) {
-  return batch * width + (ckpt_given ? 0 : gated_scan_ckpt_floats(batch, seqlen, width));
+  const int64_t pieces = pieces_of(seqlen, kBwdLen);
+  int64_t n = chain_words(batch, width, pieces) + (batch * pieces * width + 63) / 64 * 64;
+  if (!ckpt_given)
+    n += gated_scan_fwd_floats(batch, seqlen, width, true) + gated_scan_ckpt_floats(batch, seqlen, width);
+  return n;
 }
 
 hipError_t launch_gated_scan_fwd(const GatedScanLaunch& p) {
-  const GatedArgs a = args(p);
-  return launch(p.bf16 ? k_gated_fwd<uint16_t> : k_gated_fwd<float>, dim3(groups(p.batch * p.width)), dim3(256), 0,
-                p.stream, a);
+  const int64_t pieces = pieces_of(p.seqlen, kFwdLen);
+  uint32_t* const words = reinterpret_cast<uint32_t*>(p.workspace);
+  const hipError_t rc = clear(words, chain_words(p.batch, p.width, pieces), p.stream);
+  return rc != hipSuccess ? rc : fwd<true>(p, args(p, pieces, words));
 }
 
+// The workspace: the gradient's chain, the forward pass's chain when there is one, the sums of
+// dlog_a, the states.
 hipError_t launch_gated_scan_bwd(const GatedScanLaunch& p) {
-  GatedArgs a = args(p);
-  a.part = p.dlog_a != nullptr ? p.workspace : nullptr;
-  hipError_t rc;
-  const dim3 grid(groups(p.batch * p.width));
+  const int64_t pieces = pieces_of(p.seqlen, kBwdLen), fpieces = pieces_of(p.seqlen, kFwdLen);
+  uint32_t* const words = reinterpret_cast<uint32_t*>(p.workspace);
+  const bool again = p.ckpt == nullptr;
+  const int64_t back = chain_words(p.batch, p.width, pieces);
+  const int64_t fore = again ? chain_words(p.batch, p.width, fpieces) : 0;
+  float* const part = p.workspace + back + fore;
   if (p.batch > 0) {
-    if (a.ckpt == nullptr) {
-      a.ckpt = p.workspace + p.batch * p.width;
-      GatedArgs f = a;
-      f.y = nullptr;
-      f.h_last = nullptr;
-      rc = launch(p.bf16 ? k_gated_fwd<uint16_t> : k_gated_fwd<float>, grid, dim3(256), 0, p.stream, f);
-      if (rc != hipSuccess) return rc;
+    hipError_t rc = clear(words, back + fore, p.stream);
+    if (rc != hipSuccess) return rc;
+    GatedArgs a = args(p, pieces, words);
+    a.part = p.dlog_a != nullptr ? part : nullptr;
+    if (again) {
+      a.ckpt = part + (p.batch * pieces * p.width + 63) / 64 * 64;
+      GatedArgs f = args(p, fpieces, words + back);
+      f.ckpt = a.ckpt;
+      if (p.seqlen > 0 && (rc = fwd<false>(p, f)) != hipSuccess) return rc;
     }
-    rc = launch(p.bf16 ? k_gated_bwd<uint16_t> : k_gated_bwd<float>, grid, dim3(256), 0, p.stream, a);
+    rc = !p.bf16 ? go_bwd<float, 1>(a, p.stream) : pairs(p) ? go_bwd<uint16_t, 2>(a, p.stream) : go_bwd<uint16_t, 1>(a, p.stream);
     if (rc != hipSuccess) return rc;
   }
   if (p.dlog_a == nullptr) return hipSuccess;
-  return launch(k_gated_sum, dim3(groups(p.width)), dim3(256), 0, p.stream, p.workspace, p.dlog_a, p.batch, p.width);
+  return launch(k_gated_sum, dim3((unsigned)((p.width + 15) / 16)), dim3(1024), 0, p.stream, part, p.dlog_a,
+                p.batch * pieces, p.width);
 }
 
 }  // namespace ssm

@@ -22,7 +22,8 @@ def test_scan_errors(lib):
     assert _fwd(lib, L=0, la=None) == bd.SSM_ERR_NULL_ARG
     for bad in (dict(b=-1), dict(L=-1), dict(D=-1), dict(L=(1 << 31) - 100), dict(D=(1 << 23) + 1),
                 dict(b=1 << 40, L=1 << 20), dict(b=1 << 20, D=1 << 12), dict(xs=95), dict(zs=8, z=P0 + 5 * MB),
-                dict(as_=(1 << 40) + 1), dict(b=1 << 62, D=1), dict(is_=1 << 40, L=1 << 20)):
+                dict(as_=(1 << 25) + 1), dict(b=1 << 62, D=1), dict(is_=1 << 25, b=1 << 20, L=1 << 20, D=1),
+                dict(b=1 << 20, L=1 << 20, D=1)):
         assert _fwd(lib, **bad) == bd.SSM_ERR_BAD_DIM, bad
     assert _fwd(lib, dtype=2) == bd.SSM_ERR_UNSUPPORTED
     for name, p in (("x", P0), ("ga", P0 + MB), ("gx", P0 + 2 * MB), ("z", P0 + 5 * MB), ("y", P0 + 4 * MB)):
@@ -104,7 +105,7 @@ def test_update_errors(lib):
     for name in ("h", "x", "ga", "gx", "la", "y"):
         assert _upd(lib, **{name: None}) == bd.SSM_ERR_NULL_ARG, name
     for bad in (dict(b=-1), dict(n=-1), dict(D=-1), dict(n=5), dict(xs=95), dict(z=P0 + 7 * MB, zs=95),
-                dict(D=(1 << 23) + 1), dict(b=1 << 24, n=1 << 24, D=1), dict(b=1 << 20, n=1 << 20, D=8192)):
+                dict(xs=(1 << 40) + 1), dict(D=(1 << 23) + 1), dict(b=1 << 24, n=1 << 24, D=1), dict(b=1 << 20, n=1 << 20, D=8192)):
         assert _upd(lib, **bad) == bd.SSM_ERR_BAD_DIM, bad
     assert _upd(lib, dtype=3) == bd.SSM_ERR_UNSUPPORTED
     for name in ("x", "ga", "gx", "z", "y"):
