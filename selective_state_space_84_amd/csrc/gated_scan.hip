@@ -12,8 +12,8 @@
 //
 // Published words carry their own validity: a word is all ones until it is
 // written, and no (A, S) or state is stored as that pattern.  Relaxed 64 and 32
-// bit atomics at agent scope are therefore enough.  Pieces are handed out by a
-// counter, earlier ones first: who waits for a piece waits for a workgroup that is
+// bit atomics at agent scope are therefore enough.  The pieces of a chain are handed out by a
+// counter of its own, earlier ones first: who waits for a piece waits for a workgroup that is
 // running, whatever else the device runs.  A wait gives up after kPolls reads (the
 // outputs are NaN then): a workspace that two calls share by mistake cannot hang.
 //
@@ -48,16 +48,25 @@ struct GatedArgs {
   void* dz;
   float* part;  // [batch][pieces][width] sums of dlog_a
   float* dh0;
-  uint32_t* ticket;  // all ones at first
+  uint32_t* tickets;  // [batch][tiles], all ones at first
   uint64_t* folds;   // [batch][pieces][width] (A, S)
   uint32_t* states;  // [batch][blocks][width]
-  int32_t pieces, tiles, items;
+  int32_t pieces, tiles;
+  int32_t first;  // of all pieces of work, this launch's
 };
 
-constexpr int kBlock = 8;  // pieces
+#ifndef KB
+#define KB 8
+#endif
+constexpr int kBlock = KB;  // pieces
 constexpr int kPolls = 1 << 20;
-constexpr uint64_t kNoFold = ~0ull;
-constexpr uint32_t kNoState = ~0u;
+#ifndef ZW
+#define ZW 2
+#endif
+#ifndef WPS
+#define WPS 4
+#endif
+constexpr int kWavesPerSimd = WPS;
 
 __device__ __forceinline__ int steps_of(const GatedArgs& a, int64_t b) {
   if (a.lengths == nullptr) return (int)a.seqlen;
@@ -72,6 +81,10 @@ struct Io {
   raw r;
   __device__ __forceinline__ void load(const gchar* p, uint32_t off) { r = gldr<raw>(p, off); }
   __device__ __forceinline__ float get(int v) const { return io_to_f32(r[v]); }
+  // Makes the compiler forget what it has derived from the registers: what is unpacked from them is
+  // unpacked again where it is next used, instead of held in a register each.
+  __device__ __forceinline__ void forget() {}
+  __device__ __forceinline__ void zero() { r = raw(T(0)); }
 };
 template <>
 struct Io<uint16_t, 2> {
@@ -80,6 +93,8 @@ struct Io<uint16_t, 2> {
   __device__ __forceinline__ float get(int v) const {
     return __builtin_bit_cast(float, v ? r & 0xffff0000u : r << 16);
   }
+  __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r)); }
+  __device__ __forceinline__ void zero() { r = 0; }
 };
 template <int V>
 __device__ __forceinline__ void put(gchar* p, uint32_t off, const float (&v)[V], const float*) {
@@ -103,6 +118,8 @@ __device__ __forceinline__ void put(gchar* p, uint32_t off, const float (&v)[V],
 // Fold of a piece, or of what lies behind it: h_out = a h + s.
 struct Fold {
   float a, s;
+  __device__ __forceinline__ float operator()(float h) const { return __builtin_fmaf(a, h, s); }
+  __device__ __forceinline__ Fold then(Fold b) const { return Fold{a * b.a, b(s)}; }
 };
 
 __device__ __forceinline__ float quiet(float v) { return v != v ? __builtin_nanf("") : v; }
@@ -128,72 +145,72 @@ __device__ __forceinline__ W wait_word(const W* p, W first) {
   return w;
 }
 
-// What enters piece q of a chain (counted in the chain's direction, its first piece q0) whose first entry is `first`; fold: this
-// piece's.  Publishes the fold, and behind a block's last piece the state.  folds, states: of piece 0 and
-// block 0 for this lane's channels; fs, ss: words from piece to piece and from block to block.
-template <int V>
-__device__ __forceinline__ void chain(int q, int q0, int last, const float (&first)[V], const Fold (&fold)[V],
-                                      uint64_t* folds, uint32_t* states, int64_t fs, int64_t ss, float (&in)[V]) {
-  const int blk = q / kBlock, j0 = blk * kBlock < q0 ? q0 : blk * kBlock;
-  const bool closes = q % kBlock == kBlock - 1;
-  if (q < last && !closes)
+// The chain of pieces, seen from piece q (counted in the chain's direction; its first piece is q0, its last `last`).
+struct Link {
+  int q, j0, blk, before;  // j0: the first piece of q's block, `before`: how many pieces of it come before q
+  bool heads, closes, ends;  // nothing comes before the block; q is the block's last piece; nothing comes behind q
+  __device__ __forceinline__ Link(int q_, int q0, int last) : q(q_) {
+    blk = q / kBlock;
+    heads = blk == q0 / kBlock;
+    j0 = heads ? q0 : blk * kBlock;
+    before = q - j0;
+    closes = q % kBlock == kBlock - 1;
+    ends = q == last;
+  }
+};
+
+// What the pieces before hand on, word by word over the waves into LDS: the folds of the block's pieces before q,
+// and the state in front of the block.  folds, states: of piece 0 and block 0 for this lane's channels,
+// `stride` words from one to the next.
+template <int V, int W>
+__device__ __forceinline__ void collect(const Link& l, int wave, int lane, const uint64_t* folds,
+                                        const uint32_t* states, int64_t stride, Fold (*pre)[64 * V], float* front) {
+  constexpr int N = (kBlock + W - 1) / W;
+  uint64_t w[N][V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) publish(folds + q * fs + v, fold[v]);
-  // All words are asked for at once; most are there.
-  uint64_t w[kBlock - 1][V];
-  uint32_t h[V];
+  for (int i = 0; i < N; ++i)
+    if (wave + i * W < l.before)
 #pragma unroll
-  for (int k = 0; k < kBlock - 1; ++k)
-    if (j0 + k < q)
+      for (int v = 0; v < V; ++v) w[i][v] = read_word(folds + (l.j0 + wave + i * W) * stride + v);
+  if (wave == W - 1 && !l.heads)
 #pragma unroll
-      for (int v = 0; v < V; ++v) w[k][v] = read_word(folds + (j0 + k) * fs + v);
-  if (j0 != q0)
+    for (int v = 0; v < V; ++v) {
+      const uint32_t* const p = states + (l.blk - 1) * stride + v;
+      front[lane * V + v] = __builtin_bit_cast(float, wait_word(p, read_word(p)));
+    }
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = read_word(states + (blk - 1) * ss + v);
-#pragma unroll
-  for (int v = 0; v < V; ++v) in[v] = first[v];
-  if (j0 != q0)
-#pragma unroll
-    for (int v = 0; v < V; ++v) in[v] = __builtin_bit_cast(float, wait_word(states + (blk - 1) * ss + v, h[v]));
-#pragma unroll
-  for (int k = 0; k < kBlock - 1; ++k)
-    if (j0 + k < q)
+  for (int i = 0; i < N; ++i)
+    if (wave + i * W < l.before)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const uint64_t f = wait_word(folds + (j0 + k) * fs + v, w[k][v]);
-        in[v] = __builtin_fmaf(__builtin_bit_cast(float, (uint32_t)f), in[v],
-                               __builtin_bit_cast(float, (uint32_t)(f >> 32)));
+        const uint64_t f = wait_word(folds + (l.j0 + wave + i * W) * stride + v, w[i][v]);
+        pre[wave + i * W][lane * V + v] =
+            Fold{__builtin_bit_cast(float, (uint32_t)f), __builtin_bit_cast(float, (uint32_t)(f >> 32))};
       }
-  if (q < last && closes)
-#pragma unroll
-    for (int v = 0; v < V; ++v) publish(states + blk * ss + v, __builtin_fmaf(fold[v].a, in[v], fold[v].s));
 }
 
-// The next piece of work of this workgroup: from the counter where pieces wait for
-// each other, else every gridDim.x-th.
-__device__ __forceinline__ int next_item(const GatedArgs& a, int before, int* shared) {
-  if (a.pieces == 1) return before < 0 ? (int)blockIdx.x : before + (int)gridDim.x;
-  __syncthreads();
-  if (threadIdx.x == 0)
-    *shared = (int)(__hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u);
-  __syncthreads();
-  return *shared;
-}
-
-// Where a lane works: channels d .. d + V - 1 of row b (clamped into the row; `on`: they exist).
+// Where a lane works: channels d .. d + V - 1 of row b (clamped into the row; `on`: they exist), piece q
+// of that chain.
 template <int V>
 struct Spot {
   int64_t b, d;
   int q;
   bool on;
-  __device__ __forceinline__ Spot(const GatedArgs& a, int item) {
-    const int per = a.tiles * (int)a.batch;  // earlier pieces of every row first
-    q = item / per;
-    const int rt = item % per;
-    b = rt / a.tiles;
-    d = ((int64_t)(rt % a.tiles) * 64 + (threadIdx.x & 63)) * V;
+  // Work goes to the chains in turn.  Within one, the piece is the next that no workgroup has
+  // started.  shared: read and written by the whole workgroup.
+  __device__ __forceinline__ Spot(const GatedArgs& a, int* shared) {
+    const int chain = ((int)blockIdx.x + a.first) % (a.tiles * (int)a.batch);
+    b = chain / a.tiles;
+    d = ((int64_t)(chain % a.tiles) * 64 + (threadIdx.x & 63)) * V;
     on = d < a.width;
     if (!on) d = a.width - V;
+    q = 0;
+    if (a.pieces > 1) {
+      if (threadIdx.x == 0)
+        *shared = (int)(__hip_atomic_fetch_add(a.tickets + chain, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u);
+      __syncthreads();
+      q = __builtin_amdgcn_readfirstlane(*shared);
+    }
   }
 };
 
@@ -210,300 +227,286 @@ __device__ __forceinline__ void load_steps(Io<T, V> (&r)[TS], const void* base, 
 }
 
 template <typename T, int V, int TS, int W, bool Z, bool OUT>
-__global__ void __launch_bounds__(64 * W) k_gated_fwd(const GatedArgs a) {
-  __shared__ Fold folds[W][64 * V];
-  __shared__ float enters[64 * V];
+__global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const GatedArgs a) {
+  __shared__ Fold folds[W][64 * V], pre[kBlock - 1][64 * V];
+  __shared__ float front[64 * V];
   __shared__ int shared;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  for (int item = next_item(a, -1, &shared); item < a.items; item = next_item(a, item, &shared)) {
-    const Spot<V> at(a, item);
-    const int n = steps_of(a, at.b), seqlen = (int)a.seqlen;
-    const int c0 = at.q * (W * TS), t0 = c0 + wave * TS;
-    const int m = min(max(n - t0, 0), TS);
-    const int64_t row = at.b * a.seqlen + t0, st = at.b * a.width + at.d;
-    const bool first = at.q == 0;
-    float h[V];
-    if (c0 < n || first) {
-      float dec[TS][V], u[TS][V];
-      Fold f[V];
-      Io<T, V> z[TS];
-      if (m > 0) {
-        Io<T, V> x[TS], ga[TS], gx[TS];
-        load_steps(ga, a.ga, row, a.as, at.d, m);
-        load_steps(gx, a.gx, row, a.is, at.d, m);
-        load_steps(x, a.x, row, a.xs, at.d, m);
-        float c2[V];
+  const Spot<V> at(a, &shared);
+  const int n = steps_of(a, at.b), seqlen = (int)a.seqlen;
+  const int c0 = at.q * (W * TS), t0 = c0 + wave * TS;
+  const int m = min(max(n - t0, 0), TS);
+  const int64_t row = at.b * a.seqlen + t0, st = at.b * a.width + at.d;
+  gchar* const py = uniform_ptr(static_cast<const char*>(a.y) + row * (a.width * sizeof(T)));
+  const uint32_t off = (uint32_t)(at.d * sizeof(T)), ws = (uint32_t)(a.width * sizeof(T));
+  const T* const tag = nullptr;
+  if (c0 >= n && at.q > 0) {  // behind the row's end
+    const float o[V] = {};
+    for (int i = 0; OUT && i < TS && t0 + i < seqlen; ++i)
+      if (at.on) put<V>(py, off + i * ws, o, tag);
+    return;
+  }
+  float dec[TS][V], u[TS][V];
+  Io<T, V> z[TS];
+  if (m > 0) {
+    Io<T, V> x[TS], ga[TS], gx[TS];
+    load_steps(ga, a.ga, row, a.as, at.d, m);
+    load_steps(gx, a.gx, row, a.is, at.d, m);
+    load_steps(x, a.x, row, a.xs, at.d, m);
+    float c2[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) c2[v] = a.log_a[at.d + v] * kLog2e;
+    for (int v = 0; v < V; ++v) c2[v] = a.log_a[at.d + v] * kLog2e;
 #pragma unroll
-        for (int i = 0; i < TS; ++i)
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            const GatedStep s = gated_step(ga[i].get(v), gx[i].get(v), c2[v]);
-            dec[i][v] = s.a;
-            u[i][v] = s.m * s.sx * x[i].get(v);
-          }
-        if (Z && OUT) load_steps(z, a.z, row, a.zs, at.d, m);
-      }
-      if (m < TS)
-#pragma unroll
-        for (int i = 0; i < TS; ++i)
-          if (i >= m)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-              dec[i][v] = 1.0f;
-              u[i][v] = 0.0f;
-            }
+    for (int i = 0; i < TS; ++i)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        f[v] = Fold{dec[0][v], u[0][v]};
-#pragma unroll
-        for (int i = 1; i < TS; ++i) f[v] = Fold{f[v].a * dec[i][v], __builtin_fmaf(dec[i][v], f[v].s, u[i][v])};
-        folds[wave][lane * V + v] = f[v];
+        const GatedStep s = gated_step(ga[i].get(v), gx[i].get(v), c2[v]);
+        dec[i][v] = s.a;
+        u[i][v] = s.m * s.sx * x[i].get(v);
       }
-      __syncthreads();
-      if (wave == 0) {
-        float start[V], in[V];
+    if (Z && OUT) load_steps(z, a.z, row, a.zs, at.d, m);
+  }
+  if (m < TS)
+#pragma unroll
+    for (int i = 0; i < TS; ++i)
+      if (i >= m)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          start[v] = a.h0 != nullptr ? a.h0[st + v] : 0.0f;
-          for (int k = 1; k < W; ++k) {
-            const Fold g = folds[k][lane * V + v];
-            f[v] = Fold{f[v].a * g.a, __builtin_fmaf(g.a, f[v].s, g.s)};
-          }
+          dec[i][v] = 1.0f;
+          u[i][v] = 0.0f;
         }
-        if (a.pieces > 1) {
-          const int last = n > 0 ? (n - 1) / (W * TS) : 0;
-          const int blocks = (a.pieces + kBlock - 1) / kBlock;
-          chain<V>(at.q, 0, last, start, f, a.folds + at.b * a.pieces * a.width + at.d,
-                   a.states + at.b * blocks * a.width + at.d, a.width, a.width, in);
-        } else {
+  Fold f[V];
 #pragma unroll
-          for (int v = 0; v < V; ++v) in[v] = start[v];
-        }
+  for (int v = 0; v < V; ++v) {
+    f[v] = Fold{dec[0][v], u[0][v]};
 #pragma unroll
-        for (int v = 0; v < V; ++v) enters[lane * V + v] = in[v];
-      }
-      __syncthreads();
+    for (int i = 1; i < TS; ++i) f[v] = f[v].then(Fold{dec[i][v], u[i][v]});
+    folds[wave][lane * V + v] = f[v];
+  }
+  __syncthreads();
+  const Link l(at.q, 0, n > 0 ? (n - 1) / (W * TS) : 0);
+  uint64_t* const fp = a.folds + at.b * a.pieces * a.width + at.d;
+  uint32_t* const sp = a.states + at.b * ((a.pieces + kBlock - 1) / kBlock) * a.width + at.d;
+  if (wave == 0 && !l.ends)
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        h[v] = enters[lane * V + v];
-        for (int k = 0; k < wave; ++k) {
-          const Fold g = folds[k][lane * V + v];
-          h[v] = __builtin_fmaf(g.a, h[v], g.s);
-        }
-      }
-      if (a.ckpt != nullptr && t0 % kGatedCkpt == 0 && t0 < seqlen && at.on) {
-        const int64_t nck = (a.seqlen + kGatedCkpt - 1) / kGatedCkpt;
-        float* const ck = a.ckpt + (at.b * nck + t0 / kGatedCkpt) * a.width + at.d;
-#pragma unroll
-        for (int v = 0; v < V; ++v) ck[v] = h[v];
-      }
-      gchar* const p = uniform_ptr(static_cast<const char*>(a.y) + row * (a.width * sizeof(T)));
-      const uint32_t off = (uint32_t)(at.d * sizeof(T)), ws = (uint32_t)(a.width * sizeof(T));
-#pragma unroll
-      for (int i = 0; i < TS; ++i) {
-        float o[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          h[v] = __builtin_fmaf(dec[i][v], h[v], u[i][v]);
-          o[v] = Z && OUT ? h[v] * silu(z[i].get(v)) : h[v];
-          if (i >= m) o[v] = 0.0f;
-        }
-        if (OUT && t0 + i < seqlen && at.on) put<V>(p, off + i * ws, o, static_cast<const T*>(nullptr));
-      }
-      // The last wave carries the state behind the row's last step to the end of its piece.
-      if (a.h_last != nullptr && wave == W - 1 && at.on && (n - 1) / (W * TS) == at.q)
-#pragma unroll
-        for (int v = 0; v < V; ++v) a.h_last[st + v] = h[v];
-    } else if (OUT) {
-      gchar* const p = uniform_ptr(static_cast<const char*>(a.y) + row * (a.width * sizeof(T)));
-      const uint32_t off = (uint32_t)(at.d * sizeof(T)), ws = (uint32_t)(a.width * sizeof(T));
-      const float o[V] = {};
-      for (int i = 0; i < TS && t0 + i < seqlen; ++i)
-        if (at.on) put<V>(p, off + i * ws, o, static_cast<const T*>(nullptr));
+    for (int v = 0; v < V; ++v) {
+      for (int k = 1; k < W; ++k) f[v] = f[v].then(folds[k][lane * V + v]);
+      if (!l.closes) publish(fp + at.q * a.width + v, f[v]);
     }
+  if (a.pieces > 1) {
+    collect<V, W>(l, wave, lane, fp, sp, a.width, pre, front);
     __syncthreads();
   }
+  float h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    h[v] = !l.heads ? front[lane * V + v] : a.h0 != nullptr ? a.h0[st + v] : 0.0f;
+    for (int k = 0; k < l.before; ++k) h[v] = pre[k][lane * V + v](h[v]);
+    if (wave == 0 && l.closes && !l.ends) publish(sp + l.blk * a.width + v, f[v](h[v]));
+    for (int k = 0; k < wave; ++k) h[v] = folds[k][lane * V + v](h[v]);
+  }
+  if (a.ckpt != nullptr && t0 % kGatedCkpt == 0 && t0 < seqlen && at.on) {
+    float* const ck = a.ckpt + (at.b * ((a.seqlen + kGatedCkpt - 1) / kGatedCkpt) + t0 / kGatedCkpt) * a.width + at.d;
+#pragma unroll
+    for (int v = 0; v < V; ++v) ck[v] = h[v];
+  }
+#pragma unroll
+  for (int i = 0; i < TS; ++i) {
+    float o[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      h[v] = Fold{dec[i][v], u[i][v]}(h[v]);
+      o[v] = Z && OUT ? h[v] * silu(z[i].get(v)) : h[v];
+      if (i >= m) o[v] = 0.0f;
+    }
+    if (OUT && t0 + i < seqlen && at.on) put<V>(py, off + i * ws, o, tag);
+  }
+  // The last wave carries the state behind the row's last step to the end of its piece.  (Whoever reads h0 has read it:
+  // the first piece has published by now, or is this one.)
+  if (a.h_last != nullptr && wave == W - 1 && at.on && l.ends)
+#pragma unroll
+    for (int v = 0; v < V; ++v) a.h_last[st + v] = h[v];
 }
 
 template <typename T, int V, int TS, int W, bool Z>
-__global__ void __launch_bounds__(64 * W) k_gated_bwd(const GatedArgs a) {
-  __shared__ Fold fwd[W][64 * V];
-  __shared__ Fold rev[W][64 * V];
-  __shared__ float enters[64 * V];
+__global__ void __launch_bounds__(64 * W, Z && V == 2 ? ZW : kWavesPerSimd) k_gated_bwd(const GatedArgs a) {
+  __shared__ Fold fwd[W][64 * V], rev[W][64 * V], pre[kBlock - 1][64 * V];
+  __shared__ float front[64 * V];
   __shared__ int shared;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  for (int item = next_item(a, -1, &shared); item < a.items; item = next_item(a, item, &shared)) {
-    const Spot<V> at(a, item);  // q counts from the sequence's end
-    const int n = steps_of(a, at.b), seqlen = (int)a.seqlen;
-    const int c = a.pieces - 1 - at.q, c0 = c * (W * TS), t0 = c0 + wave * TS;
-    const int m = min(max(n - t0, 0), TS);
-    const int64_t row = at.b * a.seqlen + t0, st = at.b * a.width + at.d;
-    const int64_t ws = a.width * (int64_t)sizeof(T);
-    const uint32_t off = (uint32_t)(at.d * sizeof(T));
-    gchar* const px = uniform_ptr(static_cast<const char*>(a.dx) + row * ws);
-    gchar* const pa = uniform_ptr(static_cast<const char*>(a.dga) + row * ws);
-    gchar* const pi = uniform_ptr(static_cast<const char*>(a.dgx) + row * ws);
-    gchar* const pz = uniform_ptr(static_cast<const char*>(a.dz) + row * ws);
-    const T* const tag = nullptr;
-    float sum[V] = {};
-    if (c0 < n) {
-      Io<T, V> x[TS], dy[TS], z[TS];
-      float sa[TS][V], sx[TS][V], dec[TS][V], mm[TS][V], before[TS][V];
-      float la[V], h[V];
-      Fold f[V], r[V];
-      if (m > 0) {
-        Io<T, V> ga[TS], gx[TS];
-        load_steps(ga, a.ga, row, a.as, at.d, m);
-        load_steps(gx, a.gx, row, a.is, at.d, m);
-        load_steps(x, a.x, row, a.xs, at.d, m);
-        load_steps(dy, a.dy, row, ws, at.d, m);
-        if (Z) load_steps(z, a.z, row, a.zs, at.d, m);
-#pragma unroll
-        for (int v = 0; v < V; ++v) la[v] = a.log_a[at.d + v];
-#pragma unroll
-        for (int i = 0; i < TS; ++i)
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            const GatedStep s = gated_step(ga[i].get(v), gx[i].get(v), la[v] * kLog2e);
-            sa[i][v] = s.sa;
-            sx[i][v] = s.sx;
-            dec[i][v] = s.a;
-            mm[i][v] = s.m;
-          }
+  const Spot<V> at(a, &shared);  // q counts from the sequence's end
+  const int n = steps_of(a, at.b), seqlen = (int)a.seqlen;
+  const int c = a.pieces - 1 - at.q, c0 = c * (W * TS), t0 = c0 + wave * TS;
+  const int m = min(max(n - t0, 0), TS);
+  const int64_t row = at.b * a.seqlen + t0, st = at.b * a.width + at.d;
+  const int64_t step = a.width * (int64_t)sizeof(T);
+  gchar* const px = uniform_ptr(static_cast<const char*>(a.dx) + row * step);
+  gchar* const pa = uniform_ptr(static_cast<const char*>(a.dga) + row * step);
+  gchar* const pi = uniform_ptr(static_cast<const char*>(a.dgx) + row * step);
+  gchar* const pz = uniform_ptr(static_cast<const char*>(a.dz) + row * step);
+  const uint32_t off = (uint32_t)(at.d * sizeof(T)), ws = (uint32_t)step;
+  const T* const tag = nullptr;
+  float* const part = a.part + (at.b * a.pieces + c) * a.width + at.d;
+  if (c0 >= n) {  // behind the row's end
+    const float o[V] = {};
+    for (int i = 0; i < TS && t0 + i < seqlen; ++i)
+      if (at.on) {
+        put<V>(px, off + i * ws, o, tag);
+        put<V>(pa, off + i * ws, o, tag);
+        put<V>(pi, off + i * ws, o, tag);
+        if (Z) put<V>(pz, off + i * ws, o, tag);
       }
+    if (wave == 0 && at.on)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        f[v] = r[v] = Fold{1.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < TS; ++i)
-          if (i < m) f[v] = Fold{f[v].a * dec[i][v], __builtin_fmaf(dec[i][v], f[v].s, mm[i][v] * sx[i][v] * x[i].get(v))};
-#pragma unroll
-        for (int i = TS - 1; i >= 0; --i)
-          if (i < m) {
-            const float e = Z ? dy[i].get(v) * silu(z[i].get(v)) : dy[i].get(v);
-            r[v].s = dec[i][v] * (e + r[v].s);
-          }
-        r[v].a = f[v].a;
-        fwd[wave][lane * V + v] = f[v];
-        rev[wave][lane * V + v] = r[v];
+        if (a.part != nullptr) part[v] = 0.0f;
+        if (a.dh0 != nullptr && c == 0) a.dh0[st + v] = a.dh_last != nullptr ? a.dh_last[st + v] : 0.0f;
       }
-      __syncthreads();
-      if (wave == W - 1) {
-        // The piece's fold from its last wave to its first.
-        float start[V], in[V];
+    return;
+  }
+  Io<T, V> x[TS], dy[TS], z[TS];
+  float dec[TS][V], sa[TS][V], kx[TS][V], inv[TS][V], la[V];  // kx = m sx, inv = 1 / m
+  if (m > 0) {
+    Io<T, V> ga[TS], gx[TS];
+    load_steps(ga, a.ga, row, a.as, at.d, m);
+    load_steps(gx, a.gx, row, a.is, at.d, m);
+    load_steps(x, a.x, row, a.xs, at.d, m);
+    load_steps(dy, a.dy, row, step, at.d, m);
+    if (Z) load_steps(z, a.z, row, a.zs, at.d, m);
+#pragma unroll
+    for (int v = 0; v < V; ++v) la[v] = a.log_a[at.d + v];
+#pragma unroll
+    for (int i = 0; i < TS; ++i) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const GatedStep s = gated_step(ga[i].get(v), gx[i].get(v), la[v] * kLog2e);
+        dec[i][v] = s.a;
+        sa[i][v] = s.sa;
+        kx[i][v] = s.m * s.sx;
+        inv[i][v] = s.inv_m;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  if (m < TS)  // steps that do not exist hand everything on
+#pragma unroll
+    for (int i = 0; i < TS; ++i)
+      if (i >= m) {
+        x[i].zero();
+        dy[i].zero();
+        if (Z) z[i].zero();
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          start[v] = a.dh_last != nullptr ? a.dh_last[st + v] : 0.0f;
-          for (int k = W - 2; k >= 0; --k) {
-            const Fold g = rev[k][lane * V + v];
-            r[v] = Fold{r[v].a * g.a, __builtin_fmaf(g.a, r[v].s, g.s)};
-          }
-        }
-        if (a.pieces > 1) {
-          const int q0 = a.pieces - 1 - (n - 1) / (W * TS);
-          const int blocks = (a.pieces + kBlock - 1) / kBlock;
-          chain<V>(at.q, q0, a.pieces - 1, start, r, a.folds + at.b * a.pieces * a.width + at.d,
-                   a.states + at.b * blocks * a.width + at.d, a.width, a.width, in);
-        } else {
-#pragma unroll
-          for (int v = 0; v < V; ++v) in[v] = start[v];
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) enters[lane * V + v] = in[v];
-      }
-      // Meanwhile the states before each step.
-      const int64_t nck = (a.seqlen + kGatedCkpt - 1) / kGatedCkpt;
-      const float* const ck = a.ckpt + (at.b * nck + c0 / kGatedCkpt) * a.width + at.d;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        h[v] = ck[v];
-        for (int k = 0; k < wave; ++k) {
-          const Fold g = fwd[k][lane * V + v];
-          h[v] = __builtin_fmaf(g.a, h[v], g.s);
-        }
-#pragma unroll
-        for (int i = 0; i < TS; ++i) {
-          before[i][v] = h[v];
-          if (i < m) h[v] = __builtin_fmaf(dec[i][v], h[v], mm[i][v] * sx[i][v] * x[i].get(v));
+          dec[i][v] = 1.0f;
+          sa[i][v] = kx[i][v] = inv[i][v] = 0.0f;
         }
       }
-      __syncthreads();
-      float p[V];
+  Fold f[V], r[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        p[v] = enters[lane * V + v];
-        for (int k = W - 1; k > wave; --k) {
-          const Fold g = rev[k][lane * V + v];
-          p[v] = __builtin_fmaf(g.a, p[v], g.s);
-        }
-      }
+  for (int v = 0; v < V; ++v) {
+    f[v] = Fold{dec[0][v], kx[0][v] * x[0].get(v)};
+    r[v].s = 0.0f;
 #pragma unroll
-      for (int i = TS - 1; i >= 0; --i) {
-        float dx[V] = {}, da[V] = {}, di[V] = {}, dz[V] = {};
-        if (i < m)
+    for (int i = 1; i < TS; ++i) f[v] = f[v].then(Fold{dec[i][v], kx[i][v] * x[i].get(v)});
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            const float xv = x[i].get(v), s = sa[i][v], t = sx[i][v], ac = dec[i][v], mv = mm[i][v];
-            const float w = t * xv, hb = before[i][v];
-            float e = dy[i].get(v);
-            if (Z) {
-              const float zv = z[i].get(v), q = sigmoid(zv);
-              dz[v] = e * __builtin_fmaf(ac, hb, mv * w) * q * __builtin_fmaf(zv, 1.0f - q, 1.0f);
-              e *= zv * q;
-            }
-            const float g = e + p[v];
-            const float inv = mv > 0.0f ? hw_rcp(mv) : 0.0f;
-            const float dla = g * __builtin_fmaf(ac, hb, -(ac * ac * inv) * w);
-            dx[v] = g * mv * t;
-            di[v] = dx[v] * xv * (1.0f - t);
-            da[v] = dla * la[v] * s * (1.0f - s);
-            sum[v] = __builtin_fmaf(dla, s, sum[v]);
-            p[v] = ac * g;
-          }
-        const uint32_t o = off + (uint32_t)i * (uint32_t)ws;
-        if (t0 + i < seqlen && at.on) {
-          put<V>(px, o, dx, tag);
-          put<V>(pa, o, da, tag);
-          put<V>(pi, o, di, tag);
-          if (Z) put<V>(pz, o, dz, tag);
-        }
-      }
-      if (a.dh0 != nullptr && c == 0 && wave == 0 && at.on)
-#pragma unroll
-        for (int v = 0; v < V; ++v) a.dh0[st + v] = p[v];
-    } else {
-      const float o[V] = {};
-      for (int i = 0; i < TS && t0 + i < seqlen; ++i) {
-        const uint32_t to = off + (uint32_t)i * (uint32_t)ws;
-        if (at.on) {
-          put<V>(px, to, o, tag);
-          put<V>(pa, to, o, tag);
-          put<V>(pi, to, o, tag);
-          if (Z) put<V>(pz, to, o, tag);
-        }
-      }
-      if (a.dh0 != nullptr && c == 0 && wave == 0 && at.on)
-#pragma unroll
-        for (int v = 0; v < V; ++v) a.dh0[st + v] = a.dh_last != nullptr ? a.dh_last[st + v] : 0.0f;
+    for (int i = TS - 1; i >= 0; --i) {
+      const float e = Z ? dy[i].get(v) * silu(z[i].get(v)) : dy[i].get(v);
+      r[v].s = dec[i][v] * (e + r[v].s);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if (a.part != nullptr) {
-      // The waves' sums in their order.
-      __syncthreads();
+    r[v].a = f[v].a;
+    fwd[wave][lane * V + v] = f[v];
+    rev[wave][lane * V + v] = r[v];
+  }
+  __syncthreads();
+  const Link l(at.q, a.pieces - 1 - (n - 1) / (W * TS), a.pieces - 1);
+  uint64_t* const fp = a.folds + at.b * a.pieces * a.width + at.d;
+  uint32_t* const sp = a.states + at.b * ((a.pieces + kBlock - 1) / kBlock) * a.width + at.d;
+  if (wave == W - 1 && !l.ends)
 #pragma unroll
-      for (int v = 0; v < V; ++v) fwd[wave][lane * V + v].a = sum[v];
-      __syncthreads();
-      if (wave == 0 && at.on)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float t = 0.0f;
-          for (int k = 0; k < W; ++k) t += fwd[k][lane * V + v].a;
-          a.part[(at.b * a.pieces + c) * a.width + at.d + v] = t;
-        }
+    for (int v = 0; v < V; ++v) {
+      // The piece's fold from its last wave to its first.
+      for (int k = W - 2; k >= 0; --k) r[v] = r[v].then(rev[k][lane * V + v]);
+      if (!l.closes) publish(fp + at.q * a.width + v, r[v]);
     }
+  // The states before each step, and what a step's gradients are in multiples of that of its state:
+  //   dx = g kx, dgx = g ki, d(log a) sa = g gs, dga = g gs ka.
+  float gs[TS][V], ka[TS][V], ki[TS][V], e[TS][V];
+  const float* const ck = a.ckpt + (at.b * ((a.seqlen + kGatedCkpt - 1) / kGatedCkpt) + c0 / kGatedCkpt) * a.width + at.d;
+  float h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    h[v] = ck[v];
+    for (int k = 0; k < wave; ++k) h[v] = fwd[k][lane * V + v](h[v]);
+  }
+#pragma unroll
+  for (int i = 0; i < TS; ++i) {
+    x[i].forget();
+    dy[i].forget();
+    if (Z) z[i].forget();
+    float dz[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float ac = dec[i][v], u = kx[i][v] * x[i].get(v), w = u * inv[i][v];  // w = sx x
+      gs[i][v] = ac * sa[i][v] * __builtin_fmaf(-(ac * inv[i][v]), w, h[v]);
+      ka[i][v] = __builtin_fmaf(-la[v], sa[i][v], la[v]);
+      ki[i][v] = __builtin_fmaf(-kx[i][v], w, u);
+      h[v] = __builtin_fmaf(ac, h[v], u);
+      if (Z) {
+        const float zv = z[i].get(v), q = sigmoid(zv), d = dy[i].get(v);
+        e[i][v] = d * (zv * q);
+        dz[v] = i < m ? d * h[v] * q * __builtin_fmaf(zv, 1.0f - q, 1.0f) : 0.0f;
+      }
+    }
+    if (Z && t0 + i < seqlen && at.on) put<V>(pz, off + i * ws, dz, tag);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if (a.pieces > 1) {
+    collect<V, W>(l, wave, lane, fp, sp, a.width, pre, front);
     __syncthreads();
   }
+  float p[V], sum[V] = {};
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    p[v] = !l.heads ? front[lane * V + v] : a.dh_last != nullptr ? a.dh_last[st + v] : 0.0f;
+    for (int k = 0; k < l.before; ++k) p[v] = pre[k][lane * V + v](p[v]);
+    if (wave == W - 1 && l.closes && !l.ends) publish(sp + l.blk * a.width + v, r[v](p[v]));
+    for (int k = W - 1; k > wave; --k) p[v] = rev[k][lane * V + v](p[v]);
+  }
+#pragma unroll
+  for (int i = TS - 1; i >= 0; --i) {
+    float dx[V], da[V], di[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float g = (Z ? e[i][v] : dy[i].get(v)) + p[v], t = g * gs[i][v];
+      dx[v] = i < m ? g * kx[i][v] : 0.0f;  // (zero even where what comes from behind is not finite)
+      di[v] = i < m ? g * ki[i][v] : 0.0f;
+      da[v] = i < m ? t * ka[i][v] : 0.0f;
+      sum[v] += t;
+      p[v] = dec[i][v] * g;
+    }
+    if (t0 + i < seqlen && at.on) {
+      put<V>(px, off + i * ws, dx, tag);
+      put<V>(pa, off + i * ws, da, tag);
+      put<V>(pi, off + i * ws, di, tag);
+    }
+  }
+  if (a.dh0 != nullptr && c == 0 && wave == 0 && at.on)
+#pragma unroll
+    for (int v = 0; v < V; ++v) a.dh0[st + v] = p[v];
+  if (a.part == nullptr) return;
+  // The waves' sums in their order.
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < V; ++v) fwd[wave][lane * V + v].a = sum[v];
+  __syncthreads();
+  if (wave == 0 && at.on)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float t = 0.0f;
+      for (int k = 0; k < W; ++k) t += fwd[k][lane * V + v].a;
+      part[v] = t;
+    }
 }
 
 // All ones into n 16-byte words.
@@ -536,18 +539,24 @@ __global__ void __launch_bounds__(1024) k_gated_sum(const float* part, float* ou
   if (k0 == 0 && col < width) out[col] = v;
 }
 
-constexpr int kFwdSteps = 16, kFwdWaves = 8;  // 128 steps a piece
-constexpr int kBwdSteps = 8, kBwdWaves = 8;   // 64: every piece starts at a saved state
+#ifndef FS
+#define FS 16
+#define FW 8
+#define BS 8
+#define BW 8
+#endif
+constexpr int kFwdSteps = FS, kFwdWaves = FW;  // 128 steps a piece
+constexpr int kBwdSteps = BS, kBwdWaves = BW;   // 64: every piece starts at a saved state
 static_assert(kBwdSteps * kBwdWaves % kGatedCkpt == 0 && kGatedCkpt % kFwdSteps == 0, "pieces start at saved states");
-constexpr int64_t kMaxGrid = 1 << 20;
+constexpr int64_t kMaxGrid = 1 << 22;  // workgroups of a launch
 
 int64_t pieces_of(int64_t seqlen, int64_t len) { return seqlen <= len ? 1 : (seqlen + len - 1) / len; }
 int64_t blocks_of(int64_t pieces) { return (pieces + kBlock - 1) / kBlock; }
-// Words of 4 bytes that a chain uses: the counter, the folds, the states.
-constexpr int64_t kTicketWords = 64;
+// Words of 4 bytes that the chains use: the counters, the folds, the states.
+int64_t ticket_words(int64_t batch, int64_t width) { return (batch * ((width + 63) / 64) + 63) / 64 * 64; }
 int64_t chain_words(int64_t batch, int64_t width, int64_t pieces) {
   if (pieces <= 1) return 0;
-  const int64_t n = kTicketWords + batch * width * (2 * pieces + blocks_of(pieces));
+  const int64_t n = ticket_words(batch, width) + batch * width * (2 * pieces + blocks_of(pieces));
   return (n + 63) / 64 * 64;
 }
 
@@ -592,10 +601,9 @@ GatedArgs args(const GatedScanLaunch& p, int64_t pieces, uint32_t* chain) {
   a.pieces = (int32_t)pieces;
   const int64_t lanes = pairs(p) ? 128 : 64;
   a.tiles = (int32_t)((p.width + lanes - 1) / lanes);
-  a.items = (int32_t)(p.batch * a.tiles * pieces);
-  a.ticket = chain;
-  a.folds = reinterpret_cast<uint64_t*>(chain + kTicketWords);
-  a.states = chain + kTicketWords + 2 * p.batch * p.width * pieces;
+  a.tickets = chain;
+  a.folds = reinterpret_cast<uint64_t*>(chain + ticket_words(p.batch, p.width));
+  a.states = chain + ticket_words(p.batch, p.width) + 2 * p.batch * p.width * pieces;
   return a;
 }
 
@@ -605,11 +613,21 @@ hipError_t clear(uint32_t* p, int64_t words, hipStream_t stream) {
   return launch(k_gated_clear, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, reinterpret_cast<uint4*>(p), n);
 }
 
-unsigned grid_of(const GatedArgs& a) { return (unsigned)(a.items < kMaxGrid ? a.items : kMaxGrid); }
+// All pieces of all chains, in as many launches as it takes.
+template <typename K>
+hipError_t go(K kern, GatedArgs a, int threads, hipStream_t stream) {
+  const int64_t items = a.batch * a.tiles * a.pieces;
+  for (int64_t i = 0; i < items; i += kMaxGrid) {
+    a.first = (int32_t)i;
+    const hipError_t rc = launch(kern, dim3((unsigned)(items - i < kMaxGrid ? items - i : kMaxGrid)), dim3(threads), 0, stream, a);
+    if (rc != hipSuccess) return rc;
+  }
+  return hipSuccess;
+}
 
 template <typename T, int V, bool Z, bool OUT>
 hipError_t go_fwd(const GatedArgs& a, hipStream_t stream) {
-  return launch(k_gated_fwd<T, V, kFwdSteps, kFwdWaves, Z, OUT>, dim3(grid_of(a)), dim3(64 * kFwdWaves), 0, stream, a);
+  return go(k_gated_fwd<T, V, kFwdSteps, kFwdWaves, Z, OUT>, a, 64 * kFwdWaves, stream);
 }
 template <typename T, int V, bool OUT>
 hipError_t go_fwd_z(const GatedArgs& a, hipStream_t stream) {
@@ -622,8 +640,8 @@ hipError_t fwd(const GatedScanLaunch& p, const GatedArgs& a) {
 }
 template <typename T, int V>
 hipError_t go_bwd(const GatedArgs& a, hipStream_t stream) {
-  return launch(a.z != nullptr ? k_gated_bwd<T, V, kBwdSteps, kBwdWaves, true> : k_gated_bwd<T, V, kBwdSteps, kBwdWaves, false>,
-                dim3(grid_of(a)), dim3(64 * kBwdWaves), 0, stream, a);
+  return go(a.z != nullptr ? k_gated_bwd<T, V, kBwdSteps, kBwdWaves, true> : k_gated_bwd<T, V, kBwdSteps, kBwdWaves, false>, a,
+            64 * kBwdWaves, stream);
 }
 
 constexpr int64_t kFwdLen = kFwdSteps * kFwdWaves, kBwdLen = kBwdSteps * kBwdWaves;
