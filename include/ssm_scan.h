@@ -597,9 +597,9 @@ size_t ssm_qk_norm_rope_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_
  *                output; 0 stands for width.  Aligned to their elements; faster
  *                where widths, strides and addresses are multiples of 4 bytes.
  *                Strides not below width and at most 2^25.
- *   log_a      : [width] fp32, <= 0 and finite: the log of the strongest decay.
- *                Where 1 - a^2 is below fp32's normal range (and for log_a > 0)
- *                the input counts as nothing.
+ *   log_a      : [width] fp32, <= 0 and finite: the log of the strongest decay
+ *                (results for other values are unspecified).  Where 1 - a^2 is
+ *                below fp32's normal range the input counts as nothing.
  *   lengths    : [batch] int32 or NULL.  Row b has lengths[b] steps (clamped to
  *                [0, seqlen] on the device); what the inputs hold behind them is
  *                not used, y is zero there, and h_last is the state after

@@ -15,25 +15,36 @@ namespace ssm {
 
 __device__ __forceinline__ float sigmoid(float v) { return hw_rcp(1.0f + hw_exp2(-v * kLog2e)); }
 
-// 1 - 2^y for y <= 0 and p = 2^y.  Above -0.36 (2^y > 0.78) from the series of
-// (e^v - 1) / v to fifth order, v = y ln 2 (truncation below 5e-8 relative), so
-// that decays near 1 keep their distance from it; below, 1 - p loses at most
-// two bits.
-__device__ __forceinline__ float one_minus_exp2(float y, float p) {
-  float q = __builtin_fmaf(y, 1.5403530e-4f, 1.3333558e-3f);  // ln2^6 / 6!, ln2^5 / 5!
-  q = __builtin_fmaf(q, y, 9.6181291e-3f);
-  q = __builtin_fmaf(q, y, 5.5504109e-2f);
-  q = __builtin_fmaf(q, y, 2.4022651e-1f);
-  q = __builtin_fmaf(q, y, kLn2);
-  return y > -0.36f ? -y * q : 1.0f - p;
+// c ? a : b as a select: of the ternary operator the compiler makes a branch around what a or b costs, which
+// takes longer than both.
+__device__ __forceinline__ float pick(bool c, float a, float b) {
+  typedef float f1 __attribute__((ext_vector_type(1)));
+  typedef int i1 __attribute__((ext_vector_type(1)));
+  const f1 r = i1(-(int)c) ? f1(a) : f1(b);
+  return r[0];
 }
 
-// Where 1 - a^2 is below fp32's normal range the input counts as nothing: m,
-// and 1 / m as the gradient uses it, are 0.
+// 1 - 4^y for y <= 0 and p = 2^y.  Above -0.18 (4^y > 0.78) from the series of
+// (e^v - 1) / v to fifth order, v = y ln 4 (truncation below 5e-8 relative), so
+// that decays near 1 keep their distance from it; below, 1 - p^2 loses at most
+// two bits.
+__device__ __forceinline__ float one_minus_exp4(float y, float p) {
+  float q = __builtin_fmaf(y, 9.85825945e-3f, 4.26673861e-2f);  // ln4^6 / 6!, ln4^5 / 5!
+  q = __builtin_fmaf(q, y, 0.153890066f);
+  q = __builtin_fmaf(q, y, 0.444032869f);
+  q = __builtin_fmaf(q, y, 0.960906028f);
+  q = __builtin_fmaf(q, y, 1.38629436f);
+  return pick(y > -0.18f, -y * q, __builtin_fmaf(-p, p, 1.0f));
+}
+
+// Where m2 = 1 - a^2 is below fp32's normal range the input counts as nothing: the hardware's root takes it as 0,
+// and 1 / m as the gradient uses it is 0.
 constexpr float kTiny = 1.17549435e-38f;
 
 struct GatedStep {
-  float sa, sx, a, m, inv_m;
+  float sa, sx, a, m2;
+  __device__ __forceinline__ float m() const { return __builtin_amdgcn_sqrtf(m2); }
+  __device__ __forceinline__ float inv_m() const { return m2 >= kTiny ? __builtin_amdgcn_rsqf(m2) : 0.0f; }
 };
 
 // c2 = log_a log2(e).
@@ -43,10 +54,7 @@ __device__ __forceinline__ GatedStep gated_step(float ga, float gx, float c2) {
   s.sx = sigmoid(gx);
   const float y = c2 * s.sa;
   s.a = hw_exp2(y);
-  const float e = one_minus_exp2(y, s.a);
-  const float m2 = e * (2.0f - e);  // (1 - a)(1 + a)
-  s.inv_m = m2 >= kTiny ? __builtin_amdgcn_rsqf(m2) : 0.0f;
-  s.m = m2 * s.inv_m;
+  s.m2 = one_minus_exp4(y, s.a);
   return s;
 }
 

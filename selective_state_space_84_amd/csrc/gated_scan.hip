@@ -189,21 +189,18 @@ __device__ __forceinline__ void collect(const Link& l, int wave, int lane, const
       }
 }
 
-// Where a lane works: channels d .. d + V - 1 of row b (clamped into the row; `on`: they exist), piece q
-// of that chain.
+// Where a lane works: channels d .. d + V - 1 of row b, piece q of that chain.  Lanes behind the row's width do
+// the last channels' work once more, and write the same values to the same places.
 template <int V>
 struct Spot {
   int64_t b, d;
   int q;
-  bool on;
   // Work goes to the chains in turn.  Within one, the piece is the next that no workgroup has
   // started.  shared: read and written by the whole workgroup.
   __device__ __forceinline__ Spot(const GatedArgs& a, int* shared) {
     const int chain = ((int)blockIdx.x + a.first) % (a.tiles * (int)a.batch);
     b = chain / a.tiles;
-    d = ((int64_t)(chain % a.tiles) * 64 + (threadIdx.x & 63)) * V;
-    on = d < a.width;
-    if (!on) d = a.width - V;
+    d = min(((int64_t)(chain % a.tiles) * 64 + (threadIdx.x & 63)) * V, a.width - V);
     q = 0;
     if (a.pieces > 1) {
       if (threadIdx.x == 0)
@@ -243,10 +240,12 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
   if (c0 >= n && at.q > 0) {  // behind the row's end
     const float o[V] = {};
     for (int i = 0; OUT && i < TS && t0 + i < seqlen; ++i)
-      if (at.on) put<V>(py, off + i * ws, o, tag);
+      put<V>(py, off + i * ws, o, tag);
     return;
   }
-  float dec[TS][V], u[TS][V];
+  float dec[TS][V], u[TS][V], start[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) start[v] = a.h0 != nullptr && at.q < kBlock ? a.h0[st + v] : 0.0f;
   Io<T, V> z[TS];
   if (m > 0) {
     Io<T, V> x[TS], ga[TS], gx[TS];
@@ -262,7 +261,7 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
       for (int v = 0; v < V; ++v) {
         const GatedStep s = gated_step(ga[i].get(v), gx[i].get(v), c2[v]);
         dec[i][v] = s.a;
-        u[i][v] = s.m * s.sx * x[i].get(v);
+        u[i][v] = s.m() * s.sx * x[i].get(v);
       }
     if (Z && OUT) load_steps(z, a.z, row, a.zs, at.d, m);
   }
@@ -275,6 +274,10 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
           dec[i][v] = 1.0f;
           u[i][v] = 0.0f;
         }
+  // h_last may be h0 itself, and is written only when every fold of the first block has been published (or behind a
+  // barrier, by a piece that is alone): h0 is in registers before that.
+#pragma unroll
+  for (int v = 0; v < V; ++v) asm volatile("" : "+v"(start[v]));
   Fold f[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -300,12 +303,12 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
   float h[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    h[v] = !l.heads ? front[lane * V + v] : a.h0 != nullptr ? a.h0[st + v] : 0.0f;
+    h[v] = l.heads ? start[v] : front[lane * V + v];
     for (int k = 0; k < l.before; ++k) h[v] = pre[k][lane * V + v](h[v]);
     if (wave == 0 && l.closes && !l.ends) publish(sp + l.blk * a.width + v, f[v](h[v]));
     for (int k = 0; k < wave; ++k) h[v] = folds[k][lane * V + v](h[v]);
   }
-  if (a.ckpt != nullptr && t0 % kGatedCkpt == 0 && t0 < seqlen && at.on) {
+  if (a.ckpt != nullptr && t0 % kGatedCkpt == 0 && t0 < seqlen) {
     float* const ck = a.ckpt + (at.b * ((a.seqlen + kGatedCkpt - 1) / kGatedCkpt) + t0 / kGatedCkpt) * a.width + at.d;
 #pragma unroll
     for (int v = 0; v < V; ++v) ck[v] = h[v];
@@ -319,11 +322,10 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
       o[v] = Z && OUT ? h[v] * silu(z[i].get(v)) : h[v];
       if (i >= m) o[v] = 0.0f;
     }
-    if (OUT && t0 + i < seqlen && at.on) put<V>(py, off + i * ws, o, tag);
+    if (OUT && t0 + i < seqlen) put<V>(py, off + i * ws, o, tag);
   }
-  // The last wave carries the state behind the row's last step to the end of its piece.  (Whoever reads h0 has read it:
-  // the first piece has published by now, or is this one.)
-  if (a.h_last != nullptr && wave == W - 1 && at.on && l.ends)
+  // The last wave carries the state behind the row's last step to the end of its piece.
+  if (a.h_last != nullptr && wave == W - 1 && l.ends)
 #pragma unroll
     for (int v = 0; v < V; ++v) a.h_last[st + v] = h[v];
 }
@@ -349,14 +351,13 @@ __global__ void __launch_bounds__(64 * W, Z && V == 2 ? ZW : kWavesPerSimd) k_ga
   float* const part = a.part + (at.b * a.pieces + c) * a.width + at.d;
   if (c0 >= n) {  // behind the row's end
     const float o[V] = {};
-    for (int i = 0; i < TS && t0 + i < seqlen; ++i)
-      if (at.on) {
+    for (int i = 0; i < TS && t0 + i < seqlen; ++i) {
         put<V>(px, off + i * ws, o, tag);
         put<V>(pa, off + i * ws, o, tag);
         put<V>(pi, off + i * ws, o, tag);
         if (Z) put<V>(pz, off + i * ws, o, tag);
       }
-    if (wave == 0 && at.on)
+    if (wave == 0)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if (a.part != nullptr) part[v] = 0.0f;
@@ -382,8 +383,8 @@ __global__ void __launch_bounds__(64 * W, Z && V == 2 ? ZW : kWavesPerSimd) k_ga
         const GatedStep s = gated_step(ga[i].get(v), gx[i].get(v), la[v] * kLog2e);
         dec[i][v] = s.a;
         sa[i][v] = s.sa;
-        kx[i][v] = s.m * s.sx;
-        inv[i][v] = s.inv_m;
+        inv[i][v] = s.inv_m();
+        kx[i][v] = s.m2 * inv[i][v] * s.sx;
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(64 * W, Z && V == 2 ? ZW : kWavesPerSimd) k_ga
         dz[v] = i < m ? d * h[v] * q * __builtin_fmaf(zv, 1.0f - q, 1.0f) : 0.0f;
       }
     }
-    if (Z && t0 + i < seqlen && at.on) put<V>(pz, off + i * ws, dz, tag);
+    if (Z && t0 + i < seqlen) put<V>(pz, off + i * ws, dz, tag);
     __builtin_amdgcn_sched_barrier(0);
   }
   if (a.pieces > 1) {
@@ -485,13 +486,13 @@ __global__ void __launch_bounds__(64 * W, Z && V == 2 ? ZW : kWavesPerSimd) k_ga
       sum[v] += t;
       p[v] = dec[i][v] * g;
     }
-    if (t0 + i < seqlen && at.on) {
+    if (t0 + i < seqlen) {
       put<V>(px, off + i * ws, dx, tag);
       put<V>(pa, off + i * ws, da, tag);
       put<V>(pi, off + i * ws, di, tag);
     }
   }
-  if (a.dh0 != nullptr && c == 0 && wave == 0 && at.on)
+  if (a.dh0 != nullptr && c == 0 && wave == 0)
 #pragma unroll
     for (int v = 0; v < V; ++v) a.dh0[st + v] = p[v];
   if (a.part == nullptr) return;
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(64 * W, Z && V == 2 ? ZW : kWavesPerSimd) k_ga
 #pragma unroll
   for (int v = 0; v < V; ++v) fwd[wave][lane * V + v].a = sum[v];
   __syncthreads();
-  if (wave == 0 && at.on)
+  if (wave == 0)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float t = 0.0f;

@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(256) k_gated_update(const UpdateArgs a) {
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const GatedStep s = gated_step(io_to_f32(ga[j]), io_to_f32(gx[j]), c[j] * kLog2e);
-    h[j] = __builtin_fmaf(s.a, h[j], s.m * s.sx * io_to_f32(x[j]));
+    h[j] = __builtin_fmaf(s.a, h[j], s.m() * s.sx * io_to_f32(x[j]));
     io_store(y + j, a.z != nullptr ? h[j] * silu(io_to_f32(z[j])) : h[j]);
   }
   *hp = h;
