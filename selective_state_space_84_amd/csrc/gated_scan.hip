@@ -313,17 +313,25 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
 #pragma unroll
     for (int v = 0; v < V; ++v) ck[v] = h[v];
   }
+  // all: no step of these is behind the row's end (most waves need no checks).
+  auto walk = [&](auto all) {
+    constexpr bool ALL = decltype(all)::value;
 #pragma unroll
-  for (int i = 0; i < TS; ++i) {
-    float o[V];
+    for (int i = 0; i < TS; ++i) {
+      float o[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      h[v] = Fold{dec[i][v], u[i][v]}(h[v]);
-      o[v] = Z && OUT ? h[v] * silu(z[i].get(v)) : h[v];
-      if (i >= m) o[v] = 0.0f;
+      for (int v = 0; v < V; ++v) {
+        h[v] = Fold{dec[i][v], u[i][v]}(h[v]);
+        o[v] = Z && OUT ? h[v] * silu(z[i].get(v)) : h[v];
+        if (!ALL && i >= m) o[v] = 0.0f;
+      }
+      if (OUT && (ALL || t0 + i < seqlen)) put<V>(py, off + i * ws, o, tag);
     }
-    if (OUT && t0 + i < seqlen) put<V>(py, off + i * ws, o, tag);
-  }
+  };
+  if (m == TS)
+    walk(std::true_type());
+  else
+    walk(std::false_type());
   // The last wave carries the state behind the row's last step to the end of its piece.
   if (a.h_last != nullptr && wave == W - 1 && l.ends)
 #pragma unroll
@@ -474,24 +482,33 @@ __global__ void __launch_bounds__(64 * W, Z && V == 2 ? ZW : kWavesPerSimd) k_ga
     if (wave == W - 1 && l.closes && !l.ends) publish(sp + l.blk * a.width + v, r[v](p[v]));
     for (int k = W - 1; k > wave; --k) p[v] = rev[k][lane * V + v](p[v]);
   }
+  // all: no step of these is behind the row's end (most waves need no checks).
+  auto walk = [&](auto all) {
+    constexpr bool ALL = decltype(all)::value;
 #pragma unroll
-  for (int i = TS - 1; i >= 0; --i) {
-    float dx[V], da[V], di[V];
+    for (int i = TS - 1; i >= 0; --i) {
+      float dx[V], da[V], di[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float g = (Z ? e[i][v] : dy[i].get(v)) + p[v], t = g * gs[i][v];
-      dx[v] = i < m ? g * kx[i][v] : 0.0f;  // (zero even where what comes from behind is not finite)
-      di[v] = i < m ? g * ki[i][v] : 0.0f;
-      da[v] = i < m ? t * ka[i][v] : 0.0f;
-      sum[v] += t;
-      p[v] = dec[i][v] * g;
+      for (int v = 0; v < V; ++v) {
+        const float g = (Z ? e[i][v] : dy[i].get(v)) + p[v], t = g * gs[i][v];
+        dx[v] = g * kx[i][v];
+        di[v] = g * ki[i][v];
+        da[v] = t * ka[i][v];
+        if (!ALL && i >= m) dx[v] = di[v] = da[v] = 0.0f;  // even where what comes from behind is not finite
+        sum[v] += t;
+        p[v] = dec[i][v] * g;
+      }
+      if (ALL || t0 + i < seqlen) {
+        put<V>(px, off + i * ws, dx, tag);
+        put<V>(pa, off + i * ws, da, tag);
+        put<V>(pi, off + i * ws, di, tag);
+      }
     }
-    if (t0 + i < seqlen) {
-      put<V>(px, off + i * ws, dx, tag);
-      put<V>(pa, off + i * ws, da, tag);
-      put<V>(pi, off + i * ws, di, tag);
-    }
-  }
+  };
+  if (m == TS)
+    walk(std::true_type());
+  else
+    walk(std::false_type());
   if (a.dh0 != nullptr && c == 0 && wave == 0)
 #pragma unroll
     for (int v = 0; v < V; ++v) a.dh0[st + v] = p[v];
