@@ -60,9 +60,6 @@ struct GatedArgs {
 #endif
 constexpr int kBlock = KB;  // pieces
 constexpr int kPolls = 1 << 20;
-#ifndef ZW
-#define ZW 2
-#endif
 #ifndef WPS
 #define WPS 4
 #endif
@@ -74,45 +71,62 @@ __device__ __forceinline__ int steps_of(const GatedArgs& a, int64_t b) {
   return n < 0 ? 0 : n > (int)a.seqlen ? (int)a.seqlen : n;
 }
 
+// Rows go through buffer instructions: a resource (4 SGPRs) a tensor over this wave's steps, the
+// lane's offset in one VGPR, the step's in an SGPR, so that an access costs no vector
+// instruction.  Raw buffers (word 3 is the gfx9 data format, which must not be 0); what lies at or
+// past `bytes` is not written.
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t rows_of(const void* p, int64_t bytes_before, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(p)) + bytes_before, 0, (int)bytes,
+                                           0x00020000);
+}
+constexpr uint32_t kNowhere = 0x80000000u;  // a lane's offset behind every resource
+
 // V values of one lane as loaded.
 template <typename T, int V>
-struct Io {
-  typedef T raw __attribute__((ext_vector_type(V)));
-  raw r;
-  __device__ __forceinline__ void load(const gchar* p, uint32_t off) { r = gldr<raw>(p, off); }
-  __device__ __forceinline__ float get(int v) const { return io_to_f32(r[v]); }
-  // Makes the compiler forget what it has derived from the registers: what is unpacked from them is
-  // unpacked again where it is next used, instead of held in a register each.
+struct Io;
+template <>
+struct Io<float, 1> {
+  uint32_t r;
+  __device__ __forceinline__ void load(rsrc_t b, uint32_t lane, uint32_t row) {
+    r = __builtin_amdgcn_raw_buffer_load_b32(b, lane, row, 0);
+  }
+  __device__ __forceinline__ float get(int) const { return __builtin_bit_cast(float, r); }
   __device__ __forceinline__ void forget() {}
-  __device__ __forceinline__ void zero() { r = raw(T(0)); }
+};
+template <>
+struct Io<uint16_t, 1> {
+  uint16_t r;
+  __device__ __forceinline__ void load(rsrc_t b, uint32_t lane, uint32_t row) {
+    r = __builtin_amdgcn_raw_buffer_load_b16(b, lane, row, 0);
+  }
+  __device__ __forceinline__ float get(int) const { return io_to_f32(r); }
+  __device__ __forceinline__ void forget() {}
 };
 template <>
 struct Io<uint16_t, 2> {
   uint32_t r;
-  __device__ __forceinline__ void load(const gchar* p, uint32_t off) { r = gldr<uint32_t>(p, off); }
+  __device__ __forceinline__ void load(rsrc_t b, uint32_t lane, uint32_t row) {
+    r = __builtin_amdgcn_raw_buffer_load_b32(b, lane, row, 0);
+  }
   __device__ __forceinline__ float get(int v) const {
     return __builtin_bit_cast(float, v ? r & 0xffff0000u : r << 16);
   }
+  // Makes the compiler forget what it has derived from the register: what is unpacked from it is
+  // unpacked again where it is next used, instead of held in two more.
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r)); }
-  __device__ __forceinline__ void zero() { r = 0; }
 };
-template <int V>
-__device__ __forceinline__ void put(gchar* p, uint32_t off, const float (&v)[V], const float*) {
-  typedef float raw __attribute__((ext_vector_type(V)));
-  raw r;
-#pragma unroll
-  for (int k = 0; k < V; ++k) r[k] = v[k];
-  gstr(p, off, r);
+__device__ __forceinline__ void put(rsrc_t b, uint32_t lane, uint32_t row, const float (&v)[1], const float*) {
+  __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v[0]), b, lane, row, 0);
 }
-template <int V>
-__device__ __forceinline__ void put(gchar* p, uint32_t off, const float (&v)[V], const uint16_t*) {
-  if constexpr (V == 1) {
-    gstr(p, off, __builtin_bit_cast(uint16_t, (__bf16)v[0]));
-  } else {
-    typedef float f2 __attribute__((ext_vector_type(2)));
-    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-    gstr(p, off, __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[0], v[1]}, b2)));
-  }
+__device__ __forceinline__ void put(rsrc_t b, uint32_t lane, uint32_t row, const float (&v)[1], const uint16_t*) {
+  __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v[0]), b, lane, row, 0);
+}
+__device__ __forceinline__ void put(rsrc_t b, uint32_t lane, uint32_t row, const float (&v)[2], const uint16_t*) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  __builtin_amdgcn_raw_buffer_store_b32(
+      __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[0], v[1]}, b2)), b, lane, row, 0);
 }
 
 // Fold of a piece, or of what lies behind it: h_out = a h + s.
@@ -211,16 +225,14 @@ struct Spot {
   }
 };
 
-// Steps t0 .. t0 + m - 1 (1 <= m <= TS) of one input; what lies behind them repeats the last.
-// One base a wave and 32-bit offsets (TS steps lie within 2^31 bytes): bases of their own for every
-// step do not fit the scalar registers.
+// Steps row .. row + m - 1 (1 <= m <= TS) of one input; what lies behind them repeats the last.  (TS
+// steps lie within 2^31 bytes.)
 template <typename T, int V, int TS>
-__device__ __forceinline__ void load_steps(Io<T, V> (&r)[TS], const void* base, int64_t row, int64_t stride, int64_t d,
-                                           int m) {
-  const gchar* const p = uniform_ptr(static_cast<const char*>(base) + row * stride);
-  const uint32_t off = (uint32_t)(d * sizeof(T)), st = (uint32_t)stride;
+__device__ __forceinline__ void load_steps(Io<T, V> (&r)[TS], const void* base, int64_t row, int64_t stride,
+                                           uint32_t lane, int m) {
+  const rsrc_t b = rows_of(base, row * stride, (uint32_t)TS * (uint32_t)stride);
 #pragma unroll
-  for (int i = 0; i < TS; ++i) r[i].load(p, off + (uint32_t)min(i, m - 1) * st);
+  for (int i = 0; i < TS; ++i) r[i].load(b, lane, (uint32_t)min(i, m - 1) * (uint32_t)stride);
 }
 
 template <typename T, int V, int TS, int W, bool Z, bool OUT>
@@ -234,13 +246,13 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
   const int c0 = at.q * (W * TS), t0 = c0 + wave * TS;
   const int m = min(max(n - t0, 0), TS);
   const int64_t row = at.b * a.seqlen + t0, st = at.b * a.width + at.d;
-  gchar* const py = uniform_ptr(static_cast<const char*>(a.y) + row * (a.width * sizeof(T)));
   const uint32_t off = (uint32_t)(at.d * sizeof(T)), ws = (uint32_t)(a.width * sizeof(T));
+  const rsrc_t py = rows_of(a.y, row * ws, TS * ws);
   const T* const tag = nullptr;
   if (c0 >= n && at.q > 0) {  // behind the row's end
     const float o[V] = {};
     for (int i = 0; OUT && i < TS && t0 + i < seqlen; ++i)
-      put<V>(py, off + i * ws, o, tag);
+      put(py, off, i * ws, o, tag);
     return;
   }
   float dec[TS][V], u[TS][V], start[V];
@@ -249,9 +261,9 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
   Io<T, V> z[TS];
   if (m > 0) {
     Io<T, V> x[TS], ga[TS], gx[TS];
-    load_steps(ga, a.ga, row, a.as, at.d, m);
-    load_steps(gx, a.gx, row, a.is, at.d, m);
-    load_steps(x, a.x, row, a.xs, at.d, m);
+    load_steps(ga, a.ga, row, a.as, off, m);
+    load_steps(gx, a.gx, row, a.is, off, m);
+    load_steps(x, a.x, row, a.xs, off, m);
     float c2[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) c2[v] = a.log_a[at.d + v] * kLog2e;
@@ -263,7 +275,7 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
         dec[i][v] = s.a;
         u[i][v] = s.m() * s.sx * x[i].get(v);
       }
-    if (Z && OUT) load_steps(z, a.z, row, a.zs, at.d, m);
+    if (Z && OUT) load_steps(z, a.z, row, a.zs, off, m);
   }
   if (m < TS)
 #pragma unroll
@@ -325,7 +337,7 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
         o[v] = Z && OUT ? h[v] * silu(z[i].get(v)) : h[v];
         if (!ALL && i >= m) o[v] = 0.0f;
       }
-      if (OUT && (ALL || t0 + i < seqlen)) put<V>(py, off + i * ws, o, tag);
+      if (OUT && (ALL || t0 + i < seqlen)) put(py, off, i * ws, o, tag);
     }
   };
   if (m == TS)
@@ -338,8 +350,17 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
     for (int v = 0; v < V; ++v) a.h_last[st + v] = h[v];
 }
 
+// Values that are formed here and now: the compiler would put many of them off to where they are used, and hold what
+// they come from instead.
+__device__ __forceinline__ void settle(float& a) { asm volatile("" : "+v"(a)); }
+template <typename... F>
+__device__ __forceinline__ void settle(float& a, F&... more) {
+  settle(a);
+  settle(more...);
+}
+
 template <typename T, int V, int TS, int W, bool Z>
-__global__ void __launch_bounds__(64 * W, Z && V == 2 ? ZW : kWavesPerSimd) k_gated_bwd(const GatedArgs a) {
+__global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const GatedArgs a) {
   __shared__ Fold fwd[W][64 * V], rev[W][64 * V], pre[kBlock - 1][64 * V];
   __shared__ float front[64 * V];
   __shared__ int shared;
@@ -350,20 +371,20 @@ __global__ void __launch_bounds__(64 * W, Z && V == 2 ? ZW : kWavesPerSimd) k_ga
   const int m = min(max(n - t0, 0), TS);
   const int64_t row = at.b * a.seqlen + t0, st = at.b * a.width + at.d;
   const int64_t step = a.width * (int64_t)sizeof(T);
-  gchar* const px = uniform_ptr(static_cast<const char*>(a.dx) + row * step);
-  gchar* const pa = uniform_ptr(static_cast<const char*>(a.dga) + row * step);
-  gchar* const pi = uniform_ptr(static_cast<const char*>(a.dgx) + row * step);
-  gchar* const pz = uniform_ptr(static_cast<const char*>(a.dz) + row * step);
   const uint32_t off = (uint32_t)(at.d * sizeof(T)), ws = (uint32_t)step;
+  const rsrc_t px = rows_of(a.dx, row * step, TS * ws);
+  const rsrc_t pa = rows_of(a.dga, row * step, TS * ws);
+  const rsrc_t pi = rows_of(a.dgx, row * step, TS * ws);
+  const rsrc_t pz = rows_of(a.dz, row * step, TS * ws);
   const T* const tag = nullptr;
   float* const part = a.part + (at.b * a.pieces + c) * a.width + at.d;
   if (c0 >= n) {  // behind the row's end
     const float o[V] = {};
     for (int i = 0; i < TS && t0 + i < seqlen; ++i) {
-        put<V>(px, off + i * ws, o, tag);
-        put<V>(pa, off + i * ws, o, tag);
-        put<V>(pi, off + i * ws, o, tag);
-        if (Z) put<V>(pz, off + i * ws, o, tag);
+        put(px, off, i * ws, o, tag);
+        put(pa, off, i * ws, o, tag);
+        put(pi, off, i * ws, o, tag);
+        if (Z) put(pz, off, i * ws, o, tag);
       }
     if (wave == 0)
 #pragma unroll
@@ -377,11 +398,11 @@ __global__ void __launch_bounds__(64 * W, Z && V == 2 ? ZW : kWavesPerSimd) k_ga
   float dec[TS][V], sa[TS][V], kx[TS][V], inv[TS][V], la[V];  // kx = m sx, inv = 1 / m
   if (m > 0) {
     Io<T, V> ga[TS], gx[TS];
-    load_steps(ga, a.ga, row, a.as, at.d, m);
-    load_steps(gx, a.gx, row, a.is, at.d, m);
-    load_steps(x, a.x, row, a.xs, at.d, m);
-    load_steps(dy, a.dy, row, step, at.d, m);
-    if (Z) load_steps(z, a.z, row, a.zs, at.d, m);
+    load_steps(ga, a.ga, row, a.as, off, m);
+    load_steps(gx, a.gx, row, a.is, off, m);
+    load_steps(x, a.x, row, a.xs, off, m);
+    load_steps(dy, a.dy, row, step, off, m);
+    if (Z) load_steps(z, a.z, row, a.zs, off, m);
 #pragma unroll
     for (int v = 0; v < V; ++v) la[v] = a.log_a[at.d + v];
 #pragma unroll
@@ -394,16 +415,17 @@ __global__ void __launch_bounds__(64 * W, Z && V == 2 ? ZW : kWavesPerSimd) k_ga
         inv[i][v] = s.inv_m();
         kx[i][v] = s.m2 * inv[i][v] * s.sx;
       }
-      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int v = 0; v < V; ++v) settle(dec[i][v], sa[i][v], inv[i][v], kx[i][v]);
     }
   }
   if (m < TS)  // steps that do not exist hand everything on
 #pragma unroll
     for (int i = 0; i < TS; ++i)
       if (i >= m) {
-        x[i].zero();
-        dy[i].zero();
-        if (Z) z[i].zero();
+        x[i].r = 0;
+        dy[i].r = 0;
+        if (Z) z[i].r = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           dec[i][v] = 1.0f;
@@ -421,7 +443,6 @@ __global__ void __launch_bounds__(64 * W, Z && V == 2 ? ZW : kWavesPerSimd) k_ga
     for (int i = TS - 1; i >= 0; --i) {
       const float e = Z ? dy[i].get(v) * silu(z[i].get(v)) : dy[i].get(v);
       r[v].s = dec[i][v] * (e + r[v].s);
-      __builtin_amdgcn_sched_barrier(0);
     }
     r[v].a = f[v].a;
     fwd[wave][lane * V + v] = f[v];
@@ -467,8 +488,12 @@ __global__ void __launch_bounds__(64 * W, Z && V == 2 ? ZW : kWavesPerSimd) k_ga
         dz[v] = i < m ? d * h[v] * q * __builtin_fmaf(zv, 1.0f - q, 1.0f) : 0.0f;
       }
     }
-    if (Z && t0 + i < seqlen) put<V>(pz, off + i * ws, dz, tag);
-    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      settle(gs[i][v], ka[i][v], ki[i][v], h[v]);
+      if (Z) settle(e[i][v]);
+    }
+    if (Z) put(pz, t0 + i < seqlen ? off : kNowhere, i * ws, dz, tag);
   }
   if (a.pieces > 1) {
     collect<V, W>(l, wave, lane, fp, sp, a.width, pre, front);
@@ -499,9 +524,9 @@ __global__ void __launch_bounds__(64 * W, Z && V == 2 ? ZW : kWavesPerSimd) k_ga
         p[v] = dec[i][v] * g;
       }
       if (ALL || t0 + i < seqlen) {
-        put<V>(px, off + i * ws, dx, tag);
-        put<V>(pa, off + i * ws, da, tag);
-        put<V>(pi, off + i * ws, di, tag);
+        put(px, off, i * ws, dx, tag);
+        put(pa, off, i * ws, da, tag);
+        put(pi, off, i * ws, di, tag);
       }
     }
   };
