@@ -21,6 +21,7 @@
 // P_t = a_t (e_t + P_{t+1}), e = dy silu(z): what reaches the state before step
 // t.  The states inside a piece are formed again from the state at its
 // start, saved by the forward call or by a forward pass without outputs.
+#include "col_sum.h"
 #include "gated_launch.h"
 #include "gated_math.h"
 
@@ -558,30 +559,6 @@ __global__ void __launch_bounds__(256) k_gated_clear(uint4* p, int64_t n) {
   if (i < n) p[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
 }
 
-// out[d] = sum of part's rows in a fixed order: 16 columns a workgroup, 64 interleaved sums a column,
-// joined pairwise.
-__global__ void __launch_bounds__(1024) k_gated_sum(const float* part, float* out, int64_t rows, int64_t width) {
-  __shared__ float s[64][17];
-  const int c = threadIdx.x & 15, k0 = threadIdx.x >> 4;
-  const int64_t col = (int64_t)blockIdx.x * 16 + c;
-  float v = 0.0f;
-  if (col < width)
-    for (int64_t k = k0; k < rows; k += 8 * 64) {
-      float q[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = k + 64 * i < rows ? part[(k + 64 * i) * width + col] : 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v += q[i];
-    }
-  for (int d = 32; d > 0; d /= 2) {
-    s[k0][c] = v;
-    __syncthreads();
-    if (k0 < d) v += s[k0 + d][c];
-    __syncthreads();
-  }
-  if (k0 == 0 && col < width) out[col] = v;
-}
-
 #ifndef FS
 #define FS 16
 #define FW 8
@@ -739,8 +716,7 @@ hipError_t launch_gated_scan_bwd(const GatedScanLaunch& p) {
     if (rc != hipSuccess) return rc;
   }
   if (p.dlog_a == nullptr) return hipSuccess;
-  return launch(k_gated_sum, dim3((unsigned)((p.width + 15) / 16)), dim3(1024), 0, p.stream, part, p.dlog_a,
-                p.batch * pieces, p.width);
+  return col_sum(part, p.dlog_a, nullptr, 0, p.batch * pieces, p.width, p.stream);
 }
 
 }  // namespace ssm

@@ -6,9 +6,16 @@
 // with s(z) = z / (1 + e^-z) and r = 1 / sqrt(mean(t^2) + eps) over a group.
 // Gradient of n = w t r:  dt = r (w g) - t r^3 mean(w g t),  dw = sum g t r.
 //
-// A group of values belongs to a team of lanes that holds it in registers: 8, 16,
-// 32 or 64 lanes of a wave, or a whole workgroup whose size follows the group.
-// Every value is read once.
+// A group of values belongs to a team of lanes that holds it in registers, 8 or 16 values a lane: 8, 16, 32 or 64
+// lanes of a wave, or a whole workgroup whose size follows the group.  Every value is read once, all
+// sums over a row close together (one barrier where the team is a workgroup), and a gradient's team adds up
+// its rows' weight gradients in registers.
+//
+// Bound by HBM (a copy reaches 5.1 to 5.3 TB/s): the gated norm of 32768 rows of 5120 in bf16 takes 185 us, 5.4
+// TB/s; its gradient over 8 groups of 512 in 16384 rows 127 us, 5.3 TB/s; the residual norm of 32768 x 2560 with
+// an fp32 stream 181 us, 5.6 TB/s; its gradient of 16384 x 2560 147 us, 5.1 TB/s.  Groups that are not whole 16-byte
+// pieces are read value by value (gradient of 8192 x 2501: 94 us, 3.9 TB/s).
+#include "col_sum.h"
 #include "gated_launch.h"
 #include "ssm_device.h"
 
@@ -37,6 +44,7 @@ struct Eight<float, true> {
     const uint32_t v = a[j / 4][j % 4];
     return __builtin_bit_cast(float, v);
   }
+  __device__ __forceinline__ void forget() {}
 };
 template <>
 struct Eight<uint16_t, true> {
@@ -47,6 +55,8 @@ struct Eight<uint16_t, true> {
     const uint32_t v = a[j / 2];
     return __builtin_bit_cast(float, j % 2 ? v & 0xffff0000u : v << 16);
   }
+  // What was derived from the values so far is formed again, not held.
+  __device__ __forceinline__ void forget() { asm volatile("" : "+v"(a)); }
 };
 template <typename T>
 struct Eight<T, false> {
@@ -60,6 +70,7 @@ struct Eight<T, false> {
     for (int j = 0; j < 8; ++j) a[j] = j * step < left ? p[j * step] : T(0);
   }
   __device__ __forceinline__ float get(int j) const { return io_to_f32(a[j]); }
+  __device__ __forceinline__ void forget() {}
 };
 
 template <bool VEC>
@@ -108,14 +119,14 @@ __device__ __forceinline__ float lane_sum(float v) {
 // A lane's place: TEAM lanes a group (0: the whole workgroup), NV pieces of 8
 // values a lane.  Team q of all takes group q % groups of rows q / groups,
 // q / groups + dr, ...
-constexpr int kMaxWaves = 16;
+constexpr int kMaxWaves = 16, kMaxSums = 8;
 template <int TEAM, int NV, bool VEC>
 struct Place {
   int lanes, ln, dim;  // lanes of the team, this one, values of a group
   int64_t team, row, dr, col;  // col: the group's first value in its row
   int phase = 0;
-  float (*red)[2][kMaxWaves];
-  __device__ __forceinline__ Place(int dim_, int64_t groups, float (*red_)[2][kMaxWaves]) : dim(dim_), red(red_) {
+  float (*red)[kMaxWaves][kMaxSums];
+  __device__ __forceinline__ Place(int dim_, int64_t groups, float (*red_)[kMaxWaves][kMaxSums]) : dim(dim_), red(red_) {
     lanes = TEAM > 0 ? TEAM : (int)blockDim.x;
     ln = TEAM > 0 ? (int)threadIdx.x % (TEAM > 0 ? TEAM : 1) : (int)threadIdx.x;
     const int per = TEAM > 0 ? (int)blockDim.x / (TEAM > 0 ? TEAM : 1) : 1;
@@ -139,42 +150,41 @@ struct Place {
   __device__ __forceinline__ void store(T* p, const float* x, int v) const {
     if (left(v) > 0) put8<VEC>(p + at(v), x, step(), left(v));
   }
+  __device__ __forceinline__ void weight(float (&w)[8], const float* p, int v) const {
+    Eight<float, VEC> e;
+    if (p != nullptr) load(e, p + col, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = p != nullptr ? e.get(j) : 1.0f;
+  }
   __device__ __forceinline__ void weights(float (&w)[NV][8], const float* p) const {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      Eight<float, VEC> e;
-      if (p != nullptr) load(e, p + col, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[v][j] = p != nullptr ? e.get(j) : 1.0f;
-    }
+    for (int v = 0; v < NV; ++v) weight(w[v], p, v);
   }
-  // Sums over the team, in every lane of it.  The waves' sums change places between two
-  // halves, so that one barrier a sum is enough.
-  __device__ __forceinline__ void sum(float& x, float& y, bool two) {
+  // The first N sums over the team, in every lane of it.  The waves' sums change places between
+  // two halves, so that one barrier a call is enough.
+  template <int N, int M>
+  __device__ __forceinline__ void sums(float (&x)[M]) {
     constexpr int W = TEAM > 0 ? TEAM : 64;
-    x = lane_sum<W>(x);
-    if (two) y = lane_sum<W>(y);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = lane_sum<W>(x[i]);
     if constexpr (TEAM == 0) {
-      const int waves = (int)blockDim.x / 64;
-      float(*const r)[kMaxWaves] = red[phase];
+      float(*const r)[kMaxSums] = red[phase];
       phase ^= 1;
-      if (threadIdx.x % 64 == 0) {
-        r[0][threadIdx.x / 64] = x;
-        if (two) r[1][threadIdx.x / 64] = y;
-      }
+      if (threadIdx.x % 64 == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[threadIdx.x / 64][i] = x[i];
       __syncthreads();
-      x = 0.0f;
-      y = two ? 0.0f : y;
-      for (int i = 0; i < waves; ++i) {
-        x += r[0][i];
-        if (two) y += r[1][i];
-      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = 0.0f;
+      for (int w = 0; w < (int)blockDim.x / 64; ++w)
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] += r[w][i];
     }
   }
-  __device__ __forceinline__ float sum(float x) {
-    float y = 0.0f;
-    sum(x, y, false);
-    return x;
+  __device__ __forceinline__ float sum(float v) {
+    float x[1] = {v};
+    sums<1>(x);
+    return x[0];
   }
 };
 
@@ -192,7 +202,7 @@ struct NormArgs {
 
 template <typename T, bool VEC, int TEAM, int NV, bool Z, bool FIRST>
 __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_gated_norm(const NormArgs a) {
-  __shared__ float red[2][2][kMaxWaves];
+  __shared__ __align__(16) float red[2][kMaxWaves][kMaxSums];
   Place<TEAM, NV, VEC> at((int)(a.width / a.groups), a.groups, red);
   const float inv = 1.0f / (float)at.dim;
   float w[NV][8];
@@ -229,8 +239,7 @@ __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_gated_norm(const Norm
   }
 }
 
-// Adds g t r to the sums of dw, turns g into the gradient of t.
-template <int NV>
+// rs, and what turns w g into the gradient of t.
 struct NormGrad {
   float rs, c;
   __device__ __forceinline__ void take(float ss, float sg, float inv, float eps) {
@@ -240,56 +249,101 @@ struct NormGrad {
   __device__ __forceinline__ float operator()(float t, float wg) const { return rs * __builtin_fmaf(-t, c, wg); }
 };
 
-template <typename T, bool VEC, int TEAM, int NV, bool Z, bool FIRST>
-__global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_gated_norm_bwd(const NormArgs a) {
-  __shared__ float red[2][2][kMaxWaves];
-  Place<TEAM, NV, VEC> at((int)(a.width / a.groups), a.groups, red);
-  const float inv = 1.0f / (float)at.dim;
-  float w[NV][8], dw[NV][8] = {};
-  at.weights(w, a.w);
-  for (int64_t r = at.row; r < a.rows; r += at.dr) {
-    Eight<T, VEC> x[NV], z[NV], dy[NV];
+// This lane's weights in the gradients, whose registers go to the sums and to the next row's values: in LDS
+// (32 bytes a lane and weight), or, with two pieces a lane, read again for every row.
+template <int NV, typename P>
+struct Kept {
+  const P& at;
+  const float* w;
+  float* lds;
+  __device__ __forceinline__ Kept(const P& at_, const float* w_, float* lds_)
+      : at(at_), w(w_), lds(lds_ + 4 * threadIdx.x) {
+    if (NV > 1) return;
+    float v[NV][8];
+    at.weights(v, w);
+    *reinterpret_cast<f32x4*>(lds) = f32x4{v[0][0], v[0][1], v[0][2], v[0][3]};
+    *reinterpret_cast<f32x4*>(lds + 4 * blockDim.x) = f32x4{v[0][4], v[0][5], v[0][6], v[0][7]};
+  }
+  __device__ __forceinline__ void get(float (&v)[8], int k) const {
+    if (NV > 1) {
+      at.weight(v, w, k);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x4 q = *reinterpret_cast<const f32x4*>(lds + 4 * i * blockDim.x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * i + j] = q[j];
+    }
+  }
+};
+constexpr int kKeptBytes = 32;
+
+// What the gated norm's gradient reads of a row.
+template <typename T, bool VEC, int NV, bool Z>
+struct GatedRow {
+  Eight<T, VEC> x[NV], z[NV], dy[NV];
+  template <typename P>
+  __device__ __forceinline__ void load(const NormArgs& a, const P& at, int64_t r) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       at.load(x[v], static_cast<const T*>(a.x) + r * a.xs + at.col, v);
       if (Z) at.load(z[v], static_cast<const T*>(a.z) + r * a.zs + at.col, v);
       at.load(dy[v], static_cast<const T*>(a.dy) + r * a.width + at.col, v);
     }
-    float ss = 0.0f, sg = 0.0f;
+  }
+};
+
+template <typename T, bool VEC, int TEAM, int NV, bool Z, bool FIRST>
+__global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_gated_norm_bwd(const NormArgs a) {
+  __shared__ __align__(16) float red[2][kMaxWaves][kMaxSums];
+  extern __shared__ __align__(16) float lds[];
+  Place<TEAM, NV, VEC> at((int)(a.width / a.groups), a.groups, red);
+  const float inv = 1.0f / (float)at.dim;
+  const Kept<NV, Place<TEAM, NV, VEC>> kept(at, a.w, lds);
+  float dw[NV][8] = {};
+  for (int64_t r = at.row; r < a.rows; r += at.dr) {
+    GatedRow<T, VEC, NV, Z> now;
+    now.load(a, at, r);
+    float s[2] = {};
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v) {
+      float w[8];
+      kept.get(w, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float t = x[v].get(j), g = dy[v].get(j);
-        if (Z) {
-          const float s = silu(z[v].get(j));
-          (FIRST ? t : g) *= s;
-        }
-        ss = __builtin_fmaf(t, t, ss);
-        sg = __builtin_fmaf(w[v][j] * g, t, sg);
+        float t = now.x[v].get(j), g = now.dy[v].get(j);
+        if (Z) (FIRST ? t : g) *= silu(now.z[v].get(j));
+        s[0] = __builtin_fmaf(t, t, s[0]);
+        s[1] = __builtin_fmaf(w[j] * g, t, s[1]);
       }
-    at.sum(ss, sg, true);
-    NormGrad<NV> n;
-    n.take(ss, sg, inv, a.eps);
+    }
+    at.template sums<2>(s);
+    NormGrad n;
+    n.take(s[0], s[1], inv, a.eps);
     T* const dx = static_cast<T*>(a.y) + r * a.width + at.col;
     T* const dz = static_cast<T*>(a.dz) + r * a.width + at.col;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      float ox[8], oz[8];
+      float w[8], ox[8], oz[8];
+      kept.get(w, v);
+      now.x[v].forget();
+      now.z[v].forget();
+      now.dy[v].forget();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float xv = x[v].get(j), dv = dy[v].get(j);
+        const float xv = now.x[v].get(j), dv = now.dy[v].get(j);
         if (Z) {
-          const float zv = z[v].get(j), q = hw_rcp(1.0f + hw_exp2(-zv * kLog2e));
+          const float zv = now.z[v].get(j), q = hw_rcp(1.0f + hw_exp2(-zv * kLog2e));
           const float s = zv * q, slope = q * __builtin_fmaf(zv, 1.0f - q, 1.0f);
           const float t = FIRST ? xv * s : xv, g = FIRST ? dv : dv * s;
-          const float dt = n(t, w[v][j] * g);
+          const float dt = n(t, w[j] * g);
           dw[v][j] = __builtin_fmaf(g * t, n.rs, dw[v][j]);
           ox[j] = FIRST ? dt * s : dt;
-          oz[j] = (FIRST ? dt * xv : dv * (w[v][j] * (t * n.rs))) * slope;
+          oz[j] = (FIRST ? dt * xv : dv * (w[j] * (t * n.rs))) * slope;
         } else {
           dw[v][j] = __builtin_fmaf(dv * xv, n.rs, dw[v][j]);
-          ox[j] = n(xv, w[v][j] * dv);
+          ox[j] = n(xv, w[j] * dv);
         }
       }
       at.store(dx, ox, v);
@@ -320,7 +374,7 @@ struct ResArgs {
 
 template <typename T, typename R, bool VEC, int TEAM, int NV, bool POST>
 __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_residual_norm(const ResArgs a) {
-  __shared__ float red[2][2][kMaxWaves];
+  __shared__ __align__(16) float red[2][kMaxWaves][kMaxSums];
   Place<TEAM, NV, VEC> at((int)a.width, 1, red);
   const float inv = 1.0f / (float)at.dim;
   float wo[NV][8], wp[NV][8];
@@ -368,79 +422,83 @@ __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_residual_norm(const R
   }
 }
 
-template <typename T, typename R, bool VEC, int TEAM, int NV, bool POST>
-__global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_residual_norm_bwd(const ResArgs a) {
-  __shared__ float red[2][2][kMaxWaves];
-  Place<TEAM, NV, VEC> at((int)a.width, 1, red);
-  const float inv = 1.0f / (float)at.dim;
-  float wo[NV][8], wp[NV][8], dwo[NV][8] = {}, dwp[NV][8] = {};
-  at.weights(wo, a.w_post);
-  at.weights(wp, a.w_pre);
-  for (int64_t r = at.row; r < a.rows; r += at.dr) {
-    Eight<T, VEC> x[NV], dy[NV];
-    Eight<R, VEC> e[NV], de[NV];
+// What the residual norm's gradient reads of a row.
+template <typename T, typename R, bool VEC, int NV>
+struct ResRow {
+  Eight<T, VEC> x[NV], dy[NV];
+  Eight<R, VEC> e[NV], de[NV];
+  template <typename P>
+  __device__ __forceinline__ void load(const ResArgs& a, const P& at, int64_t r) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      if (a.x != nullptr)
-        at.load(x[v], static_cast<const T*>(a.x) + r * a.xs, v);
-      else
-        x[v].zero();
+      x[v].zero();
+      de[v].zero();
+      if (a.x != nullptr) at.load(x[v], static_cast<const T*>(a.x) + r * a.xs, v);
       at.load(dy[v], static_cast<const T*>(a.dy) + r * a.width, v);
       at.load(e[v], static_cast<const R*>(a.res) + r * a.width, v);
-      if (a.dres_out != nullptr)
-        at.load(de[v], static_cast<const R*>(a.dres_out) + r * a.width, v);
-      else
-        de[v].zero();
+      if (a.dres_out != nullptr) at.load(de[v], static_cast<const R*>(a.dres_out) + r * a.width, v);
     }
-    float ss = 0.0f, sg = 0.0f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float t = e[v].get(j);
-        ss = __builtin_fmaf(t, t, ss);
-        sg = __builtin_fmaf(wp[v][j] * dy[v].get(j), t, sg);
-      }
-    at.sum(ss, sg, true);
-    NormGrad<NV> n;
-    n.take(ss, sg, inv, a.eps);
-    // The gradient of the sum, then of what was added.
-    float g[NV][8], sx = 0.0f, sp = 0.0f;
+  }
+};
+
+template <typename T, typename R, bool VEC, int TEAM, int NV, bool POST>
+__global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_residual_norm_bwd(const ResArgs a) {
+  __shared__ __align__(16) float red[2][kMaxWaves][kMaxSums];
+  extern __shared__ __align__(16) float lds[];
+  Place<TEAM, NV, VEC> at((int)a.width, 1, red);
+  const float inv = 1.0f / (float)at.dim;
+  const Kept<NV, Place<TEAM, NV, VEC>> pre(at, a.w_pre, lds), post(at, a.w_post, lds + 8 * blockDim.x);
+  float dwo[NV][8] = {}, dwp[NV][8] = {};
+  for (int64_t r = at.row; r < a.rows; r += at.dr) {
+    ResRow<T, R, VEC, NV> now;
+    now.load(a, at, r);
+    // With g the gradient of the sum R: g = rs (w_pre dy - R c) + dres_out, and for x's own norm sum(w_post alpha g x),
+    // which falls into three sums that need neither rs nor c: all sums close at once.
+    float s[6] = {};
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
+      float wp[8], wo[8];
+      pre.get(wp, v);
+      if (POST) post.get(wo, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float t = e[v].get(j), d = dy[v].get(j);
-        dwp[v][j] = __builtin_fmaf(d * t, n.rs, dwp[v][j]);
-        g[v][j] = n(t, wp[v][j] * d) + de[v].get(j);
-      }
-      if (a.dres != nullptr) at.store(static_cast<R*>(a.dres) + r * a.width, g[v], v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        g[v][j] *= a.alpha;
+        const float t = now.e[v].get(j), wd = wp[j] * now.dy[v].get(j);
+        s[0] = __builtin_fmaf(t, t, s[0]);
+        s[1] = __builtin_fmaf(wd, t, s[1]);
         if (POST) {
-          const float t = x[v].get(j);
-          sx = __builtin_fmaf(t, t, sx);
-          sp = __builtin_fmaf(wo[v][j] * g[v][j], t, sp);
+          const float x = now.x[v].get(j), wx = wo[j] * x;
+          s[2] = __builtin_fmaf(x, x, s[2]);
+          s[3] = __builtin_fmaf(wx, wd, s[3]);
+          s[4] = __builtin_fmaf(wx, t, s[4]);
+          s[5] = __builtin_fmaf(wx, now.de[v].get(j), s[5]);
         }
       }
     }
-    NormGrad<NV> m;
+    at.template sums<POST ? 6 : 2>(s);
+    NormGrad n, m;
+    n.take(s[0], s[1], inv, a.eps);
     m.rs = 1.0f;
     m.c = 0.0f;
-    if (POST) {
-      at.sum(sx, sp, true);
-      m.take(sx, sp, inv, a.eps);
-    }
+    if (POST) m.take(s[2], a.alpha * __builtin_fmaf(n.rs, __builtin_fmaf(-n.c, s[4], s[3]), s[5]), inv, a.eps);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
+      float wp[8], wo[8], g[8], gx[8];
+      pre.get(wp, v);
+      post.get(wo, v);
+      now.e[v].forget();
+      now.dy[v].forget();
+      now.x[v].forget();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float t = x[v].get(j);
-        dwo[v][j] = __builtin_fmaf(g[v][j] * t, m.rs, dwo[v][j]);
-        g[v][j] = POST ? m(t, wo[v][j] * g[v][j]) : wo[v][j] * g[v][j];
+        const float t = now.e[v].get(j), d = now.dy[v].get(j), x = now.x[v].get(j);
+        dwp[v][j] = __builtin_fmaf(d * t, n.rs, dwp[v][j]);
+        g[j] = n(t, wp[j] * d) + now.de[v].get(j);
+        const float ag = a.alpha * g[j];
+        dwo[v][j] = __builtin_fmaf(ag * x, m.rs, dwo[v][j]);
+        gx[j] = POST ? m(x, wo[j] * ag) : wo[j] * ag;
       }
-      at.store(static_cast<T*>(a.dx) + r * a.width, g[v], v);
+      if (a.dres != nullptr) at.store(static_cast<R*>(a.dres) + r * a.width, g, v);
+      at.store(static_cast<T*>(a.dx) + r * a.width, gx, v);
     }
   }
   if (a.part == nullptr || at.row >= a.rows) return;
@@ -451,34 +509,6 @@ __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_residual_norm_bwd(con
   }
 }
 
-// dw[c] = sum over the teams' rows of part, in a fixed order: 16 columns a workgroup, 64
-// interleaved sums a column (eight loads of each on their way), joined pairwise.
-__global__ void __launch_bounds__(1024) k_norm_sum(const float* part, float* dw0, float* dw1, int64_t second,
-                                                   int32_t n, int64_t width) {
-  __shared__ float s[64][17];
-  float* const dw = blockIdx.y == 0 ? dw0 : dw1;
-  if (dw == nullptr) return;
-  const int c = threadIdx.x & 15, k0 = threadIdx.x >> 4;
-  const int64_t col = (int64_t)blockIdx.x * 16 + c;
-  const float* const p = part + (blockIdx.y == 0 ? 0 : second) + col;
-  float v = 0.0f;
-  if (col < width)
-    for (int k = k0; k < n; k += 8 * 64) {
-      float q[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = k + 64 * i < n ? p[(int64_t)(k + 64 * i) * width] : 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v += q[i];
-    }
-  for (int d = 32; d > 0; d /= 2) {
-    s[k0][c] = v;
-    __syncthreads();
-    if (k0 < d) v += s[k0 + d][c];
-    __syncthreads();
-  }
-  if (k0 == 0 && col < width) dw[col] = v;
-}
-
 // The shape of a launch: lanes a team (0: the workgroup), pieces a lane, threads and
 // workgroups.
 struct Shape {
@@ -487,10 +517,17 @@ struct Shape {
   unsigned grid;
 };
 
-constexpr int64_t kThreads = 256 * 1024;  // lanes in flight
+// Workgroups of w waves a CU is given, each of which walks every so-many-th row.
+// Forward: eight times what a CU holds at once (32 waves of one piece a lane, 16 of two), so that CUs that
+// get ahead take more (32768 rows of 5120, gate first: 185 us; four times 194, once 229; 32768 x 2560 with
+// residual: 181, 188, 201; against that 32768 x 1024: 36.9, 34.7, 36.2).
+// Gradients: eight waves, in whole workgroups: more only add sums of weights to write and to join, and
+// rows in between (16384 x 2560 with residual: 147 us, with 20 waves 171, with 5 163; 32768 x 768: 88, 96, 122;
+// 16384 x 8 x 512: 127, 135, 194; 8192 x 2501: 94, 129, 141).
+int64_t groups_per_cu(int w, int nv, bool grad) { return grad ? (w < 8 ? (7 + w) / w : 1) : 8 * (nv == 1 ? 32 / w : 1); }
 
-// rows x groups teams of work; most: teams that may be launched at most per group.
-Shape shape_of(int64_t rows, int64_t dim, int64_t groups) {
+// rows x groups teams of work.
+Shape shape_of(int64_t rows, int64_t dim, int64_t groups, bool grad) {
   Shape s{};
   const int64_t pieces = (dim + 7) / 8;
   if (pieces <= 64) {
@@ -503,8 +540,8 @@ Shape shape_of(int64_t rows, int64_t dim, int64_t groups) {
     s.threads = (int)((pieces + 64 * s.nv - 1) / (64 * s.nv) * 64);
   }
   const int per = s.team > 0 ? s.threads / s.team : 1;
-  // Teams: what the chip holds, no more than there is work, whole workgroups and whole rows of groups.
-  int64_t rows_at_once = kThreads / s.threads * per / groups;
+  // Teams: no more than there is work, whole workgroups and whole rows of groups.
+  int64_t rows_at_once = 256 * groups_per_cu(s.threads / 64, s.nv, grad) * per / groups;
   if (rows_at_once > rows) rows_at_once = rows;
   if (rows_at_once < 1) rows_at_once = 1;
   while (rows_at_once * groups % per != 0) ++rows_at_once;
@@ -592,7 +629,8 @@ hipError_t go_gated(const GatedNormLaunch& p, const NormArgs& a, const Shape& s)
           constexpr int TEAM = decltype(team)::value, NV = decltype(nv)::value;
           constexpr bool VEC = decltype(vec)::value, Z = decltype(z)::value, FIRST = decltype(first)::value || !Z;
           if constexpr (GRAD)
-            return launch(k_gated_norm_bwd<T, VEC, TEAM, NV, Z, FIRST>, dim3(s.grid), dim3(s.threads), 0, p.stream, a);
+            return launch(k_gated_norm_bwd<T, VEC, TEAM, NV, Z, FIRST>, dim3(s.grid), dim3(s.threads),
+                          NV == 1 ? s.threads * kKeptBytes : 0, p.stream, a);
           else
             return launch(k_gated_norm<T, VEC, TEAM, NV, Z, FIRST>, dim3(s.grid), dim3(s.threads), 0, p.stream, a);
         });
@@ -609,18 +647,13 @@ hipError_t go_residual(const ResidualNormLaunch& p, const ResArgs& a, const Shap
         constexpr int TEAM = decltype(team)::value, NV = decltype(nv)::value;
         constexpr bool VEC = decltype(vec)::value, POST = decltype(post)::value;
         if constexpr (GRAD)
-          return launch(k_residual_norm_bwd<T, R, VEC, TEAM, NV, POST>, dim3(s.grid), dim3(s.threads), 0, p.stream, a);
+          return launch(k_residual_norm_bwd<T, R, VEC, TEAM, NV, POST>, dim3(s.grid), dim3(s.threads),
+                        NV == 1 ? 2 * s.threads * kKeptBytes : 0, p.stream, a);
         else
           return launch(k_residual_norm<T, R, VEC, TEAM, NV, POST>, dim3(s.grid), dim3(s.threads), 0, p.stream, a);
       });
     });
   });
-}
-
-hipError_t sum_parts(const float* part, float* dw0, float* dw1, int64_t second, int64_t n, int64_t width,
-                     hipStream_t stream) {
-  return launch(k_norm_sum, dim3((unsigned)((width + 15) / 16), 2), dim3(1024), 0, stream, part, dw0, dw1, second,
-                (int32_t)n, width);
 }
 
 // Rows of sums: the teams of one group, those without a row left out.
@@ -632,14 +665,14 @@ int64_t parts_of(const Shape& s, int64_t rows, int64_t groups) {
 }  // namespace
 
 int64_t gated_norm_bwd_floats(int64_t rows, int64_t width, int64_t groups) {
-  return rows == 0 ? 0 : parts_of(shape_of(rows, width / groups, groups), rows, groups) * width;
+  return rows == 0 ? 0 : parts_of(shape_of(rows, width / groups, groups, true), rows, groups) * width;
 }
 int64_t residual_norm_bwd_floats(int64_t rows, int64_t width) {
-  return rows == 0 ? 0 : 2 * parts_of(shape_of(rows, width, 1), rows, 1) * width;
+  return rows == 0 ? 0 : 2 * parts_of(shape_of(rows, width, 1, true), rows, 1) * width;
 }
 
 hipError_t launch_gated_norm(const GatedNormLaunch& p) {
-  const Shape s = shape_of(p.rows, p.width / p.groups, p.groups);
+  const Shape s = shape_of(p.rows, p.width / p.groups, p.groups, false);
   const NormArgs a = args(p);
   return p.bf16 ? go_gated<false, uint16_t>(p, a, s) : go_gated<false, float>(p, a, s);
 }
@@ -647,18 +680,18 @@ hipError_t launch_gated_norm(const GatedNormLaunch& p) {
 hipError_t launch_gated_norm_bwd(const GatedNormLaunch& p) {
   int64_t n = 0;
   if (p.rows > 0) {
-    const Shape s = shape_of(p.rows, p.width / p.groups, p.groups);
+    const Shape s = shape_of(p.rows, p.width / p.groups, p.groups, true);
     NormArgs a = args(p);
     a.part = p.dw != nullptr ? p.workspace : nullptr;
     n = parts_of(s, p.rows, p.groups);
     const hipError_t rc = p.bf16 ? go_gated<true, uint16_t>(p, a, s) : go_gated<true, float>(p, a, s);
     if (rc != hipSuccess) return rc;
   }
-  return p.dw == nullptr ? hipSuccess : sum_parts(p.workspace, p.dw, nullptr, 0, n, p.width, p.stream);
+  return p.dw == nullptr ? hipSuccess : col_sum(p.workspace, p.dw, nullptr, 0, n, p.width, p.stream);
 }
 
 hipError_t launch_residual_norm(const ResidualNormLaunch& p) {
-  const Shape s = shape_of(p.rows, p.width, 1);
+  const Shape s = shape_of(p.rows, p.width, 1, false);
   const ResArgs a = args(p);
   if (!p.bf16) return go_residual<false, float, float>(p, a, s);
   return p.res_bf16 ? go_residual<false, uint16_t, uint16_t>(p, a, s) : go_residual<false, uint16_t, float>(p, a, s);
@@ -668,7 +701,7 @@ hipError_t launch_residual_norm_bwd(const ResidualNormLaunch& p) {
   const bool want = p.dw_pre != nullptr || p.dw_post != nullptr;
   int64_t n = 0, second = 0;
   if (p.rows > 0) {
-    const Shape s = shape_of(p.rows, p.width, 1);
+    const Shape s = shape_of(p.rows, p.width, 1, true);
     ResArgs a = args(p);
     a.part = want ? p.workspace : nullptr;
     n = parts_of(s, p.rows, 1);
@@ -678,7 +711,7 @@ hipError_t launch_residual_norm_bwd(const ResidualNormLaunch& p) {
                                        : go_residual<true, uint16_t, float>(p, a, s);
     if (rc != hipSuccess) return rc;
   }
-  return want ? sum_parts(p.workspace, p.dw_pre, p.dw_post, second, n, p.width, p.stream) : hipSuccess;
+  return want ? col_sum(p.workspace, p.dw_pre, p.dw_post, second, n, p.width, p.stream) : hipSuccess;
 }
 
 }  // namespace ssm
