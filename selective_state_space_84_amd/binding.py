@@ -695,6 +695,8 @@ def _steps(t, what: str) -> Tuple[Optional[int], int]:
     if t.is_contiguous():
         return t.data_ptr() or None, width
     st = t.stride()
+    if len(st) == 2 and st[1] == 1 and shape[0] > 1 and st[0] >= width:
+        return t.data_ptr() or None, st[0]
     ok = st[-1] == 1 or width <= 1
     step = rows = None
     for n, s in zip(reversed(shape[:-1]), reversed(st[:-1])):
@@ -712,13 +714,46 @@ def _steps(t, what: str) -> Tuple[Optional[int], int]:
 
 
 def _gated_shapes(x, ga, gx, log_a, z, lead):
+    """x's shape, after one comparison for the usual case; the checks one by one name what is wrong."""
     import torch
-    if x.dim() != lead + 1:
-        raise ValueError("x must have %d axes, got %s" % (lead + 1, tuple(x.shape)))
-    _want(ga, x.shape, x.dtype, "ga")
-    _want(gx, x.shape, x.dtype, "gx")
-    _want(z, x.shape, x.dtype, "z")
-    _want(log_a, x.shape[-1:], torch.float32, "log_a")
+    shape, dt = x.shape, x.dtype
+    if len(shape) == lead + 1 and ga.shape == shape and gx.shape == shape and ga.dtype is dt and gx.dtype is dt and \
+            log_a.shape == shape[-1:] and log_a.dtype is torch.float32 and \
+            (z is None or (z.shape == shape and z.dtype is dt)):
+        return shape
+    if len(shape) != lead + 1:
+        raise ValueError("x must have %d axes, got %s" % (lead + 1, tuple(shape)))
+    _want(ga, shape, dt, "ga")
+    _want(gx, shape, dt, "gx")
+    _want(z, shape, dt, "z")
+    _want(log_a, shape[-1:], torch.float32, "log_a")
+    raise ValueError("arguments do not fit together")
+
+
+def _like(x):
+    """A dense tensor like x."""
+    import torch
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
+def _scratch(workspace, need, x, what):
+    """_workspace on x's device."""
+    import torch
+    if workspace is None and 0 < need < _TOO_BIG:
+        return x.new_empty(need, dtype=torch.uint8), need
+    return _workspace(workspace, need, x.device, what)
+
+
+_TOO_BIG = ctypes.c_size_t(-1).value
+
+
+def _outs(g, names, x):
+    """_fill with x's device and, where nothing is given, fewer calls."""
+    if g:
+        _fill(g, names, x.device)
+        return
+    for name, shape, dtype in names:
+        g[name] = _like(x) if dtype is x.dtype and shape == x.shape else x.new_empty(shape, dtype=dtype)
 
 
 def _ckpt_floats(lib, batch, seqlen, width, what):
@@ -740,26 +775,28 @@ def ssm_gated_scan_fwd(x, ga, gx, log_a, z=None, *, lengths=None, h0=None, y=Non
     holds states on the way for ssm_gated_scan_bwd.
     """
     import torch
-    _gated_shapes(x, ga, gx, log_a, z, 2)
-    batch, seqlen, width = x.shape
+    batch, seqlen, width = _gated_shapes(x, ga, gx, log_a, z, 2)
     dt, f32 = _io_dtype(x), torch.float32
     st = (batch, width)
-    _want(lengths, (batch,), torch.int32, "lengths")
-    _want(h0, st, f32, "h0")
-    _want(y, x.shape, x.dtype, "y")
-    _want(h_last, st, f32, "h_last")
+    if lengths is not None:
+        _want(lengths, (batch,), torch.int32, "lengths")
+    if h0 is not None:
+        _want(h0, st, f32, "h0")
+    if y is not None:
+        _want(y, x.shape, x.dtype, "y")
+    if h_last is not None:
+        _want(h_last, st, f32, "h_last")
     lib = load_library()
     with _scope(stream, x, ga, gx, log_a, z, lengths, h0, y, h_last, workspace):
-        dev = x.device
         if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            y = _like(x)
         if h_last is None and want_h_last:
-            h_last = torch.empty(st, dtype=f32, device=dev)
+            h_last = x.new_empty(st, dtype=f32)
         ckpt = None
         if want_ckpt:
-            ckpt = torch.empty(_ckpt_floats(lib, batch, seqlen, width, "ssm_gated_scan_fwd"), dtype=f32, device=dev)
+            ckpt = x.new_empty(_ckpt_floats(lib, batch, seqlen, width, "ssm_gated_scan_fwd"), dtype=f32)
         need = lib.ssm_gated_scan_fwd_workspace_size(batch, seqlen, width, dt)
-        workspace, have = _workspace(workspace, need, dev, "ssm_gated_scan_fwd")
+        workspace, have = _scratch(workspace, need, x, "ssm_gated_scan_fwd")
         (xp, xs), (ap, as_), (ip, is_) = _steps(x, "x"), _steps(ga, "ga"), _steps(gx, "gx")
         zp, zs = (None, 0) if z is None else _steps(z, "z")
         rc = lib.ssm_gated_scan_fwd(xp, ap, ip, _dense(log_a, "log_a"), zp, _dense(lengths, "lengths"),
@@ -780,18 +817,20 @@ def ssm_gated_scan_bwd(x, ga, gx, log_a, z=None, *, dy, lengths=None, h0=None, d
     (recomputed).  Outputs are allocated unless given in ``grads``.
     """
     import torch
-    _gated_shapes(x, ga, gx, log_a, z, 2)
-    batch, seqlen, width = x.shape
-    dt, f32 = _io_dtype(x), torch.float32
+    shape = batch, seqlen, width = _gated_shapes(x, ga, gx, log_a, z, 2)
+    dt, f32, xt = _io_dtype(x), torch.float32, x.dtype
     st = (batch, width)
-    _want(lengths, (batch,), torch.int32, "lengths")
-    _want(h0, st, f32, "h0")
-    _want(dy, x.shape, x.dtype, "dy")
-    _want(dh_last, st, f32, "dh_last")
+    _want(dy, shape, xt, "dy")
+    if lengths is not None:
+        _want(lengths, (batch,), torch.int32, "lengths")
+    if h0 is not None:
+        _want(h0, st, f32, "h0")
+    if dh_last is not None:
+        _want(dh_last, st, f32, "dh_last")
     g = dict(grads or {})
-    names = [("dx", x.shape, x.dtype), ("dga", x.shape, x.dtype), ("dgx", x.shape, x.dtype)]
+    names = [("dx", shape, xt), ("dga", shape, xt), ("dgx", shape, xt)]
     if z is not None:
-        names.append(("dz", x.shape, x.dtype))
+        names.append(("dz", shape, xt))
     if want_dlog_a or "dlog_a" in g:
         names.append(("dlog_a", (width,), f32))
     if want_dh0 or "dh0" in g:
@@ -800,11 +839,11 @@ def ssm_gated_scan_bwd(x, ga, gx, log_a, z=None, *, dy, lengths=None, h0=None, d
     if ckpt is not None:
         _want(ckpt, (_ckpt_floats(lib, batch, seqlen, width, "ssm_gated_scan_bwd"),), f32, "ckpt")
     with _scope(stream, x, ga, gx, log_a, z, lengths, h0, dy, dh_last, ckpt, workspace, *g.values()):
-        _fill(g, names, x.device)
+        _outs(g, names, x)
         # Saved states of no steps are no pointer: the recomputation of none costs nothing.
         cp = _dense(ckpt, "ckpt")
         need = lib.ssm_gated_scan_bwd_workspace_size(batch, seqlen, width, dt, 0 if cp is None else 1)
-        workspace, have = _workspace(workspace, need, x.device, "ssm_gated_scan_bwd")
+        workspace, have = _scratch(workspace, need, x, "ssm_gated_scan_bwd")
         (xp, xs), (ap, as_), (ip, is_) = _steps(x, "x"), _steps(ga, "ga"), _steps(gx, "gx")
         zp, zs = (None, 0) if z is None else _steps(z, "z")
         rc = lib.ssm_gated_scan_bwd(
@@ -825,16 +864,17 @@ def ssm_gated_scan_update(h, x, ga, gx, log_a, z=None, *, slots=None, y=None, st
     None when h holds the batch in order.
     """
     import torch
-    _gated_shapes(x, ga, gx, log_a, z, 1)
-    batch, width = x.shape
+    batch, width = _gated_shapes(x, ga, gx, log_a, z, 1)
     n_slots = h.shape[0]
     _want(h, (n_slots, width), torch.float32, "h")
-    _want(slots, (batch,), torch.int32, "slots")
-    _want(y, x.shape, x.dtype, "y")
+    if slots is not None:
+        _want(slots, (batch,), torch.int32, "slots")
+    if y is not None:
+        _want(y, x.shape, x.dtype, "y")
     dt = _io_dtype(x)
     with _scope(stream, x, h, slots, ga, gx, log_a, z, y):
         if y is None:
-            y = torch.empty((batch, width), dtype=x.dtype, device=x.device)
+            y = _like(x)
         (xp, xs), (ap, as_), (ip, is_) = _steps(x, "x"), _steps(ga, "ga"), _steps(gx, "gx")
         zp, zs = (None, 0) if z is None else _steps(z, "z")
         rc = load_library().ssm_gated_scan_update(
@@ -861,13 +901,16 @@ def ssm_gated_norm_fwd(x, z=None, w=None, *, groups=1, gate_first=True, eps=1e-6
     """
     import torch
     rows, width = _norm_rows(x, "x")
-    _want(z, x.shape, x.dtype, "z")
-    _want(w, (width,), torch.float32, "w")
-    _want(y, x.shape, x.dtype, "y")
+    if z is not None:
+        _want(z, x.shape, x.dtype, "z")
+    if w is not None:
+        _want(w, (width,), torch.float32, "w")
+    if y is not None:
+        _want(y, x.shape, x.dtype, "y")
     dt = _io_dtype(x)
     with _scope(stream, x, z, w, y):
         if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            y = _like(x)
         xp, xs = _steps(x, "x")
         zp, zs = (None, 0) if z is None else _steps(z, "z")
         rc = load_library().ssm_gated_norm_fwd(xp, zp, _dense(w, "w"), _dense(y, "y"), rows, width, groups, xs, zs,
@@ -895,9 +938,9 @@ def ssm_gated_norm_bwd(x, z=None, w=None, *, dy, groups=1, gate_first=True, eps=
         names.append(("dw", (width,), torch.float32))
     lib = load_library()
     with _scope(stream, x, z, w, dy, workspace, *g.values()):
-        _fill(g, names, x.device)
+        _outs(g, names, x)
         need = lib.ssm_gated_norm_bwd_workspace_size(rows, width, groups) if "dw" in g else 0
-        workspace, have = _workspace(workspace, need, x.device, "ssm_gated_norm_bwd")
+        workspace, have = _scratch(workspace, need, x, "ssm_gated_norm_bwd")
         xp, xs = _steps(x, "x")
         zp, zs = (None, 0) if z is None else _steps(z, "z")
         rc = lib.ssm_gated_norm_bwd(xp, zp, _dense(w, "w"), _dense(dy, "dy"), _dense(g["dx"], "dx"),
@@ -925,17 +968,22 @@ def ssm_residual_norm_fwd(x, residual, w_pre=None, w_post=None, *, alpha=1.0, po
         res_out.dtype if res_out is not None else (x.dtype if res_dtype is None else res_dtype))
     if res_dtype is not None and rt != res_dtype:
         raise ValueError("residual must be %s, got %s" % (res_dtype, rt))
-    _want(residual, x.shape, rt, "residual")
-    _want(res_out, x.shape, rt, "res_out")
-    _want(y, x.shape, x.dtype, "y")
-    _want(w_pre, (width,), torch.float32, "w_pre")
-    _want(w_post, (width,), torch.float32, "w_post")
+    if residual is not None:
+        _want(residual, x.shape, rt, "residual")
+    if res_out is not None:
+        _want(res_out, x.shape, rt, "res_out")
+    if y is not None:
+        _want(y, x.shape, x.dtype, "y")
+    if w_pre is not None:
+        _want(w_pre, (width,), torch.float32, "w_pre")
+    if w_post is not None:
+        _want(w_post, (width,), torch.float32, "w_post")
     dt, rd = _io_dtype(x), _res_dtype(rt)
     with _scope(stream, x, residual, w_pre, w_post, res_out, y):
         if res_out is None:
-            res_out = torch.empty(x.shape, dtype=rt, device=x.device)
+            res_out = _like(x) if rt is x.dtype else x.new_empty(x.shape, dtype=rt)
         if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            y = _like(x)
         xp, xs = _steps(x, "x")
         rc = load_library().ssm_residual_norm_fwd(
             xp, _dense(residual, "residual"), _dense(w_pre, "w_pre"), _dense(w_post, "w_post"),
@@ -965,26 +1013,31 @@ def ssm_residual_norm_bwd(x, res_out, w_pre=None, w_post=None, *, dy, dres_out=N
     """
     import torch
     rows, width = _norm_rows(res_out, "res_out")
-    _want(x, res_out.shape, dy.dtype, "x")
-    _want(dy, res_out.shape, dy.dtype, "dy")
-    _want(dres_out, res_out.shape, res_out.dtype, "dres_out")
-    _want(w_pre, (width,), torch.float32, "w_pre")
-    _want(w_post, (width,), torch.float32, "w_post")
-    dt, rd = _io_dtype(dy), _res_dtype(res_out.dtype)
+    shape, rt = res_out.shape, res_out.dtype
+    _want(dy, shape, dy.dtype, "dy")
+    if x is not None:
+        _want(x, shape, dy.dtype, "x")
+    if dres_out is not None:
+        _want(dres_out, shape, rt, "dres_out")
+    if w_pre is not None:
+        _want(w_pre, (width,), torch.float32, "w_pre")
+    if w_post is not None:
+        _want(w_post, (width,), torch.float32, "w_post")
+    dt, rd = _io_dtype(dy), _res_dtype(rt)
     g = dict(grads or {})
-    names = [("dx", res_out.shape, dy.dtype)]
+    names = [("dx", shape, dy.dtype)]
     if want_dres or "dres" in g:
-        names.append(("dres", res_out.shape, res_out.dtype))
+        names.append(("dres", shape, rt))
     for n in ("dw_pre", "dw_post"):
         if want_dw or n in g:
             names.append((n, (width,), torch.float32))
     lib = load_library()
     with _scope(stream, res_out, x, w_pre, w_post, dy, dres_out, workspace, *g.values()):
-        _fill(g, names, res_out.device)
+        _outs(g, names, dy)
         need = 0
         if "dw_pre" in g or "dw_post" in g:
             need = lib.ssm_residual_norm_bwd_workspace_size(rows, width)
-        workspace, have = _workspace(workspace, need, res_out.device, "ssm_residual_norm_bwd")
+        workspace, have = _scratch(workspace, need, dy, "ssm_residual_norm_bwd")
         xp, xs = (None, 0) if x is None else _steps(x, "x")
         rc = lib.ssm_residual_norm_bwd(
             xp, _dense(res_out, "res_out"), _dense(w_pre, "w_pre"), _dense(w_post, "w_post"), _dense(dy, "dy"),
