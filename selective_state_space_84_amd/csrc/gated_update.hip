@@ -1,5 +1,7 @@
 // One step of the gated recurrence (decode), in place on the states of a
-// batch of requests.
+// batch of requests: every lane forms the gates of its channels and moves their
+// state.  Bound by HBM for large batches (8 bytes of state and 8 to 10 of bf16
+// operands a channel) and by the launch for small ones.
 #include "gated_launch.h"
 #include "gated_math.h"
 
@@ -31,11 +33,11 @@ __global__ void __launch_bounds__(256) k_gated_update(const UpdateArgs a) {
   auto in = [&](const void* p, int64_t stride) {
     return *reinterpret_cast<const in_t*>(static_cast<const T*>(p) + b * stride + d);
   };
-  T* const y = static_cast<T*>(a.y) + b * a.width + d;
+  in_t out;
+  in_t* const y = reinterpret_cast<in_t*>(static_cast<T*>(a.y) + b * a.width + d);
   const int64_t slot = a.slots != nullptr ? a.slots[b] : b;
   if (slot < 0 || slot >= a.n_slots) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) io_store(y + j, 0.0f);
+    *y = in_t(T(0));
     return;
   }
   st_t* const hp = reinterpret_cast<st_t*>(a.h + slot * a.width + d);
@@ -48,9 +50,27 @@ __global__ void __launch_bounds__(256) k_gated_update(const UpdateArgs a) {
   for (int j = 0; j < V; ++j) {
     const GatedStep s = gated_step(io_to_f32(ga[j]), io_to_f32(gx[j]), c[j] * kLog2e);
     h[j] = __builtin_fmaf(s.a, h[j], s.m() * s.sx * io_to_f32(x[j]));
-    io_store(y + j, a.z != nullptr ? h[j] * silu(io_to_f32(z[j])) : h[j]);
+    T o;
+    io_store(&o, a.z != nullptr ? h[j] * silu(io_to_f32(z[j])) : h[j]);
+    out[j] = o;
   }
   *hp = h;
+  *y = out;
+}
+
+// Four channels a lane where every row allows accesses of four.
+bool fours(const GatedUpdateLaunch& p) {
+  const int64_t n = p.width | p.x_stride | p.ga_stride | p.gx_stride | (p.z != nullptr ? p.z_stride : 0);
+  uintptr_t io = 0;
+  for (const void* q : {p.x, p.ga, p.gx, p.z, (const void*)p.y}) io |= reinterpret_cast<uintptr_t>(q);
+  const uintptr_t f32 = reinterpret_cast<uintptr_t>(p.h) | reinterpret_cast<uintptr_t>(p.log_a);
+  return n % 4 == 0 && io % (p.bf16 ? 8 : 16) == 0 && f32 % 16 == 0;
+}
+
+template <typename T, int V>
+hipError_t go(const GatedUpdateLaunch& p, UpdateArgs a) {
+  a.tiles = (uint32_t)((p.width + 256 * V - 1) / (256 * V));
+  return launch(k_gated_update<T, V>, dim3((unsigned)(p.batch * a.tiles)), dim3(256), 0, p.stream, a);
 }
 
 }  // namespace
@@ -59,11 +79,9 @@ int64_t gated_update_tiles(int64_t width) { return (width + 255) / 256; }
 
 hipError_t launch_gated_scan_update(const GatedUpdateLaunch& p) {
   const UpdateArgs a{p.h, p.slots,   p.x,     p.ga,       p.gx,        p.z,         p.log_a,
-                     p.y, p.n_slots, p.width, p.x_stride, p.ga_stride, p.gx_stride, p.z_stride,
-                     (uint32_t)gated_update_tiles(p.width)};
-  const dim3 grid((unsigned)(p.batch * gated_update_tiles(p.width)));
-  if (p.bf16) return launch(k_gated_update<uint16_t, 1>, grid, dim3(256), 0, p.stream, a);
-  return launch(k_gated_update<float, 1>, grid, dim3(256), 0, p.stream, a);
+                     p.y, p.n_slots, p.width, p.x_stride, p.ga_stride, p.gx_stride, p.z_stride, 0};
+  if (fours(p)) return p.bf16 ? go<uint16_t, 4>(p, a) : go<float, 4>(p, a);
+  return p.bf16 ? go<uint16_t, 1>(p, a) : go<float, 1>(p, a);
 }
 
 }  // namespace ssm
