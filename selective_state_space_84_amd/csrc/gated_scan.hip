@@ -5,7 +5,7 @@
 // forms decays and inputs and folds them to h_out = A h_in + S; the waves' folds
 // meet in LDS, and the piece's fold is published.  The state that enters the
 // piece comes from the pieces before it: pieces are grouped in blocks of
-// kBlock, a block's last piece publishes the state behind the block, and the
+// 8 or 32, a block's last piece publishes the state behind the block, and the
 // others fold the (A, S) of the pieces before them in the block onto the state
 // in front of it.  So a sequence's chain is one hop a block long, its sums have a
 // fixed order, and every input is read once.
@@ -52,14 +52,11 @@ struct GatedArgs {
   uint32_t* tickets;  // [batch][tiles], all ones at first
   uint64_t* folds;   // [batch][pieces][width] (A, S)
   uint32_t* states;  // [batch][blocks][width]
-  int32_t pieces, tiles;
+  int32_t pieces, tiles, block;
   int32_t first;  // of all pieces of work, this launch's
 };
 
-#ifndef KB
-#define KB 8
-#endif
-constexpr int kBlock = KB;  // pieces
+constexpr int kMaxBlock = 32;  // pieces
 constexpr int kPolls = 1 << 20;
 #ifndef WPS
 #define WPS 4
@@ -164,12 +161,12 @@ __device__ __forceinline__ W wait_word(const W* p, W first) {
 struct Link {
   int q, j0, blk, before;  // j0: the first piece of q's block, `before`: how many pieces of it come before q
   bool heads, closes, ends;  // nothing comes before the block; q is the block's last piece; nothing comes behind q
-  __device__ __forceinline__ Link(int q_, int q0, int last) : q(q_) {
-    blk = q / kBlock;
-    heads = blk == q0 / kBlock;
-    j0 = heads ? q0 : blk * kBlock;
+  __device__ __forceinline__ Link(int q_, int q0, int last, int block) : q(q_) {
+    blk = q / block;
+    heads = blk == q0 / block;
+    j0 = heads ? q0 : blk * block;
     before = q - j0;
-    closes = q % kBlock == kBlock - 1;
+    closes = q % block == block - 1;
     ends = q == last;
   }
 };
@@ -180,28 +177,23 @@ struct Link {
 template <int V, int W>
 __device__ __forceinline__ void collect(const Link& l, int wave, int lane, const uint64_t* folds,
                                         const uint32_t* states, int64_t stride, Fold (*pre)[64 * V], float* front) {
-  constexpr int N = (kBlock + W - 1) / W;
-  uint64_t w[N][V];
+  for (int k = wave; k < l.before; k += W) {
+    const uint64_t* const p = folds + (l.j0 + k) * stride;
+    uint64_t w[V];
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (wave + i * W < l.before)
+    for (int v = 0; v < V; ++v) w[v] = read_word(p + v);
 #pragma unroll
-      for (int v = 0; v < V; ++v) w[i][v] = read_word(folds + (l.j0 + wave + i * W) * stride + v);
+    for (int v = 0; v < V; ++v) {
+      const uint64_t f = wait_word(p + v, w[v]);
+      pre[k][lane * V + v] = Fold{__builtin_bit_cast(float, (uint32_t)f), __builtin_bit_cast(float, (uint32_t)(f >> 32))};
+    }
+  }
   if (wave == W - 1 && !l.heads)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const uint32_t* const p = states + (l.blk - 1) * stride + v;
       front[lane * V + v] = __builtin_bit_cast(float, wait_word(p, read_word(p)));
     }
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (wave + i * W < l.before)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const uint64_t f = wait_word(folds + (l.j0 + wave + i * W) * stride + v, w[i][v]);
-        pre[wave + i * W][lane * V + v] =
-            Fold{__builtin_bit_cast(float, (uint32_t)f), __builtin_bit_cast(float, (uint32_t)(f >> 32))};
-      }
 }
 
 // Where a lane works: channels d .. d + V - 1 of row b, piece q of that chain.  Lanes behind the row's width do
@@ -238,7 +230,7 @@ __device__ __forceinline__ void load_steps(Io<T, V> (&r)[TS], const void* base, 
 
 template <typename T, int V, int TS, int W, bool Z, bool OUT>
 __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const GatedArgs a) {
-  __shared__ Fold folds[W][64 * V], pre[kBlock - 1][64 * V];
+  __shared__ Fold folds[W][64 * V], pre[kMaxBlock - 1][64 * V];
   __shared__ float front[64 * V];
   __shared__ int shared;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -258,7 +250,7 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
   }
   float dec[TS][V], u[TS][V], start[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) start[v] = a.h0 != nullptr && at.q < kBlock ? a.h0[st + v] : 0.0f;
+  for (int v = 0; v < V; ++v) start[v] = a.h0 != nullptr && at.q < a.block ? a.h0[st + v] : 0.0f;
   Io<T, V> z[TS];
   if (m > 0) {
     Io<T, V> x[TS], ga[TS], gx[TS];
@@ -300,9 +292,9 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
     folds[wave][lane * V + v] = f[v];
   }
   __syncthreads();
-  const Link l(at.q, 0, n > 0 ? (n - 1) / (W * TS) : 0);
+  const Link l(at.q, 0, n > 0 ? (n - 1) / (W * TS) : 0, a.block);
   uint64_t* const fp = a.folds + at.b * a.pieces * a.width + at.d;
-  uint32_t* const sp = a.states + at.b * ((a.pieces + kBlock - 1) / kBlock) * a.width + at.d;
+  uint32_t* const sp = a.states + at.b * ((a.pieces + a.block - 1) / a.block) * a.width + at.d;
   if (wave == 0 && !l.ends)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -362,7 +354,7 @@ __device__ __forceinline__ void settle(float& a, F&... more) {
 
 template <typename T, int V, int TS, int W, bool Z>
 __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const GatedArgs a) {
-  __shared__ Fold fwd[W][64 * V], rev[W][64 * V], pre[kBlock - 1][64 * V];
+  __shared__ Fold fwd[W][64 * V], rev[W][64 * V], pre[kMaxBlock - 1][64 * V];
   __shared__ float front[64 * V];
   __shared__ int shared;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -450,9 +442,9 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const Gated
     rev[wave][lane * V + v] = r[v];
   }
   __syncthreads();
-  const Link l(at.q, a.pieces - 1 - (n - 1) / (W * TS), a.pieces - 1);
+  const Link l(at.q, a.pieces - 1 - (n - 1) / (W * TS), a.pieces - 1, a.block);
   uint64_t* const fp = a.folds + at.b * a.pieces * a.width + at.d;
-  uint32_t* const sp = a.states + at.b * ((a.pieces + kBlock - 1) / kBlock) * a.width + at.d;
+  uint32_t* const sp = a.states + at.b * ((a.pieces + a.block - 1) / a.block) * a.width + at.d;
   if (wave == W - 1 && !l.ends)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -571,7 +563,11 @@ static_assert(kBwdSteps * kBwdWaves % kGatedCkpt == 0 && kGatedCkpt % kFwdSteps 
 constexpr int64_t kMaxGrid = 1 << 22;  // workgroups of a launch
 
 int64_t pieces_of(int64_t seqlen, int64_t len) { return seqlen <= len ? 1 : (seqlen + len - 1) / len; }
-int64_t blocks_of(int64_t pieces) { return (pieces + kBlock - 1) / kBlock; }
+// Pieces of a block.  A wide block has fewer hops, but every piece reads half a block of folds: worth it
+// where few chains leave the chip waiting for the hops (bf16, 32768 x 512: 64 us with 8, 51 with 32; 32768 x
+// 1024, 8 chains, 82 and 80; 32768 x 1536, 12 chains, 103 and 104; gradient and forward of 16384 x 256: 98 and 69).
+int64_t block_of(int64_t chains) { return chains <= 8 ? kMaxBlock : 8; }
+int64_t blocks_of(int64_t pieces) { return (pieces + 7) / 8; }  // room for the narrow ones
 // Words of 4 bytes that the chains use: the counters, the folds, the states.
 int64_t ticket_words(int64_t batch, int64_t width) { return (batch * ((width + 63) / 64) + 63) / 64 * 64; }
 int64_t chain_words(int64_t batch, int64_t width, int64_t pieces) {
@@ -621,6 +617,7 @@ GatedArgs args(const GatedScanLaunch& p, int64_t pieces, uint32_t* chain) {
   a.pieces = (int32_t)pieces;
   const int64_t lanes = pairs(p) ? 128 : 64;
   a.tiles = (int32_t)((p.width + lanes - 1) / lanes);
+  a.block = (int32_t)block_of(p.batch * a.tiles);
   a.tickets = chain;
   a.folds = reinterpret_cast<uint64_t*>(chain + ticket_words(p.batch, p.width));
   a.states = chain + ticket_words(p.batch, p.width) + 2 * p.batch * p.width * pieces;
