@@ -14,7 +14,7 @@ namespace {
 constexpr int64_t kMaxSteps = INT32_MAX - 256;
 constexpr int64_t kMaxWidth = (int64_t)1 << 23;
 constexpr int64_t kMaxStep = (int64_t)1 << 40;      // elements between rows
-constexpr int64_t kMaxScanStep = (int64_t)1 << 25;  // and between steps of a scan, which addresses 16 with 32-bit offsets
+constexpr int64_t kMaxScanStep = (int64_t)1 << 25;  // between steps of a scan, which addresses 16 by 32-bit offsets
 constexpr int64_t kMaxStates = (int64_t)1 << 31;
 // Every byte count below stays far inside 64 bits when no tensor has more elements than this.
 constexpr int64_t kMaxElems = (int64_t)1 << 48;

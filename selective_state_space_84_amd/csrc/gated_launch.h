@@ -16,7 +16,7 @@ struct GatedScanLaunch {
   const float* h0;         // nullable, [batch][width]
   void* y;
   float* h_last;           // nullable
-  float* ckpt;             // nullable: states before every kGatedCkpt-th step, written forwards and read by the gradient
+  float* ckpt;             // nullable: states before every kGatedCkpt-th step; the gradient reads them
   int64_t batch, seqlen, width;
   int64_t x_stride, ga_stride, gx_stride, z_stride;
   bool bf16;

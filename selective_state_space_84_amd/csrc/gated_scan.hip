@@ -1,26 +1,31 @@
 // Gated linear recurrence over whole sequences and its gradient.
 //
-// One pass over the data.  A workgroup takes a piece of the sequence, W waves of
-// TS steps each, for 64 V channels (V a lane).  A wave loads its steps at once,
-// forms decays and inputs and folds them to h_out = A h_in + S; the waves' folds
-// meet in LDS, and the piece's fold is published.  The state that enters the
-// piece comes from the pieces before it: pieces are grouped in blocks of
-// 8 or 32, a block's last piece publishes the state behind the block, and the
-// others fold the (A, S) of the pieces before them in the block onto the state
-// in front of it.  So a sequence's chain is one hop a block long, its sums have a
-// fixed order, and every input is read once.
+// One pass over the data.  A workgroup takes a piece of the sequence, W waves of TS steps each, for 64 V channels
+// (V a lane).  A wave loads its steps at once, forms decays and inputs and folds them to h_out = A h_in + S; the
+// waves' folds meet in LDS, and the piece's fold is published.  The state that enters the piece comes from the
+// pieces before it: these are grouped in blocks of 8 or 32, a block's last piece publishes the state behind the
+// block, and the others fold the (A, S) of the pieces before them in the block onto the state in front of it.  So
+// a sequence's chain is one hop a block long, its sums have a fixed order (the block's length does not show in
+// them), and every input is read once.
 //
-// Published words carry their own validity: a word is all ones until it is
-// written, and no (A, S) or state is stored as that pattern.  Relaxed 64 and 32
-// bit atomics at agent scope are therefore enough.  The pieces of a chain are handed out by a
-// counter of its own, earlier ones first: who waits for a piece waits for a workgroup that is
-// running, whatever else the device runs.  A wait gives up after kPolls reads (the
-// outputs are NaN then): a workspace that two calls share by mistake cannot hang.
+// Published words carry their own validity: a word is all ones until it is written, and no (A, S) or state is
+// stored as that pattern.  Relaxed 64- and 32-bit atomics at agent scope are therefore enough.  The pieces of a
+// chain are handed out by a counter of its own, earlier ones first: who waits for a piece waits for a workgroup
+// that is running, whatever else the device runs.  A workspace that two calls share by mistake gives wrong
+// results, but no access out of range (a piece beyond the last is left) and no endless wait (kPolls).
 //
-// The gradient runs the same way from the last piece to the first, on
-// P_t = a_t (e_t + P_{t+1}), e = dy silu(z): what reaches the state before step
-// t.  The states inside a piece are formed again from the state at its
-// start, saved by the forward call or by a forward pass without outputs.
+// The gradient runs the same way from the last piece to the first, on P_t = a_t (e_t + P_{t+1}), e = dy silu(z):
+// what reaches the state before step t.  The states inside a piece are formed again from the state at its start,
+// saved by the forward call or by a forward pass without outputs.  While a piece waits, it forms what its
+// gradients are in multiples of g, the gradient of a step's state, so that five products a step are left then.
+//
+// Bound by HBM, and nearly as much by the vector units (about 36 instructions an element forward, six of them
+// transcendental, busy 60% of the time).  Measured in bf16 (a copy reaches 5.1 to 5.3 TB/s): 4 x 8192 x 5120 with
+// output gate 345 us, 4.9 TB/s; 1 x 32768 x 2560 151 us, 4.4 TB/s; 8 x 2048 x 4096 forward and gradient 328 to 352
+// us, 4.2 to 4.5 TB/s.
+// Shapes, before the last steps: 16 steps a wave and 8 waves forward, 1 x 32768 x 2560: 166 us; 8 steps 16 waves 195,
+// 16 steps 4 waves 203, 8 steps 8 waves 202, 16 steps 16 waves 177; four channels a lane 222 against 153.  Gradient
+// of 8 steps and 8 waves, 8 x 2048 x 4096 with the forward call: 369 us; 4 steps and 16 waves 475.
 #include "col_sum.h"
 #include "gated_launch.h"
 #include "gated_math.h"
@@ -56,12 +61,9 @@ struct GatedArgs {
   int32_t first;  // of all pieces of work, this launch's
 };
 
-constexpr int kMaxBlock = 32;  // pieces
-constexpr int kPolls = 1 << 20;
-#ifndef WPS
-#define WPS 4
-#endif
-constexpr int kWavesPerSimd = WPS;
+constexpr int kMaxBlock = 32;      // pieces
+constexpr int kPolls = 1 << 18;    // reads of a word before its wait is given up, 0.1 s at least
+constexpr int kWavesPerSimd = 4;   // two workgroups a CU: one loads while the other computes or waits
 
 __device__ __forceinline__ int steps_of(const GatedArgs& a, int64_t b) {
   if (a.lengths == nullptr) return (int)a.seqlen;
@@ -185,7 +187,8 @@ __device__ __forceinline__ void collect(const Link& l, int wave, int lane, const
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const uint64_t f = wait_word(p + v, w[v]);
-      pre[k][lane * V + v] = Fold{__builtin_bit_cast(float, (uint32_t)f), __builtin_bit_cast(float, (uint32_t)(f >> 32))};
+      pre[k][lane * V + v] =
+          Fold{__builtin_bit_cast(float, (uint32_t)f), __builtin_bit_cast(float, (uint32_t)(f >> 32))};
     }
   }
   if (wave == W - 1 && !l.heads)
@@ -235,6 +238,7 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
   __shared__ int shared;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const Spot<V> at(a, &shared);
+  if ((uint32_t)at.q >= (uint32_t)a.pieces) return;  // a counter that another call moves too
   const int n = steps_of(a, at.b), seqlen = (int)a.seqlen;
   const int c0 = at.q * (W * TS), t0 = c0 + wave * TS;
   const int m = min(max(n - t0, 0), TS);
@@ -359,6 +363,7 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const Gated
   __shared__ int shared;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const Spot<V> at(a, &shared);  // q counts from the sequence's end
+  if ((uint32_t)at.q >= (uint32_t)a.pieces) return;
   const int n = steps_of(a, at.b), seqlen = (int)a.seqlen;
   const int c = a.pieces - 1 - at.q, c0 = c * (W * TS), t0 = c0 + wave * TS;
   const int m = min(max(n - t0, 0), TS);
@@ -455,7 +460,8 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const Gated
   // The states before each step, and what a step's gradients are in multiples of that of its state:
   //   dx = g kx, dgx = g ki, d(log a) sa = g gs, dga = g gs ka.
   float gs[TS][V], ka[TS][V], ki[TS][V], e[TS][V];
-  const float* const ck = a.ckpt + (at.b * ((a.seqlen + kGatedCkpt - 1) / kGatedCkpt) + c0 / kGatedCkpt) * a.width + at.d;
+  const int64_t saved = (a.seqlen + kGatedCkpt - 1) / kGatedCkpt;
+  const float* const ck = a.ckpt + (at.b * saved + c0 / kGatedCkpt) * a.width + at.d;
   float h[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -551,14 +557,8 @@ __global__ void __launch_bounds__(256) k_gated_clear(uint4* p, int64_t n) {
   if (i < n) p[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
 }
 
-#ifndef FS
-#define FS 16
-#define FW 8
-#define BS 8
-#define BW 8
-#endif
-constexpr int kFwdSteps = FS, kFwdWaves = FW;  // 128 steps a piece
-constexpr int kBwdSteps = BS, kBwdWaves = BW;   // 64: every piece starts at a saved state
+constexpr int kFwdSteps = 16, kFwdWaves = 8;  // 128 steps a piece
+constexpr int kBwdSteps = 8, kBwdWaves = 8;   // 64: every piece starts at a saved state
 static_assert(kBwdSteps * kBwdWaves % kGatedCkpt == 0 && kGatedCkpt % kFwdSteps == 0, "pieces start at saved states");
 constexpr int64_t kMaxGrid = 1 << 22;  // workgroups of a launch
 
@@ -618,9 +618,11 @@ GatedArgs args(const GatedScanLaunch& p, int64_t pieces, uint32_t* chain) {
   const int64_t lanes = pairs(p) ? 128 : 64;
   a.tiles = (int32_t)((p.width + lanes - 1) / lanes);
   a.block = (int32_t)block_of(p.batch * a.tiles);
-  a.tickets = chain;
-  a.folds = reinterpret_cast<uint64_t*>(chain + ticket_words(p.batch, p.width));
-  a.states = chain + ticket_words(p.batch, p.width) + 2 * p.batch * p.width * pieces;
+  if (pieces > 1) {
+    a.tickets = chain;
+    a.folds = reinterpret_cast<uint64_t*>(chain + ticket_words(p.batch, p.width));
+    a.states = chain + ticket_words(p.batch, p.width) + 2 * p.batch * p.width * pieces;
+  }
   return a;
 }
 
@@ -636,7 +638,8 @@ hipError_t go(K kern, GatedArgs a, int threads, hipStream_t stream) {
   const int64_t items = a.batch * a.tiles * a.pieces;
   for (int64_t i = 0; i < items; i += kMaxGrid) {
     a.first = (int32_t)i;
-    const hipError_t rc = launch(kern, dim3((unsigned)(items - i < kMaxGrid ? items - i : kMaxGrid)), dim3(threads), 0, stream, a);
+    const int64_t n = items - i < kMaxGrid ? items - i : kMaxGrid;
+    const hipError_t rc = launch(kern, dim3((unsigned)n), dim3(threads), 0, stream, a);
     if (rc != hipSuccess) return rc;
   }
   return hipSuccess;
@@ -657,8 +660,8 @@ hipError_t fwd(const GatedScanLaunch& p, const GatedArgs& a) {
 }
 template <typename T, int V>
 hipError_t go_bwd(const GatedArgs& a, hipStream_t stream) {
-  return go(a.z != nullptr ? k_gated_bwd<T, V, kBwdSteps, kBwdWaves, true> : k_gated_bwd<T, V, kBwdSteps, kBwdWaves, false>, a,
-            64 * kBwdWaves, stream);
+  return a.z != nullptr ? go(k_gated_bwd<T, V, kBwdSteps, kBwdWaves, true>, a, 64 * kBwdWaves, stream)
+                        : go(k_gated_bwd<T, V, kBwdSteps, kBwdWaves, false>, a, 64 * kBwdWaves, stream);
 }
 
 constexpr int64_t kFwdLen = kFwdSteps * kFwdWaves, kBwdLen = kBwdSteps * kBwdWaves;
@@ -709,7 +712,9 @@ hipError_t launch_gated_scan_bwd(const GatedScanLaunch& p) {
       f.ckpt = a.ckpt;
       if (p.seqlen > 0 && (rc = fwd<false>(p, f)) != hipSuccess) return rc;
     }
-    rc = !p.bf16 ? go_bwd<float, 1>(a, p.stream) : pairs(p) ? go_bwd<uint16_t, 2>(a, p.stream) : go_bwd<uint16_t, 1>(a, p.stream);
+    rc = !p.bf16    ? go_bwd<float, 1>(a, p.stream)
+         : pairs(p) ? go_bwd<uint16_t, 2>(a, p.stream)
+                    : go_bwd<uint16_t, 1>(a, p.stream);
     if (rc != hipSuccess) return rc;
   }
   if (p.dlog_a == nullptr) return hipSuccess;

@@ -126,7 +126,8 @@ struct Place {
   int64_t team, row, dr, col;  // col: the group's first value in its row
   int phase = 0;
   float (*red)[kMaxWaves][kMaxSums];
-  __device__ __forceinline__ Place(int dim_, int64_t groups, float (*red_)[kMaxWaves][kMaxSums]) : dim(dim_), red(red_) {
+  __device__ __forceinline__ Place(int dim_, int64_t groups, float (*red_)[kMaxWaves][kMaxSums])
+      : dim(dim_), red(red_) {
     lanes = TEAM > 0 ? TEAM : (int)blockDim.x;
     ln = TEAM > 0 ? (int)threadIdx.x % (TEAM > 0 ? TEAM : 1) : (int)threadIdx.x;
     const int per = TEAM > 0 ? (int)blockDim.x / (TEAM > 0 ? TEAM : 1) : 1;
@@ -524,7 +525,10 @@ struct Shape {
 // Gradients: eight waves, in whole workgroups: more only add sums of weights to write and to join, and
 // rows in between (16384 x 2560 with residual: 147 us, with 20 waves 171, with 5 163; 32768 x 768: 88, 96, 122;
 // 16384 x 8 x 512: 127, 135, 194; 8192 x 2501: 94, 129, 141).
-int64_t groups_per_cu(int w, int nv, bool grad) { return grad ? (w < 8 ? (7 + w) / w : 1) : 8 * (nv == 1 ? 32 / w : 1); }
+int64_t groups_per_cu(int w, int nv, bool grad) {
+  if (grad) return w < 8 ? (7 + w) / w : 1;
+  return 8 * (nv == 1 ? 32 / w : 1);
+}
 
 // rows x groups teams of work.
 Shape shape_of(int64_t rows, int64_t dim, int64_t groups, bool grad) {

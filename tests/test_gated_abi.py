@@ -13,7 +13,8 @@ BAD = ctypes.c_size_t(-1).value
 
 def _fwd(lib, x=P0, ga=P0 + MB, gx=P0 + 2 * MB, la=P0 + 3 * MB, z=None, lens=None, h0=None, y=P0 + 4 * MB, hl=None,
          ck=None, b=2, L=40, D=96, xs=0, as_=0, is_=0, zs=0, dtype=1, ws=P0 + 90 * MB, wsb=MB):
-    return lib.ssm_gated_scan_fwd(x, ga, gx, la, z, lens, h0, y, hl, ck, b, L, D, xs, as_, is_, zs, dtype, ws, wsb, None)
+    return lib.ssm_gated_scan_fwd(x, ga, gx, la, z, lens, h0, y, hl, ck, b, L, D, xs, as_, is_, zs, dtype, ws, wsb,
+                                  None)
 
 
 def test_scan_errors(lib):
@@ -57,6 +58,23 @@ def test_scan_workspace(lib):
     assert lib.ssm_gated_scan_bwd_workspace_size(1, 4, 4, 1, 2) == BAD
     assert lib.ssm_gated_scan_bwd_workspace_size(2, 4096, 96, 1, 1) <= lib.ssm_gated_scan_bwd_workspace_size(
         2, 4096, 96, 1, 0)
+
+
+def test_scan_pieces_stay_countable(lib):
+    """Pieces of 64 steps and 64 channels are counted in 31 bits; workspaces of large calls stay exact in 64."""
+    for args, ok in (((1, 1, 1 << 23), True), ((16384, 64, 1 << 23), False), ((1, (1 << 31) - 257, 64), True),
+                     ((65, (1 << 31) - 257, 64), False), ((64, (1 << 31) - 257, 64), True),
+                     (((1 << 31), 1, 1), False), (((1 << 31) - 1, 1, 1), True), (((1 << 24), 64 * 128, 1), False)):
+        for f in (lambda *a: lib.ssm_gated_scan_fwd_workspace_size(*a, 1),
+                  lambda *a: lib.ssm_gated_scan_bwd_workspace_size(*a, 0, 0), lib.ssm_gated_scan_ckpt_bytes):
+            assert (f(*args) != BAD) == ok, args
+    b, L, D = 63, (1 << 31) - 257, 64
+    pieces = -(-L // 128)
+    assert lib.ssm_gated_scan_fwd_workspace_size(b, L, D, 1) >= b * D * pieces * 8
+    assert lib.ssm_gated_scan_ckpt_bytes(b, L, D) == b * D * -(-L // 64) * 4
+    assert lib.ssm_gated_scan_fwd_workspace_size(8, 128, 64, 1) == 0
+    # A call of one piece needs no workspace; one of two does.
+    assert lib.ssm_gated_scan_fwd_workspace_size(8, 129, 64, 1) > 0
 
 
 def test_scan_empty(lib):
@@ -105,7 +123,8 @@ def test_update_errors(lib):
     for name in ("h", "x", "ga", "gx", "la", "y"):
         assert _upd(lib, **{name: None}) == bd.SSM_ERR_NULL_ARG, name
     for bad in (dict(b=-1), dict(n=-1), dict(D=-1), dict(n=5), dict(xs=95), dict(z=P0 + 7 * MB, zs=95),
-                dict(xs=(1 << 40) + 1), dict(D=(1 << 23) + 1), dict(b=1 << 24, n=1 << 24, D=1), dict(b=1 << 20, n=1 << 20, D=8192)):
+                dict(xs=(1 << 40) + 1), dict(D=(1 << 23) + 1), dict(b=1 << 24, n=1 << 24, D=1),
+                dict(b=1 << 20, n=1 << 20, D=8192)):
         assert _upd(lib, **bad) == bd.SSM_ERR_BAD_DIM, bad
     assert _upd(lib, dtype=3) == bd.SSM_ERR_UNSUPPORTED
     for name in ("x", "ga", "gx", "z", "y"):

@@ -146,8 +146,9 @@ def test_long_sequences(lib, B, L, D, dtype):
     got = _check(d, dy, dh, dtype, ckpt=B != 3)
     ref = P.scan(**{k: _np(v) for k, v in d.items()}, dy=_np(dy), dh_last=_np(dh))
     # A step's decay is off by 2 U of the hardware's exponential (which leans to one side), log_a's roundings times
-    # |log a|, and 3 roundings, 5.5 U together for slow channels; errors that lean add up over what a state remembers, T =
-    # 1 / (1 - a) steps with the gate half open: 5.5 U T for a state or a state's gradient, twice that for their product.
+    # |log a|, and 3 roundings, 5.5 U together for slow channels; errors that lean add up over what a state remembers,
+    # T = 1 / (1 - a) steps with the gate half open: 5.5 U T for a state or a state's gradient, twice that for their
+    # product.
     T = 1.0 / (1.0 - np.exp(0.5 * float(d["log_a"].max())))
     for n, lim in (("h_last", 5.5), ("dh0", 5.5), ("dlog_a", 11.0), ("y", 5.5), ("dx", 5.5), ("dgx", 5.5),
                    ("dga", 11.0), ("dz", 5.5)):
@@ -358,8 +359,8 @@ def test_two_at_once(lib):
 
 
 def test_training_step_against_differences(lib):
-    """Norm, gated recurrence, gated norm and residual norm together, as a layer runs them: gradients against differences
-    of the loss (fp32)."""
+    """Norm, gated recurrence, gated norm and residual norm together, as a layer runs them: gradients against
+    differences of the loss (fp32)."""
     import torch
     from selective_state_space_84_amd import binding as bd
     r = np.random.default_rng(17)

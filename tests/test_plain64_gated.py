@@ -99,6 +99,7 @@ def test_residual_norm_gradient_against_differences(post):
 def test_norm_by_hand():
     x = np.array([[3.0, 4.0, 0.0, 0.0]])
     assert np.allclose(P.gated_norm(x, None, None, 1, True, 0.0)["y"][0], [[1.2, 1.6, 0, 0]])
-    assert np.allclose(P.gated_norm(x, None, None, 2, True, 1.0)["y"][0], [[3 / np.sqrt(13.5), 4 / np.sqrt(13.5), 0, 0]])
+    want = [[3 / np.sqrt(13.5), 4 / np.sqrt(13.5), 0, 0]]
+    assert np.allclose(P.gated_norm(x, None, None, 2, True, 1.0)["y"][0], want)
     o = P.residual_norm(x, np.array([[1.0, 1.0, 1.0, 1.0]]), None, np.array([1.0, 2.0, 1.0, 1.0]), 0.5, True, 0.0)
     assert np.allclose(o["res_out"][0], [[1.6, 2.6, 1.0, 1.0]])
