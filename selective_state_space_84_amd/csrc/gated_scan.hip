@@ -19,7 +19,7 @@
 // saved by the forward call or by a forward pass without outputs.  While a piece waits, it forms what its
 // gradients are in multiples of g, the gradient of a step's state, so that five products a step are left then.
 //
-// Bound by HBM, and nearly as much by the vector units (about 36 instructions an element forward, six of them
+// Bound by HBM, and nearly as much by the vector units (33 instructions an element forward, six of them
 // transcendental, busy 60% of the time).  Measured in bf16 (a copy reaches 5.1 to 5.3 TB/s): 4 x 8192 x 5120 with
 // output gate 345 us, 4.9 TB/s; 1 x 32768 x 2560 151 us, 4.4 TB/s; 8 x 2048 x 4096 forward and gradient 328 to 352
 // us, 4.2 to 4.5 TB/s.
