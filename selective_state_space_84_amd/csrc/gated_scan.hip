@@ -231,6 +231,15 @@ __device__ __forceinline__ void load_steps(Io<T, V> (&r)[TS], const void* base, 
   for (int i = 0; i < TS; ++i) r[i].load(b, lane, (uint32_t)min(i, m - 1) * (uint32_t)stride);
 }
 
+// Values that are formed here and now: the compiler would put many of them off to where they are used, and hold what
+// they come from instead.
+__device__ __forceinline__ void settle(float& a) { asm volatile("" : "+v"(a)); }
+template <typename... F>
+__device__ __forceinline__ void settle(float& a, F&... more) {
+  settle(a);
+  settle(more...);
+}
+
 template <typename T, int V, int TS, int W, bool Z, bool OUT>
 __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const GatedArgs a) {
   __shared__ Fold folds[W][64 * V], pre[kMaxBlock - 1][64 * V];
@@ -265,13 +274,16 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
 #pragma unroll
     for (int v = 0; v < V; ++v) c2[v] = a.log_a[at.d + v] * kLog2e;
 #pragma unroll
-    for (int i = 0; i < TS; ++i)
+    for (int i = 0; i < TS; ++i) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const GatedStep s = gated_step(ga[i].get(v), gx[i].get(v), c2[v]);
         dec[i][v] = s.a;
         u[i][v] = s.m() * s.sx * x[i].get(v);
       }
+#pragma unroll
+      for (int v = 0; v < V; ++v) settle(dec[i][v], u[i][v]);
+    }
     if (Z && OUT) load_steps(z, a.z, row, a.zs, off, m);
   }
   if (m < TS)
@@ -345,15 +357,6 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
   if (a.h_last != nullptr && wave == W - 1 && l.ends)
 #pragma unroll
     for (int v = 0; v < V; ++v) a.h_last[st + v] = h[v];
-}
-
-// Values that are formed here and now: the compiler would put many of them off to where they are used, and hold what
-// they come from instead.
-__device__ __forceinline__ void settle(float& a) { asm volatile("" : "+v"(a)); }
-template <typename... F>
-__device__ __forceinline__ void settle(float& a, F&... more) {
-  settle(a);
-  settle(more...);
 }
 
 template <typename T, int V, int TS, int W, bool Z>
