@@ -274,6 +274,69 @@ def test_scan_large_offsets(lib):
     assert torch.equal(g["dh0"][:, D - 64:], g1["dh0"])
 
 
+def test_more_pieces_than_a_launch(lib):
+    """1.5 million rows of three pieces (gradient: five) take several launches: sampled rows against the same alone."""
+    import torch
+    from selective_state_space_84_amd import binding as bd
+    B, L = 1500000, 300
+    x = torch.empty(B, L, 1, dtype=torch.bfloat16, device=DEV).normal_()
+    log_a = torch.tensor([-0.05], device=DEV)
+    lens = torch.randint(0, L + 1, (B,), dtype=torch.int32, device=DEV)
+    y, hl, ck = bd.ssm_gated_scan_fwd(x, x, x, log_a, lengths=lens, want_ckpt=True)
+    g = bd.ssm_gated_scan_bwd(x, x, x, log_a, dy=x, lengths=lens, ckpt=ck, want_dlog_a=False)
+    for r in (0, 699050, 1048575, 1398102, B - 3):  # around the launches' borders
+        cut, n = x[r:r + 3].clone(), lens[r:r + 3].clone()
+        y1, h1, _ = bd.ssm_gated_scan_fwd(cut, cut, cut, log_a, lengths=n)
+        g1 = bd.ssm_gated_scan_bwd(cut, cut, cut, log_a, dy=cut, lengths=n, want_dlog_a=False)
+        assert torch.equal(y[r:r + 3], y1) and torch.equal(hl[r:r + 3], h1), r
+        for k in g1:
+            assert torch.equal(g[k][r:r + 3], g1[k]), (r, k)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_widest_rows_and_strides(lib, dtype):
+    """The largest width, and the largest distance between steps."""
+    import torch
+    from selective_state_space_84_amd import binding as bd
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    D = 1 << 23
+    x = torch.empty(1, 3, D, dtype=dt, device=DEV).normal_()
+    log_a = -torch.rand(D, device=DEV)
+    y, hl, _ = bd.ssm_gated_scan_fwd(x, x, x, log_a)
+    g = bd.ssm_gated_scan_bwd(x, x, x, log_a, dy=y)
+    cut, la = x[:, :, D - 130:].contiguous(), log_a[D - 130:].contiguous()
+    y1, h1, _ = bd.ssm_gated_scan_fwd(cut, cut, cut, la)
+    g1 = bd.ssm_gated_scan_bwd(cut, cut, cut, la, dy=y1)
+    assert torch.equal(y[:, :, D - 130:], y1) and torch.equal(hl[:, D - 130:], h1)
+    for k in g1:
+        assert torch.equal(g[k][..., D - 130:], g1[k]), k
+    del x, y, g
+    far = torch.empty(1, 18, 1 << 25, dtype=dt, device=DEV)
+    far[:, :, 64:194].normal_()
+    v = far[:, :, 64:194]
+    y, hl, _ = bd.ssm_gated_scan_fwd(v, v, v, la)
+    c = v.contiguous()
+    y1, h1, _ = bd.ssm_gated_scan_fwd(c, c, c, la)
+    assert torch.equal(y, y1) and torch.equal(hl, h1)
+    a, b = bd.ssm_gated_scan_bwd(v, v, v, la, dy=y), bd.ssm_gated_scan_bwd(c, c, c, la, dy=y)
+    assert all(torch.equal(a[k], b[k]) for k in a)
+
+
+def test_zeros_behind_a_row_whatever_comes_from_there(lib):
+    """A gradient of the last state that is not finite reaches the row's steps and nothing behind them."""
+    import torch
+    from selective_state_space_84_amd import binding as bd
+    d, dy, dh = _make(18, 3, 200, 70, "bf16")
+    dh[:] = float("inf")
+    dh[1] = float("nan")
+    lens = [150, 64, 0]
+    g = bd.ssm_gated_scan_bwd(**d, dy=dy, dh_last=dh, lengths=_lens(lens))
+    for b, n in enumerate(lens):
+        for k in ("dx", "dga", "dgx", "dz"):
+            assert not g[k][b, n:].any(), (b, k)
+    assert torch.isnan(g["dx"][1, :64]).all() and torch.equal(g["dh0"][2], dh[2])
+
+
 def test_prompt_then_tokens(lib):
     """A prompt continued token by token equals one longer prompt, through the norms around it."""
     import torch
