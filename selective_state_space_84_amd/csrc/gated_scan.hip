@@ -199,6 +199,19 @@ __device__ __forceinline__ void collect(const Link& l, int wave, int lane, const
     }
 }
 
+// Workgroup i of a round over all chains takes this one.  Workgroups go to the 8 XCDs in turn, so that neighbours in i
+// share no L2, while neighbouring tiles share the cache lines at their border where rows are not whole lines, and pages
+// of memory always.  Eight neighbouring tiles therefore go to one XCD (forward and gradient of 8 x 2048 x 2049: 204 us,
+// else 248; 4 x 8192 x 5120 with output gate 333, else 346); not more, so that every XCD has a share of every row, which
+// may end early (padded batch 8 x 2048 x 4096: 101 us, with 16 tiles 116, with an eighth of all 129).
+__device__ __forceinline__ int neighbours(int i, int chains) {
+  constexpr int kXcd = 8, kGroup = 8;
+  const int whole = chains / (kXcd * kGroup) * (kXcd * kGroup);
+  if (i >= whole) return whole + xcd_remap(i - whole, chains - whole);
+  const int k = i / kXcd;
+  return (k / kGroup * kXcd + i % kXcd) * kGroup + k % kGroup;
+}
+
 // Where a lane works: channels d .. d + V - 1 of row b, piece q of that chain.  Lanes behind the row's width do
 // the last channels' work once more, and write the same values to the same places.
 template <int V>
@@ -208,7 +221,8 @@ struct Spot {
   // Work goes to the chains in turn.  Within one, the piece is the next that no workgroup has
   // started.  shared: read and written by the whole workgroup.
   __device__ __forceinline__ Spot(const GatedArgs& a, int* shared) {
-    const int chain = ((int)blockIdx.x + a.first) % (a.tiles * (int)a.batch);
+    const int chains = a.tiles * (int)a.batch;
+    const int chain = neighbours(((int)blockIdx.x + a.first) % chains, chains);
     b = chain / a.tiles;
     d = min(((int64_t)(chain % a.tiles) * 64 + (threadIdx.x & 63)) * V, a.width - V);
     q = 0;
