@@ -21,8 +21,8 @@
 //
 // Bound by HBM, and nearly as much by the vector units (33 instructions an element forward, six of them
 // transcendental, busy 60% of the time).  Measured in bf16 (a copy reaches 5.1 to 5.3 TB/s): 4 x 8192 x 5120 with
-// output gate 345 us, 4.9 TB/s; 1 x 32768 x 2560 151 us, 4.4 TB/s; 8 x 2048 x 4096 forward and gradient 328 to 352
-// us, 4.2 to 4.5 TB/s.
+// output gate 312 us, 5.4 TB/s; 1 x 32768 x 2560 146 us, 4.6 TB/s; 8 x 2048 x 4096 forward and gradient 324 us, 4.6
+// TB/s.
 // Shapes, before the last steps: 16 steps a wave and 8 waves forward, 1 x 32768 x 2560: 166 us; 8 steps 16 waves 195,
 // 16 steps 4 waves 203, 8 steps 8 waves 202, 16 steps 16 waves 177; four channels a lane 222 against 153.  Gradient
 // of 8 steps and 8 waves, 8 x 2048 x 4096 with the forward call: 369 us; 4 steps and 16 waves 475.
@@ -82,14 +82,18 @@ __device__ __forceinline__ rsrc_t rows_of(const void* p, int64_t bytes_before, u
 }
 constexpr uint32_t kNowhere = 0x80000000u;  // a lane's offset behind every resource
 
+// How the caches take an access: in the usual way, or as data that passes through once.
+constexpr int kUsual = 0, kOnce = 2;
+
 // V values of one lane as loaded.
 template <typename T, int V>
 struct Io;
 template <>
 struct Io<float, 1> {
   uint32_t r;
+  template <int HINT>
   __device__ __forceinline__ void load(rsrc_t b, uint32_t lane, uint32_t row) {
-    r = __builtin_amdgcn_raw_buffer_load_b32(b, lane, row, 0);
+    r = __builtin_amdgcn_raw_buffer_load_b32(b, lane, row, HINT);
   }
   __device__ __forceinline__ float get(int) const { return __builtin_bit_cast(float, r); }
   __device__ __forceinline__ void forget() {}
@@ -97,8 +101,9 @@ struct Io<float, 1> {
 template <>
 struct Io<uint16_t, 1> {
   uint16_t r;
+  template <int HINT>
   __device__ __forceinline__ void load(rsrc_t b, uint32_t lane, uint32_t row) {
-    r = __builtin_amdgcn_raw_buffer_load_b16(b, lane, row, 0);
+    r = __builtin_amdgcn_raw_buffer_load_b16(b, lane, row, HINT);
   }
   __device__ __forceinline__ float get(int) const { return io_to_f32(r); }
   __device__ __forceinline__ void forget() {}
@@ -106,8 +111,9 @@ struct Io<uint16_t, 1> {
 template <>
 struct Io<uint16_t, 2> {
   uint32_t r;
+  template <int HINT>
   __device__ __forceinline__ void load(rsrc_t b, uint32_t lane, uint32_t row) {
-    r = __builtin_amdgcn_raw_buffer_load_b32(b, lane, row, 0);
+    r = __builtin_amdgcn_raw_buffer_load_b32(b, lane, row, HINT);
   }
   __device__ __forceinline__ float get(int v) const {
     return __builtin_bit_cast(float, v ? r & 0xffff0000u : r << 16);
@@ -116,17 +122,20 @@ struct Io<uint16_t, 2> {
   // unpacked again where it is next used, instead of held in two more.
   __device__ __forceinline__ void forget() { asm volatile("" : "+v"(r)); }
 };
+template <int HINT>
 __device__ __forceinline__ void put(rsrc_t b, uint32_t lane, uint32_t row, const float (&v)[1], const float*) {
-  __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v[0]), b, lane, row, 0);
+  __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v[0]), b, lane, row, HINT);
 }
+template <int HINT>
 __device__ __forceinline__ void put(rsrc_t b, uint32_t lane, uint32_t row, const float (&v)[1], const uint16_t*) {
-  __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v[0]), b, lane, row, 0);
+  __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v[0]), b, lane, row, HINT);
 }
+template <int HINT>
 __device__ __forceinline__ void put(rsrc_t b, uint32_t lane, uint32_t row, const float (&v)[2], const uint16_t*) {
   typedef float f2 __attribute__((ext_vector_type(2)));
   typedef __bf16 b2 __attribute__((ext_vector_type(2)));
   __builtin_amdgcn_raw_buffer_store_b32(
-      __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[0], v[1]}, b2)), b, lane, row, 0);
+      __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[0], v[1]}, b2)), b, lane, row, HINT);
 }
 
 // Fold of a piece, or of what lies behind it: h_out = a h + s.
@@ -201,9 +210,10 @@ __device__ __forceinline__ void collect(const Link& l, int wave, int lane, const
 
 // Workgroup i of a round over all chains takes this one.  Workgroups go to the 8 XCDs in turn, so that neighbours in i
 // share no L2, while neighbouring tiles share the cache lines at their border where rows are not whole lines, and pages
-// of memory always.  Eight neighbouring tiles therefore go to one XCD (forward and gradient of 8 x 2048 x 2049: 204 us,
-// else 248; 4 x 8192 x 5120 with output gate 333, else 346); not more, so that every XCD has a share of every row, which
-// may end early (padded batch 8 x 2048 x 4096: 101 us, with 16 tiles 116, with an eighth of all 129).
+// of memory always.  Eight neighbouring tiles therefore go to one XCD (forward and gradient of 8 x 2048 x 2049: 204
+// us, else 248; 4 x 8192 x 5120 with output gate, before such rows passed the caches by: 333, else 346); not more, so
+// that every XCD has a share of every row, which may end early (padded batch 8 x 2048 x 4096: 101 us, with 16 tiles
+// 116, with an eighth of all 129).
 __device__ __forceinline__ int neighbours(int i, int chains) {
   constexpr int kXcd = 8, kGroup = 8;
   const int whole = chains / (kXcd * kGroup) * (kXcd * kGroup);
@@ -237,12 +247,12 @@ struct Spot {
 
 // Steps row .. row + m - 1 (1 <= m <= TS) of one input; what lies behind them repeats the last.  (TS
 // steps lie within 2^31 bytes.)
-template <typename T, int V, int TS>
+template <int HINT, typename T, int V, int TS>
 __device__ __forceinline__ void load_steps(Io<T, V> (&r)[TS], const void* base, int64_t row, int64_t stride,
                                            uint32_t lane, int m) {
   const rsrc_t b = rows_of(base, row * stride, (uint32_t)TS * (uint32_t)stride);
 #pragma unroll
-  for (int i = 0; i < TS; ++i) r[i].load(b, lane, (uint32_t)min(i, m - 1) * (uint32_t)stride);
+  for (int i = 0; i < TS; ++i) r[i].template load<HINT>(b, lane, (uint32_t)min(i, m - 1) * (uint32_t)stride);
 }
 
 // Values that are formed here and now: the compiler would put many of them off to where they are used, and hold what
@@ -254,7 +264,7 @@ __device__ __forceinline__ void settle(float& a, F&... more) {
   settle(more...);
 }
 
-template <typename T, int V, int TS, int W, bool Z, bool OUT>
+template <typename T, int V, int TS, int W, bool Z, bool OUT, int GET, int PUT>
 __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const GatedArgs a) {
   __shared__ Fold folds[W][64 * V], pre[kMaxBlock - 1][64 * V];
   __shared__ float front[64 * V];
@@ -272,7 +282,7 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
   if (c0 >= n && at.q > 0) {  // behind the row's end
     const float o[V] = {};
     for (int i = 0; OUT && i < TS && t0 + i < seqlen; ++i)
-      put(py, off, i * ws, o, tag);
+      put<PUT>(py, off, i * ws, o, tag);
     return;
   }
   float dec[TS][V], u[TS][V], start[V];
@@ -281,9 +291,9 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
   Io<T, V> z[TS];
   if (m > 0) {
     Io<T, V> x[TS], ga[TS], gx[TS];
-    load_steps(ga, a.ga, row, a.as, off, m);
-    load_steps(gx, a.gx, row, a.is, off, m);
-    load_steps(x, a.x, row, a.xs, off, m);
+    load_steps<GET>(ga, a.ga, row, a.as, off, m);
+    load_steps<GET>(gx, a.gx, row, a.is, off, m);
+    load_steps<GET>(x, a.x, row, a.xs, off, m);
     float c2[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) c2[v] = a.log_a[at.d + v] * kLog2e;
@@ -298,7 +308,7 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
 #pragma unroll
       for (int v = 0; v < V; ++v) settle(dec[i][v], u[i][v]);
     }
-    if (Z && OUT) load_steps(z, a.z, row, a.zs, off, m);
+    if (Z && OUT) load_steps<GET>(z, a.z, row, a.zs, off, m);
   }
   if (m < TS)
 #pragma unroll
@@ -360,7 +370,7 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
         o[v] = Z && OUT ? h[v] * silu(z[i].get(v)) : h[v];
         if (!ALL && i >= m) o[v] = 0.0f;
       }
-      if (OUT && (ALL || t0 + i < seqlen)) put(py, off, i * ws, o, tag);
+      if (OUT && (ALL || t0 + i < seqlen)) put<PUT>(py, off, i * ws, o, tag);
     }
   };
   if (m == TS)
@@ -373,7 +383,7 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
     for (int v = 0; v < V; ++v) a.h_last[st + v] = h[v];
 }
 
-template <typename T, int V, int TS, int W, bool Z>
+template <typename T, int V, int TS, int W, bool Z, int HINT>
 __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const GatedArgs a) {
   __shared__ Fold fwd[W][64 * V], rev[W][64 * V], pre[kMaxBlock - 1][64 * V];
   __shared__ float front[64 * V];
@@ -396,10 +406,10 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const Gated
   if (c0 >= n) {  // behind the row's end
     const float o[V] = {};
     for (int i = 0; i < TS && t0 + i < seqlen; ++i) {
-        put(px, off, i * ws, o, tag);
-        put(pa, off, i * ws, o, tag);
-        put(pi, off, i * ws, o, tag);
-        if (Z) put(pz, off, i * ws, o, tag);
+        put<HINT>(px, off, i * ws, o, tag);
+        put<HINT>(pa, off, i * ws, o, tag);
+        put<HINT>(pi, off, i * ws, o, tag);
+        if (Z) put<HINT>(pz, off, i * ws, o, tag);
       }
     if (wave == 0)
 #pragma unroll
@@ -413,11 +423,11 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const Gated
   float dec[TS][V], sa[TS][V], kx[TS][V], inv[TS][V], la[V];  // kx = m sx, inv = 1 / m
   if (m > 0) {
     Io<T, V> ga[TS], gx[TS];
-    load_steps(ga, a.ga, row, a.as, off, m);
-    load_steps(gx, a.gx, row, a.is, off, m);
-    load_steps(x, a.x, row, a.xs, off, m);
-    load_steps(dy, a.dy, row, step, off, m);
-    if (Z) load_steps(z, a.z, row, a.zs, off, m);
+    load_steps<HINT>(ga, a.ga, row, a.as, off, m);
+    load_steps<HINT>(gx, a.gx, row, a.is, off, m);
+    load_steps<HINT>(x, a.x, row, a.xs, off, m);
+    load_steps<HINT>(dy, a.dy, row, step, off, m);
+    if (Z) load_steps<HINT>(z, a.z, row, a.zs, off, m);
 #pragma unroll
     for (int v = 0; v < V; ++v) la[v] = a.log_a[at.d + v];
 #pragma unroll
@@ -509,7 +519,7 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const Gated
       settle(gs[i][v], ka[i][v], ki[i][v], h[v]);
       if (Z) settle(e[i][v]);
     }
-    if (Z) put(pz, t0 + i < seqlen ? off : kNowhere, i * ws, dz, tag);
+    if (Z) put<HINT>(pz, t0 + i < seqlen ? off : kNowhere, i * ws, dz, tag);
   }
   if (a.pieces > 1) {
     collect<V, W>(l, wave, lane, fp, sp, a.width, pre, front);
@@ -540,9 +550,9 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const Gated
         p[v] = dec[i][v] * g;
       }
       if (ALL || t0 + i < seqlen) {
-        put(px, off, i * ws, dx, tag);
-        put(pa, off, i * ws, da, tag);
-        put(pi, off, i * ws, di, tag);
+        put<HINT>(px, off, i * ws, dx, tag);
+        put<HINT>(pa, off, i * ws, da, tag);
+        put<HINT>(pi, off, i * ws, di, tag);
       }
     }
   };
@@ -593,16 +603,25 @@ int64_t chain_words(int64_t batch, int64_t width, int64_t pieces) {
   return (n + 63) / 64 * 64;
 }
 
-// Two bf16 channels a lane where every row allows 4-byte accesses.
-bool pairs(const GatedScanLaunch& p) {
-  if (!p.bf16 || p.width % 2 != 0) return false;
-  const int64_t strides = p.x_stride | p.ga_stride | p.gx_stride | (p.z != nullptr ? p.z_stride : 0);
-  uintptr_t at = 0;
+// Every address that the rows begin at, and every distance between rows, as one union of bits.
+uint64_t places(const GatedScanLaunch& p) {
+  uint64_t at = (uint64_t)(p.x_stride | p.ga_stride | p.gx_stride | p.width | (p.z != nullptr ? p.z_stride : 0));
+  at *= p.bf16 ? 2 : 4;
   for (const void* q : {p.x, p.ga, p.gx, p.z, (const void*)p.y, p.dy, (const void*)p.dx, (const void*)p.dga,
                         (const void*)p.dgx, (const void*)p.dz})
     at |= reinterpret_cast<uintptr_t>(q);
-  return strides % 2 == 0 && at % 4 == 0;
+  return at;
 }
+// Two bf16 channels a lane where every row allows 4-byte accesses.
+bool pairs(const GatedScanLaunch& p) { return p.bf16 && places(p) % 4 == 0; }
+// Rows of whole cache lines, 128 bytes: no two waves touch the same one (a wave's access is 128 or 256 bytes).
+// Such calls let the caches take what they write, and what they read, as data used once: 4 x 8192 x 5120 with
+// output gate 333 -> 312 us, 1 x 32768 x 2560 152 -> 146, forward and gradient of 8 x 2048 x 4096 351 -> 324 (fp32, 2 x
+// 4096 x 2560: 187 -> 165), of 4 x 1024 x 2048 54 -> 52; 1 x 512 x 1024 the same, alone or with a norm or a product
+// that reads y next; fp32 2 x 1024 x 2048 45 -> 47.  A forward call that saves states reads in the usual way, since a
+// gradient that may read the same again follows.  With lines that two waves share it is the other way round: 8 x
+// 2048 x 2049 forward and gradient 204 -> 228 with such writes, 310 with both.
+bool lines(const GatedScanLaunch& p) { return places(p) % 128 == 0; }
 
 GatedArgs args(const GatedScanLaunch& p, int64_t pieces, uint32_t* chain) {
   const int64_t es = p.bf16 ? 2 : 4;
@@ -662,23 +681,34 @@ hipError_t go(K kern, GatedArgs a, int threads, hipStream_t stream) {
   return hipSuccess;
 }
 
-template <typename T, int V, bool Z, bool OUT>
+template <typename T, int V, bool OUT, int GET, int PUT>
 hipError_t go_fwd(const GatedArgs& a, hipStream_t stream) {
-  return go(k_gated_fwd<T, V, kFwdSteps, kFwdWaves, Z, OUT>, a, 64 * kFwdWaves, stream);
+  return OUT && a.z != nullptr
+             ? go(k_gated_fwd<T, V, kFwdSteps, kFwdWaves, OUT, OUT, GET, PUT>, a, 64 * kFwdWaves, stream)
+             : go(k_gated_fwd<T, V, kFwdSteps, kFwdWaves, false, OUT, GET, PUT>, a, 64 * kFwdWaves, stream);
+}
+template <typename T, int V, int HINT>
+hipError_t go_bwd(const GatedArgs& a, hipStream_t stream) {
+  return a.z != nullptr ? go(k_gated_bwd<T, V, kBwdSteps, kBwdWaves, true, HINT>, a, 64 * kBwdWaves, stream)
+                        : go(k_gated_bwd<T, V, kBwdSteps, kBwdWaves, false, HINT>, a, 64 * kBwdWaves, stream);
 }
 template <typename T, int V, bool OUT>
-hipError_t go_fwd_z(const GatedArgs& a, hipStream_t stream) {
-  return a.z != nullptr && OUT ? go_fwd<T, V, OUT, OUT>(a, stream) : go_fwd<T, V, false, OUT>(a, stream);
+hipError_t fwd_lines(const GatedScanLaunch& p, const GatedArgs& a) {
+  if (!OUT || !lines(p)) return go_fwd<T, V, OUT, kUsual, kUsual>(a, p.stream);
+  return a.ckpt != nullptr ? go_fwd<T, V, OUT, kUsual, OUT ? kOnce : kUsual>(a, p.stream)
+                           : go_fwd<T, V, OUT, OUT ? kOnce : kUsual, OUT ? kOnce : kUsual>(a, p.stream);
 }
 template <bool OUT>
 hipError_t fwd(const GatedScanLaunch& p, const GatedArgs& a) {
-  if (!p.bf16) return go_fwd_z<float, 1, OUT>(a, p.stream);
-  return pairs(p) ? go_fwd_z<uint16_t, 2, OUT>(a, p.stream) : go_fwd_z<uint16_t, 1, OUT>(a, p.stream);
+  return !p.bf16    ? fwd_lines<float, 1, OUT>(p, a)
+         : pairs(p) ? fwd_lines<uint16_t, 2, OUT>(p, a)
+                    : go_fwd<uint16_t, 1, OUT, kUsual, kUsual>(a, p.stream);
 }
-template <typename T, int V>
-hipError_t go_bwd(const GatedArgs& a, hipStream_t stream) {
-  return a.z != nullptr ? go(k_gated_bwd<T, V, kBwdSteps, kBwdWaves, true>, a, 64 * kBwdWaves, stream)
-                        : go(k_gated_bwd<T, V, kBwdSteps, kBwdWaves, false>, a, 64 * kBwdWaves, stream);
+hipError_t bwd(const GatedScanLaunch& p, const GatedArgs& a) {
+  if (lines(p)) return p.bf16 ? go_bwd<uint16_t, 2, kOnce>(a, p.stream) : go_bwd<float, 1, kOnce>(a, p.stream);
+  return !p.bf16    ? go_bwd<float, 1, kUsual>(a, p.stream)
+         : pairs(p) ? go_bwd<uint16_t, 2, kUsual>(a, p.stream)
+                    : go_bwd<uint16_t, 1, kUsual>(a, p.stream);
 }
 
 constexpr int64_t kFwdLen = kFwdSteps * kFwdWaves, kBwdLen = kBwdSteps * kBwdWaves;
@@ -729,10 +759,7 @@ hipError_t launch_gated_scan_bwd(const GatedScanLaunch& p) {
       f.ckpt = a.ckpt;
       if (p.seqlen > 0 && (rc = fwd<false>(p, f)) != hipSuccess) return rc;
     }
-    rc = !p.bf16    ? go_bwd<float, 1>(a, p.stream)
-         : pairs(p) ? go_bwd<uint16_t, 2>(a, p.stream)
-                    : go_bwd<uint16_t, 1>(a, p.stream);
-    if (rc != hipSuccess) return rc;
+    if ((rc = bwd(p, a)) != hipSuccess) return rc;
   }
   if (p.dlog_a == nullptr) return hipSuccess;
   return col_sum(part, p.dlog_a, nullptr, 0, p.batch * pieces, p.width, p.stream);

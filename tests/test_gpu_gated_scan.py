@@ -79,6 +79,37 @@ def test_strides(lib, pad, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("z", [False, True])
+@pytest.mark.parametrize("lengths", [None, [700, 0, 699, 129, 1]])
+def test_rows_of_whole_cache_lines(lib, lengths, z, dtype):
+    """Rows of 128 bytes and multiples, also as column ranges, which the caches are told about: the definition's
+    results, and to the bit those of the same rows elsewhere in memory; with and without saved states."""
+    import torch
+    from selective_state_space_84_amd import binding as bd
+    B, L = 5, 700
+    for D, pad in ((64, 64), (192, 0)):
+        print("case", D, pad, flush=True)
+        d, dy, dh = _make(D, B, L, D, dtype, z=z, pad=pad)
+        if lengths is not None:
+            for b, n in enumerate(lengths):
+                for t in (d["x"], d["ga"], d["gx"], d["z"], dy):
+                    if t is not None:
+                        t[b, n:] = float("nan")
+        got = _check(d, dy, dh, dtype, lengths)
+        other = dict(d)
+        for k in ("x", "ga", "gx", "z"):
+            if d[k] is not None:
+                wide = torch.empty(B, L, D + 2, dtype=d[k].dtype, device=DEV)
+                other[k] = wide[:, :, :D].copy_(d[k])
+        for ins in (d, other):
+            y, hl, none = bd.ssm_gated_scan_fwd(**ins, lengths=_lens(lengths))
+            assert none is None and torch.equal(y, got["y"]) and torch.equal(hl, got["h_last"])
+            g = bd.ssm_gated_scan_bwd(**ins, dy=dy, lengths=_lens(lengths), dh_last=dh)
+            for k, v in g.items():
+                assert torch.equal(v, got[k]), k
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("ckpt", [False, True])
 @pytest.mark.parametrize("L,lengths,D", [
     (400, [400, 399, 0, 1, 128, 129, 64, 257, -3], 100),
