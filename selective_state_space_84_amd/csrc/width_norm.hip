@@ -11,9 +11,9 @@
 // sums over a row close together (one barrier where the team is a workgroup), and a gradient's team adds up
 // its rows' weight gradients in registers.
 //
-// Bound by HBM (a copy reaches 5.1 to 5.3 TB/s): the gated norm of 32768 rows of 5120 in bf16 takes 185 us, 5.4
-// TB/s; its gradient over 8 groups of 512 in 16384 rows 127 us, 5.3 TB/s; the residual norm of 32768 x 2560 with
-// an fp32 stream 181 us, 5.6 TB/s; its gradient of 16384 x 2560 147 us, 5.1 TB/s.  Groups that are not whole 16-byte
+// Bound by HBM (a copy reaches 5.1 to 5.3 TB/s): the gated norm of 32768 rows of 5120 in bf16 takes 174 us, 5.8
+// TB/s; its gradient over 8 groups of 512 in 16384 rows 122 us, 5.5 TB/s; the residual norm of 32768 x 2560 with
+// an fp32 stream 181 us, 5.6 TB/s; its gradient of 16384 x 2560 130 us, 5.8 TB/s.  Groups that are not whole 16-byte
 // pieces are read value by value (gradient of 8192 x 2501: 94 us, 3.9 TB/s).
 #include "col_sum.h"
 #include "gated_launch.h"
@@ -27,6 +27,25 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
+// With bf16 values the gated norm and both gradients take the rows that they read, and bf16 rows that they write, as
+// data used once, which the caches need not keep: gated norm of 32768 x 5120 185 -> 174 us, its gradient over 8 groups
+// of 512 in 16384 rows 127 -> 122, the residual norm's of 16384 x 2560 with an fp32 stream 147 -> 130.  Not so
+// weights, fp32 values (gated gradient of 8192 x 4096 130 -> 148) and the residual update (32768 x 2560 with an fp32
+// stream 181 -> 189).
+template <typename T>
+constexpr bool kOnce = sizeof(T) == 2;
+template <bool ONCE, typename P>
+__device__ __forceinline__ P fetch(const P* p) {
+  return ONCE ? __builtin_nontemporal_load(p) : *p;
+}
+template <bool ONCE, typename P>
+__device__ __forceinline__ void leave(P* p, P v) {
+  if constexpr (ONCE)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+
 // Eight values of one lane.  VEC: neighbours, in 16-byte accesses.  Else: one by one,
 // `step` apart, so that the lanes of a team read neighbours; those from `left`
 // on do not exist.
@@ -36,9 +55,10 @@ template <>
 struct Eight<float, true> {
   u32x4 a[2];
   __device__ __forceinline__ void zero() { a[0] = a[1] = u32x4{0, 0, 0, 0}; }
+  template <bool ONCE>
   __device__ __forceinline__ void load(const float* p, int, int) {
-    a[0] = *reinterpret_cast<const u32x4*>(p);
-    a[1] = *reinterpret_cast<const u32x4*>(p + 4);
+    a[0] = fetch<ONCE>(reinterpret_cast<const u32x4*>(p));
+    a[1] = fetch<ONCE>(reinterpret_cast<const u32x4*>(p + 4));
   }
   __device__ __forceinline__ float get(int j) const {
     const uint32_t v = a[j / 4][j % 4];
@@ -50,7 +70,10 @@ template <>
 struct Eight<uint16_t, true> {
   u32x4 a;
   __device__ __forceinline__ void zero() { a = u32x4{0, 0, 0, 0}; }
-  __device__ __forceinline__ void load(const uint16_t* p, int, int) { a = *reinterpret_cast<const u32x4*>(p); }
+  template <bool ONCE>
+  __device__ __forceinline__ void load(const uint16_t* p, int, int) {
+    a = fetch<ONCE>(reinterpret_cast<const u32x4*>(p));
+  }
   __device__ __forceinline__ float get(int j) const {
     const uint32_t v = a[j / 2];
     return __builtin_bit_cast(float, j % 2 ? v & 0xffff0000u : v << 16);
@@ -65,6 +88,7 @@ struct Eight<T, false> {
 #pragma unroll
     for (int j = 0; j < 8; ++j) a[j] = T(0);
   }
+  template <bool ONCE>
   __device__ __forceinline__ void load(const T* p, int step, int left) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) a[j] = j * step < left ? p[j * step] : T(0);
@@ -73,25 +97,25 @@ struct Eight<T, false> {
   __device__ __forceinline__ void forget() {}
 };
 
-template <bool VEC>
+template <bool VEC, bool ONCE>
 __device__ __forceinline__ void put8(float* p, const float* v, int step, int left) {
   if constexpr (VEC) {
-    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    leave<ONCE>(reinterpret_cast<f32x4*>(p), f32x4{v[0], v[1], v[2], v[3]});
+    leave<ONCE>(reinterpret_cast<f32x4*>(p + 4), f32x4{v[4], v[5], v[6], v[7]});
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (j * step < left) p[j * step] = v[j];
   }
 }
-template <bool VEC>
+template <bool VEC, bool ONCE>
 __device__ __forceinline__ void put8(uint16_t* p, const float* v, int step, int left) {
   if constexpr (VEC) {
     u32x4 r;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       r[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2 * k], v[2 * k + 1]}, bf16x2));
-    *reinterpret_cast<u32x4*>(p) = r;
+    leave<ONCE>(reinterpret_cast<u32x4*>(p), r);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -140,20 +164,20 @@ struct Place {
   __device__ __forceinline__ int at(int v) const { return VEC ? (v * lanes + ln) * 8 : v * 8 * lanes + ln; }
   __device__ __forceinline__ int step() const { return VEC ? 1 : lanes; }
   __device__ __forceinline__ int left(int v) const { return dim - at(v); }
-  template <typename E, typename T>
+  template <bool ONCE, typename E, typename T>
   __device__ __forceinline__ void load(E& e, const T* p, int v) const {
     if (left(v) > 0)
-      e.load(p + at(v), step(), left(v));
+      e.template load<ONCE>(p + at(v), step(), left(v));
     else
       e.zero();
   }
-  template <typename T>
+  template <bool ONCE, typename T>
   __device__ __forceinline__ void store(T* p, const float* x, int v) const {
-    if (left(v) > 0) put8<VEC>(p + at(v), x, step(), left(v));
+    if (left(v) > 0) put8<VEC, ONCE>(p + at(v), x, step(), left(v));
   }
   __device__ __forceinline__ void weight(float (&w)[8], const float* p, int v) const {
     Eight<float, VEC> e;
-    if (p != nullptr) load(e, p + col, v);
+    if (p != nullptr) load<false>(e, p + col, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] = p != nullptr ? e.get(j) : 1.0f;
   }
@@ -214,8 +238,8 @@ __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_gated_norm(const Norm
     Eight<T, VEC> x[NV], z[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      at.load(x[v], xp, v);
-      if (Z) at.load(z[v], zp, v);
+      at.template load<kOnce<T>>(x[v], xp, v);
+      if (Z) at.template load<kOnce<T>>(z[v], zp, v);
     }
     float t[NV][8], ss = 0.0f;
 #pragma unroll
@@ -235,7 +259,7 @@ __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_gated_norm(const Norm
         t[v][j] *= rs * w[v][j];
         if (Z && !FIRST) t[v][j] *= silu(z[v].get(j));
       }
-      at.store(yp, t[v], v);
+      at.template store<kOnce<T>>(yp, t[v], v);
     }
   }
 }
@@ -288,9 +312,9 @@ struct GatedRow {
   __device__ __forceinline__ void load(const NormArgs& a, const P& at, int64_t r) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      at.load(x[v], static_cast<const T*>(a.x) + r * a.xs + at.col, v);
-      if (Z) at.load(z[v], static_cast<const T*>(a.z) + r * a.zs + at.col, v);
-      at.load(dy[v], static_cast<const T*>(a.dy) + r * a.width + at.col, v);
+      at.template load<kOnce<T>>(x[v], static_cast<const T*>(a.x) + r * a.xs + at.col, v);
+      if (Z) at.template load<kOnce<T>>(z[v], static_cast<const T*>(a.z) + r * a.zs + at.col, v);
+      at.template load<kOnce<T>>(dy[v], static_cast<const T*>(a.dy) + r * a.width + at.col, v);
     }
   }
 };
@@ -347,13 +371,13 @@ __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_gated_norm_bwd(const 
           ox[j] = n(xv, w[j] * dv);
         }
       }
-      at.store(dx, ox, v);
-      if (Z) at.store(dz, oz, v);
+      at.template store<kOnce<T>>(dx, ox, v);
+      if (Z) at.template store<kOnce<T>>(dz, oz, v);
     }
   }
   if (a.part == nullptr || at.row >= a.rows) return;
 #pragma unroll
-  for (int v = 0; v < NV; ++v) at.store(a.part + at.team * at.dim, dw[v], v);
+  for (int v = 0; v < NV; ++v) at.template store<false>(a.part + at.team * at.dim, dw[v], v);
 }
 
 struct ResArgs {
@@ -386,9 +410,9 @@ __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_residual_norm(const R
     Eight<R, VEC> e[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      at.load(x[v], static_cast<const T*>(a.x) + r * a.xs, v);
+      at.template load<false>(x[v], static_cast<const T*>(a.x) + r * a.xs, v);
       if (a.res != nullptr)
-        at.load(e[v], static_cast<const R*>(a.res) + r * a.width, v);
+        at.template load<false>(e[v], static_cast<const R*>(a.res) + r * a.width, v);
       else
         e[v].zero();
     }
@@ -411,14 +435,14 @@ __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_residual_norm(const R
         // Behind the group there are only zeros (with weights of 1): they add nothing.
         ss = __builtin_fmaf(t[v][j], t[v][j], ss);
       }
-      at.store(rp, t[v], v);
+      at.template store<false>(rp, t[v], v);
     }
     const float rs = __builtin_amdgcn_rsqf(__builtin_fmaf(at.sum(ss), inv, a.eps));
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) t[v][j] *= rs * wp[v][j];
-      at.store(static_cast<T*>(a.y) + r * a.width, t[v], v);
+      at.template store<false>(static_cast<T*>(a.y) + r * a.width, t[v], v);
     }
   }
 }
@@ -434,10 +458,10 @@ struct ResRow {
     for (int v = 0; v < NV; ++v) {
       x[v].zero();
       de[v].zero();
-      if (a.x != nullptr) at.load(x[v], static_cast<const T*>(a.x) + r * a.xs, v);
-      at.load(dy[v], static_cast<const T*>(a.dy) + r * a.width, v);
-      at.load(e[v], static_cast<const R*>(a.res) + r * a.width, v);
-      if (a.dres_out != nullptr) at.load(de[v], static_cast<const R*>(a.dres_out) + r * a.width, v);
+      if (a.x != nullptr) at.template load<kOnce<T>>(x[v], static_cast<const T*>(a.x) + r * a.xs, v);
+      at.template load<kOnce<T>>(dy[v], static_cast<const T*>(a.dy) + r * a.width, v);
+      at.template load<kOnce<T>>(e[v], static_cast<const R*>(a.res) + r * a.width, v);
+      if (a.dres_out != nullptr) at.template load<kOnce<T>>(de[v], static_cast<const R*>(a.dres_out) + r * a.width, v);
     }
   }
 };
@@ -498,15 +522,15 @@ __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_residual_norm_bwd(con
         dwo[v][j] = __builtin_fmaf(ag * x, m.rs, dwo[v][j]);
         gx[j] = POST ? m(x, wo[j] * ag) : wo[j] * ag;
       }
-      if (a.dres != nullptr) at.store(static_cast<R*>(a.dres) + r * a.width, g, v);
-      at.store(static_cast<T*>(a.dx) + r * a.width, gx, v);
+      if (a.dres != nullptr) at.template store<false>(static_cast<R*>(a.dres) + r * a.width, g, v);
+      at.template store<kOnce<T>>(static_cast<T*>(a.dx) + r * a.width, gx, v);
     }
   }
   if (a.part == nullptr || at.row >= a.rows) return;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    at.store(a.part + at.team * at.dim, dwp[v], v);
-    at.store(a.part + a.part_post + at.team * at.dim, dwo[v], v);
+    at.template store<false>(a.part + at.team * at.dim, dwp[v], v);
+    at.template store<false>(a.part + a.part_post + at.team * at.dim, dwo[v], v);
   }
 }
 
@@ -520,11 +544,11 @@ struct Shape {
 
 // Workgroups of w waves a CU is given, each of which walks every so-many-th row.
 // Forward: eight times what a CU holds at once (32 waves of one piece a lane, 16 of two), so that CUs that
-// get ahead take more (32768 rows of 5120, gate first: 185 us; four times 194, once 229; 32768 x 2560 with
-// residual: 181, 188, 201; against that 32768 x 1024: 36.9, 34.7, 36.2).
+// get ahead take more (32768 rows of 5120, gate first: 174 us; four times and 16 times 179; twice 188; 32768 x 2560 with
+// residual: 181, 188, 180, 195; against that 32768 x 1024: 37.4, 34.2, 37.1, 35.6).
 // Gradients: eight waves, in whole workgroups: more only add sums of weights to write and to join, and
-// rows in between (16384 x 2560 with residual: 147 us, with 20 waves 171, with 5 163; 32768 x 768: 88, 96, 122;
-// 16384 x 8 x 512: 127, 135, 194; 8192 x 2501: 94, 129, 141).
+// rows in between (16384 x 2560 with residual: 129 us, with 16 waves 165, with 24 154; 32768 x 768: 88, 92, 100;
+// 16384 x 8 x 512: 122, 127, 138; against that 32768 x 1024: 74.9, 70.7, 81.1).
 int64_t groups_per_cu(int w, int nv, bool grad) {
   if (grad) return w < 8 ? (7 + w) / w : 1;
   return 8 * (nv == 1 ? 32 / w : 1);
