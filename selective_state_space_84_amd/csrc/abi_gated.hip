@@ -34,7 +34,7 @@ int check_step(int64_t* stride, int64_t width, int64_t rows, int64_t most = kMax
 
 int check_scan_dims(int64_t batch, int64_t seqlen, int64_t width) {
   if (batch < 0 || seqlen < 0 || width < 0) return SSM_ERR_BAD_DIM;
-  if (seqlen > kMaxSteps || width > kMaxWidth) return SSM_ERR_BAD_DIM;
+  if (batch > kMaxElems || seqlen > kMaxSteps || width > kMaxWidth) return SSM_ERR_BAD_DIM;
   int64_t n, st;
   if (!mul3(batch, seqlen, width, &n) || !mul3(batch, width, 1, &st) || n > kMaxElems || st > kMaxStates)
     return SSM_ERR_BAD_DIM;
@@ -143,7 +143,7 @@ int gated_update_impl(ssm::GatedUpdateLaunch p, int32_t io_dtype) {
 
 // Rows of `width` values, `groups` norms a row.
 int check_norm_dims(int64_t rows, int64_t width, int64_t groups) {
-  if (rows < 0 || width < 0 || groups <= 0 || width > kMaxWidth) return SSM_ERR_BAD_DIM;
+  if (rows < 0 || width < 0 || groups <= 0 || width > kMaxWidth || groups > kMaxWidth) return SSM_ERR_BAD_DIM;
   int64_t n;
   if (!mul3(rows, width, 1, &n) || n > kMaxElems || rows > kMaxElems) return SSM_ERR_BAD_DIM;
   if (width % groups != 0 || width / groups > ssm::kMaxNormWidth) return SSM_ERR_UNSUPPORTED;

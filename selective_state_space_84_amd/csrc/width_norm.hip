@@ -544,8 +544,8 @@ struct Shape {
 
 // Workgroups of w waves a CU is given, each of which walks every so-many-th row.
 // Forward: eight times what a CU holds at once (32 waves of one piece a lane, 16 of two), so that CUs that
-// get ahead take more (32768 rows of 5120, gate first: 174 us; four times and 16 times 179; twice 188; 32768 x 2560 with
-// residual: 181, 188, 180, 195; against that 32768 x 1024: 37.4, 34.2, 37.1, 35.6).
+// get ahead take more (32768 rows of 5120, gate first: 174 us; four times and 16 times 179; twice 188; 32768 x 2560
+// with residual: 181, 188, 180, 195; against that 32768 x 1024: 37.4, 34.2, 37.1, 35.6).
 // Gradients: eight waves, in whole workgroups: more only add sums of weights to write and to join, and
 // rows in between (16384 x 2560 with residual: 129 us, with 16 waves 165, with 24 154; 32768 x 768: 88, 92, 100;
 // 16384 x 8 x 512: 122, 127, 138; against that 32768 x 1024: 74.9, 70.7, 81.1).

@@ -83,6 +83,22 @@ def test_scan_empty(lib):
     assert _fwd(lib, D=0, x=None, ga=None, gx=None, la=None, y=None) == bd.SSM_OK
 
 
+def test_counts_without_an_element(lib):
+    """Rows and groups of nothing are still counted in 64 bits, also in bytes."""
+    for b in (1 << 62, (1 << 48) + 1):
+        assert _fwd(lib, b=b, L=0, D=0, lens=P0 + 6 * MB) == bd.SSM_ERR_BAD_DIM
+        assert _bwd(lib, b=b, L=0, D=0, lens=P0 + 6 * MB) == bd.SSM_ERR_BAD_DIM
+        assert lib.ssm_gated_scan_fwd_workspace_size(b, 0, 0, 1) == BAD
+    assert _fwd(lib, b=1 << 48, L=0, D=0) == bd.SSM_OK
+    for groups in ((1 << 62) + 1, (1 << 23) + 1):
+        assert lib.ssm_gated_norm_fwd(P0, None, None, P0 + MB, 4, 0, groups, 0, 0, 1e-6, 1, 1, None) == \
+            bd.SSM_ERR_BAD_DIM
+        assert lib.ssm_gated_norm_bwd(P0, None, None, P0 + MB, P0 + 2 * MB, None, P0 + 3 * MB, 4, 0, groups, 0, 0, 1e-6,
+                                      1, 1, P0 + 4 * MB, MB, None) == bd.SSM_ERR_BAD_DIM
+        assert lib.ssm_gated_norm_bwd_workspace_size(4, 0, groups) == BAD
+    assert lib.ssm_gated_norm_fwd(P0, None, None, P0 + MB, 4, 0, 1 << 23, 0, 0, 1e-6, 1, 1, None) == bd.SSM_OK
+
+
 def _bwd(lib, x=P0, ga=P0 + MB, gx=P0 + 2 * MB, la=P0 + 3 * MB, z=None, lens=None, h0=None, dy=P0 + 4 * MB, dh=None,
          ck=None, dx=P0 + 10 * MB, dga=P0 + 11 * MB, dgx=P0 + 12 * MB, dz=None, dla=P0 + 13 * MB, dh0=None, b=2, L=40,
          D=96, xs=0, dtype=1, ws=P0 + 90 * MB, wsb=8 * MB):
