@@ -7,13 +7,19 @@
 //   dx = g m sx, dgx = g m x sx (1 - sx),
 //   d(log a) = g (a h - (a^2 / m) sx x),
 //   dga = d(log a) log_a sa (1 - sa), and d(log a) sa adds to dlog_a.
+// What is left of a gate, 1 - s = e / (1 + e) = e s with e = e^-v, is a product and
+// not a difference: 1 - s in fp32 is off by half of it at v = 16 and without a correct digit at 20.
 #pragma once
 
 #include "ssm_device.h"
 
 namespace ssm {
 
-__device__ __forceinline__ float sigmoid(float v) { return hw_rcp(1.0f + hw_exp2(-v * kLog2e)); }
+__device__ __forceinline__ float exp_minus(float v) { return hw_exp2(-v * kLog2e); }
+// sigmoid(v) from e = e^-v, and 1 - sigmoid(v) from that (where e is infinite, the product is NaN and 1 is left).
+__device__ __forceinline__ float sigmoid_of(float e) { return hw_rcp(1.0f + e); }
+__device__ __forceinline__ float left_of(float e, float s) { return __builtin_fminf(e * s, 1.0f); }
+__device__ __forceinline__ float sigmoid(float v) { return sigmoid_of(exp_minus(v)); }
 
 // c ? a : b as a select: of the ternary operator the compiler makes a branch around what a or b costs, which
 // takes longer than both.
@@ -42,7 +48,7 @@ __device__ __forceinline__ float one_minus_exp4(float y, float p) {
 constexpr float kTiny = 1.17549435e-38f;
 
 struct GatedStep {
-  float sa, sx, a, m2;
+  float ea, ex, sa, sx, a, m2;  // ea, ex: e^-ga, e^-gx
   __device__ __forceinline__ float m() const { return __builtin_amdgcn_sqrtf(m2); }
   __device__ __forceinline__ float inv_m() const { return m2 >= kTiny ? __builtin_amdgcn_rsqf(m2) : 0.0f; }
 };
@@ -50,8 +56,10 @@ struct GatedStep {
 // c2 = log_a log2(e).
 __device__ __forceinline__ GatedStep gated_step(float ga, float gx, float c2) {
   GatedStep s;
-  s.sa = sigmoid(ga);
-  s.sx = sigmoid(gx);
+  s.ea = exp_minus(ga);
+  s.ex = exp_minus(gx);
+  s.sa = sigmoid_of(s.ea);
+  s.sx = sigmoid_of(s.ex);
   const float y = c2 * s.sa;
   s.a = hw_exp2(y);
   s.m2 = one_minus_exp4(y, s.a);

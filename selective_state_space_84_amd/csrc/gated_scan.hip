@@ -17,7 +17,10 @@
 // The gradient runs the same way from the last piece to the first, on P_t = a_t (e_t + P_{t+1}), e = dy silu(z):
 // what reaches the state before step t.  The states inside a piece are formed again from the state at its start,
 // saved by the forward call or by a forward pass without outputs.  While a piece waits, it forms what its
-// gradients are in multiples of g, the gradient of a step's state, so that five products a step are left then.
+// gradients are in multiples of g, the gradient of a step's state, so that six products a step are left then.  What is
+// left of a gate, 1 - s, is formed without a difference and waits in LDS (gx) or comes from e^-ga once more: against
+// products of s alone, which lose it for open gates, 8 x 2048 x 4096 with the forward call takes the same, 1 x 16384 x
+// 2560 218 us for 215.
 //
 // Bound by HBM, and nearly as much by the vector units (33 instructions an element forward, six of them
 // transcendental, busy 60% of the time).  Measured in bf16 (a copy reaches 5.1 to 5.3 TB/s): 4 x 8192 x 5120 with
@@ -385,8 +388,10 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_fwd(const Gated
 
 template <typename T, int V, int TS, int W, bool Z, int HINT>
 __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const GatedArgs a) {
-  __shared__ Fold fwd[W][64 * V], rev[W][64 * V], pre[kMaxBlock - 1][64 * V];
+  __shared__ Fold fwd[W - 1][64 * V], rev[W][64 * V], pre[kMaxBlock - 1][64 * V];
   __shared__ float front[64 * V];
+  // 1 - sx, which no register has room for; two workgroups (80 KB each with two channels a lane) still fit a CU.
+  __shared__ __align__(8) float left[W][TS][64 * V];
   __shared__ int shared;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const Spot<V> at(a, &shared);  // q counts from the sequence's end
@@ -420,7 +425,7 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const Gated
     return;
   }
   Io<T, V> x[TS], dy[TS], z[TS];
-  float dec[TS][V], sa[TS][V], kx[TS][V], inv[TS][V], la[V];  // kx = m sx, inv = 1 / m
+  float dec[TS][V], ea[TS][V], kx[TS][V], i2[TS][V];  // ea = e^-ga, kx = m sx, i2 = 1 / m^2
   if (m > 0) {
     Io<T, V> ga[TS], gx[TS];
     load_steps<HINT>(ga, a.ga, row, a.as, off, m);
@@ -428,20 +433,23 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const Gated
     load_steps<HINT>(x, a.x, row, a.xs, off, m);
     load_steps<HINT>(dy, a.dy, row, step, off, m);
     if (Z) load_steps<HINT>(z, a.z, row, a.zs, off, m);
+    float c2[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) la[v] = a.log_a[at.d + v];
+    for (int v = 0; v < V; ++v) c2[v] = a.log_a[at.d + v] * kLog2e;
 #pragma unroll
     for (int i = 0; i < TS; ++i) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const GatedStep s = gated_step(ga[i].get(v), gx[i].get(v), la[v] * kLog2e);
+        const GatedStep s = gated_step(ga[i].get(v), gx[i].get(v), c2[v]);
+        const float inv = s.inv_m();
         dec[i][v] = s.a;
-        sa[i][v] = s.sa;
-        inv[i][v] = s.inv_m();
-        kx[i][v] = s.m2 * inv[i][v] * s.sx;
+        ea[i][v] = s.ea;
+        i2[i][v] = inv * inv;
+        kx[i][v] = s.m2 * inv * s.sx;
+        left[wave][i][lane * V + v] = left_of(s.ex, s.sx);
       }
 #pragma unroll
-      for (int v = 0; v < V; ++v) settle(dec[i][v], sa[i][v], inv[i][v], kx[i][v]);
+      for (int v = 0; v < V; ++v) settle(dec[i][v], ea[i][v], i2[i][v], kx[i][v]);
     }
   }
   if (m < TS)  // steps that do not exist hand everything on
@@ -454,7 +462,9 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const Gated
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           dec[i][v] = 1.0f;
-          sa[i][v] = kx[i][v] = inv[i][v] = 0.0f;
+          ea[i][v] = __builtin_inff();  // a gate that is shut
+          kx[i][v] = i2[i][v] = 0.0f;
+          left[wave][i][lane * V + v] = 0.0f;
         }
       }
   Fold f[V], r[V];
@@ -470,7 +480,7 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const Gated
       r[v].s = dec[i][v] * (e + r[v].s);
     }
     r[v].a = f[v].a;
-    fwd[wave][lane * V + v] = f[v];
+    if (wave < W - 1) fwd[wave][lane * V + v] = f[v];
     rev[wave][lane * V + v] = r[v];
   }
   __syncthreads();
@@ -485,7 +495,7 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const Gated
       if (!l.closes) publish(fp + at.q * a.width + v, r[v]);
     }
   // The states before each step, and what a step's gradients are in multiples of that of its state:
-  //   dx = g kx, dgx = g ki, d(log a) sa = g gs, dga = g gs ka.
+  //   dx = g kx, dgx = g ki, d(log a) sa = g gs, dga = g gs log_a ka.
   float gs[TS][V], ka[TS][V], ki[TS][V], e[TS][V];
   const int64_t saved = (a.seqlen + kGatedCkpt - 1) / kGatedCkpt;
   const float* const ck = a.ckpt + (at.b * saved + c0 / kGatedCkpt) * a.width + at.d;
@@ -503,10 +513,10 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const Gated
     float dz[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float ac = dec[i][v], u = kx[i][v] * x[i].get(v), w = u * inv[i][v];  // w = sx x
-      gs[i][v] = ac * sa[i][v] * __builtin_fmaf(-(ac * inv[i][v]), w, h[v]);
-      ka[i][v] = __builtin_fmaf(-la[v], sa[i][v], la[v]);
-      ki[i][v] = __builtin_fmaf(-kx[i][v], w, u);
+      const float ac = dec[i][v], u = kx[i][v] * x[i].get(v), s = sigmoid_of(ea[i][v]);
+      gs[i][v] = ac * s * __builtin_fmaf(-(ac * i2[i][v]), u, h[v]);
+      ka[i][v] = left_of(ea[i][v], s);
+      ki[i][v] = u * left[wave][i][lane * V + v];
       h[v] = __builtin_fmaf(ac, h[v], u);
       if (Z) {
         const float zv = z[i].get(v), q = sigmoid(zv), d = dy[i].get(v);
@@ -525,7 +535,9 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const Gated
     collect<V, W>(l, wave, lane, fp, sp, a.width, pre, front);
     __syncthreads();
   }
-  float p[V], sum[V] = {};
+  float p[V], sum[V] = {}, la[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) la[v] = a.log_a[at.d + v];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     p[v] = !l.heads ? front[lane * V + v] : a.dh_last != nullptr ? a.dh_last[st + v] : 0.0f;
@@ -544,7 +556,7 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const Gated
         const float g = (Z ? e[i][v] : dy[i].get(v)) + p[v], t = g * gs[i][v];
         dx[v] = g * kx[i][v];
         di[v] = g * ki[i][v];
-        da[v] = t * ka[i][v];
+        da[v] = t * la[v] * ka[i][v];
         if (!ALL && i >= m) dx[v] = di[v] = da[v] = 0.0f;  // even where what comes from behind is not finite
         sum[v] += t;
         p[v] = dec[i][v] * g;
@@ -567,13 +579,13 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const Gated
   // The waves' sums in their order.
   __syncthreads();
 #pragma unroll
-  for (int v = 0; v < V; ++v) fwd[wave][lane * V + v].a = sum[v];
+  for (int v = 0; v < V; ++v) rev[wave][lane * V + v].a = sum[v];
   __syncthreads();
   if (wave == 0)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float t = 0.0f;
-      for (int k = 0; k < W; ++k) t += fwd[k][lane * V + v].a;
+      for (int k = 0; k < W; ++k) t += rev[k][lane * V + v].a;
       part[v] = t;
     }
 }
