@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(64 * W, kWavesPerSimd) k_gated_bwd(const Gated
         di[v] = g * ki[i][v];
         da[v] = t * la[v] * ka[i][v];
         if (!ALL && i >= m) dx[v] = di[v] = da[v] = 0.0f;  // even where what comes from behind is not finite
-        sum[v] += t;
+        if (ALL || i < m) sum[v] += t;
         p[v] = dec[i][v] * g;
       }
       if (ALL || t0 + i < seqlen) {

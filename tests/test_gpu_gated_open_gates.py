@@ -51,3 +51,27 @@ def test_gates_of_any_size(lib, dtype):
     d["ga"][:, ::5], d["gx"][:, 1::5] = 100.0, 1000.0
     d["gx"][:, 2::5] = -100.0
     _check(d, dy, dh, dtype, ckpt=True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("z", [False, True])
+def test_sum_over_steps_ends_with_the_row(lib, z, dtype):
+    """dlog_a sums a row's own steps, whatever reaches the steps behind them: with x = 0, h0 > 0 and an infinite
+    gradient of the last state every step of a row adds +inf, and those behind it nothing (not inf * 0).  Where the
+    decays of a row multiply to less than e^-80 (fp32 ends at e^-87), a state or a product of decays may be 0 in fp32
+    and its product with inf NaN: such channels are left out."""
+    import torch
+    from selective_state_space_84_amd import binding as bd
+    for n in (0, 1, 7, 8, 9, 63, 64, 65, 100, 128, 130):
+        print("case", n, z, dtype, flush=True)
+        d, dy, dh = _make(n, 1, 130, 70, dtype, z=z)
+        d["x"].zero_()
+        d["h0"].abs_().add_(1.0)
+        dh.fill_(float("inf"))
+        lens = torch.tensor([n], dtype=torch.int32, device=dy.device)
+        g = bd.ssm_gated_scan_bwd(**d, dy=dy, dh_last=dh, lengths=lens)
+        la = (_np(d["log_a"]) * P.sigmoid(_np(d["ga"][0, :n]))).sum(0)
+        kept = torch.as_tensor(la > -80.0, device=dy.device)
+        assert kept.sum() >= 20 and (kept.all() or n > 9)
+        assert (g["dlog_a"][kept] == (float("inf") if n else 0.0)).all(), n
+        assert (g["dh0"][0, kept] == float("inf")).all(), n
