@@ -696,7 +696,9 @@ int ssm_gated_scan_update(float* h, const int32_t* slots, const void* x, const v
  *   y       : [rows][width] io_dtype, dense.  It may be x itself (dense, in
  *             place) and overlaps nothing else.
  *   eps >= 0.  groups divides width, with at most 16384 values in a group.
- * Means are fp32: |t| below 10^18; a group of zeros with eps 0 gives NaN.
+ * Means are fp32: |t| below 10^18, and with eps below 10^-36 a root mean square
+ * of every group above 10^-18 (below it, outputs may be NaN or infinite; a group of zeros with eps 0
+ * gives NaN).
  */
 int ssm_gated_norm_fwd(const void* x, const void* z, const float* w, void* y, int64_t rows, int64_t width,
                        int64_t groups, int64_t x_stride, int64_t z_stride, float eps, int32_t gate_first,

@@ -140,6 +140,11 @@ __device__ __forceinline__ float lane_sum(float v) {
   return v;
 }
 
+// Sums of squares, and of products of two values, are 1/64 of what they are from a lane's 8 or 16 values on, so that those of
+// 16384 values up to 10^18 stay in fp32's range: a power of two, which rounds nothing, put back with the mean (one product a
+// lane and row).
+constexpr float kShare = 1.0f / 64, kWhole = 64.0f;
+
 // A lane's place: TEAM lanes a group (0: the whole workgroup), NV pieces of 8
 // values a lane.  Team q of all takes group q % groups of rows q / groups,
 // q / groups + dr, ...
@@ -250,7 +255,7 @@ __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_gated_norm(const Norm
         if (Z && FIRST) t[v][j] *= silu(z[v].get(j));
         ss = __builtin_fmaf(t[v][j], t[v][j], ss);
       }
-    const float rs = __builtin_amdgcn_rsqf(__builtin_fmaf(at.sum(ss), inv, a.eps));
+    const float rs = __builtin_amdgcn_rsqf(__builtin_fmaf(at.sum(kShare * ss), kWhole * inv, a.eps));
     T* const yp = static_cast<T*>(a.y) + r * a.width + at.col;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -264,11 +269,11 @@ __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_gated_norm(const Norm
   }
 }
 
-// rs, and what turns w g into the gradient of t.
+// rs, and what turns w g into the gradient of t.  ss: kShare of the sum of squares.
 struct NormGrad {
   float rs, c;
   __device__ __forceinline__ void take(float ss, float sg, float inv, float eps) {
-    rs = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, inv, eps));
+    rs = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, kWhole * inv, eps));
     c = sg * inv * rs * rs;
   }
   __device__ __forceinline__ float operator()(float t, float wg) const { return rs * __builtin_fmaf(-t, c, wg); }
@@ -343,6 +348,7 @@ __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_gated_norm_bwd(const 
         s[1] = __builtin_fmaf(w[j] * g, t, s[1]);
       }
     }
+    s[0] *= kShare;
     at.template sums<2>(s);
     NormGrad n;
     n.take(s[0], s[1], inv, a.eps);
@@ -423,7 +429,7 @@ __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_residual_norm(const R
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(x[v].get(j), x[v].get(j), ss);
-      c *= __builtin_amdgcn_rsqf(__builtin_fmaf(at.sum(ss), inv, a.eps));
+      c *= __builtin_amdgcn_rsqf(__builtin_fmaf(at.sum(kShare * ss), kWhole * inv, a.eps));
     }
     float t[NV][8], ss = 0.0f;
     R* const rp = static_cast<R*>(a.res_out) + r * a.width;
@@ -437,7 +443,7 @@ __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_residual_norm(const R
       }
       at.template store<false>(rp, t[v], v);
     }
-    const float rs = __builtin_amdgcn_rsqf(__builtin_fmaf(at.sum(ss), inv, a.eps));
+    const float rs = __builtin_amdgcn_rsqf(__builtin_fmaf(at.sum(kShare * ss), kWhole * inv, a.eps));
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
 #pragma unroll
@@ -499,12 +505,15 @@ __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_residual_norm_bwd(con
         }
       }
     }
+    s[0] *= kShare;
+    s[2] *= kShare;
+    s[4] *= kShare;
     at.template sums<POST ? 6 : 2>(s);
     NormGrad n, m;
     n.take(s[0], s[1], inv, a.eps);
     m.rs = 1.0f;
     m.c = 0.0f;
-    if (POST) m.take(s[2], a.alpha * __builtin_fmaf(n.rs, __builtin_fmaf(-n.c, s[4], s[3]), s[5]), inv, a.eps);
+    if (POST) m.take(s[2], a.alpha * __builtin_fmaf(n.rs, __builtin_fmaf(-(kWhole * n.c), s[4], s[3]), s[5]), inv, a.eps);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float wp[8], wo[8], g[8], gx[8];
