@@ -597,7 +597,7 @@ size_t ssm_qk_norm_rope_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_
  *                output; 0 stands for width.  Aligned to their elements; faster
  *                where widths, strides and addresses are multiples of 4 bytes.
  *                Strides not below width and at most 2^25.
- *   log_a      : [width] fp32, <= 0 and finite: the log of the strongest decay
+ *   log_a      : [width] fp32 in [-10^38, 0]: the log of the strongest decay
  *                (results for other values are unspecified).  Where 1 - a^2 is
  *                below fp32's normal range the input counts as nothing.
  *   lengths    : [batch] int32 or NULL.  Row b has lengths[b] steps (clamped to
@@ -614,7 +614,9 @@ size_t ssm_qk_norm_rope_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_
  *   workspace  : ssm_gated_scan_fwd_workspace_size() bytes, 256-byte aligned
  *                (may be NULL when that is 0); contents on entry ignored.
  *                Calls that may run at the same time need one each, and so do
- *                two captured graphs that may be replayed at the same time.
+ *                two captured graphs that may be replayed at the same time.  Calls
+ *                that share one by mistake still end, with SSM_OK and wrong values or
+ *                NaN.
  * The state is fp32 and y is rounded once.  Sums are taken in a fixed order:
  * results are bitwise reproducible for given sizes and strides.  Same
  * conventions, validation and error codes as the scan; width above 2^23, more
