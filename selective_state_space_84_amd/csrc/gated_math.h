@@ -8,7 +8,7 @@
 //   d(log a) = g (a h - (a^2 / m) sx x),
 //   dga = d(log a) log_a sa (1 - sa), and d(log a) sa adds to dlog_a.
 // What is left of a gate, 1 - s = e / (1 + e) = e s with e = e^-v, is a product and
-// not a difference: 1 - s in fp32 is off by half of it at v = 16 and without a correct digit at 20.
+// not a difference, which in fp32 is a multiple of 2^-24: 0.6% off at v = 12, all of it at 17.
 #pragma once
 
 #include "ssm_device.h"
@@ -31,7 +31,7 @@ __device__ __forceinline__ float pick(bool c, float a, float b) {
 }
 
 // 1 - 4^y for y <= 0 and p = 2^y.  Above -0.18 (4^y > 0.78) from the series of
-// (e^v - 1) / v to fifth order, v = y ln 4 (truncation below 5e-8 relative), so
+// (e^v - 1) / v to fifth order, v = y ln 4 (truncation below 5.3e-8 relative), so
 // that decays near 1 keep their distance from it; below, 1 - p^2 loses at most
 // two bits.
 __device__ __forceinline__ float one_minus_exp4(float y, float p) {

@@ -24,7 +24,7 @@
 //
 // Bound by HBM, and nearly as much by the vector units (33 instructions an element forward, six of them
 // transcendental, busy 60% of the time).  Measured in bf16 (a copy reaches 5.1 to 5.3 TB/s): 4 x 8192 x 5120 with
-// output gate 312 us, 5.4 TB/s; 1 x 32768 x 2560 146 us, 4.6 TB/s; 8 x 2048 x 4096 forward and gradient 324 us, 4.6
+// output gate 312 us, 5.4 TB/s; 1 x 32768 x 2560 146 us, 4.6 TB/s; 8 x 2048 x 4096 forward and gradient 325 us, 4.6
 // TB/s.
 // Shapes, before the last steps: 16 steps a wave and 8 waves forward, 1 x 32768 x 2560: 166 us; 8 steps 16 waves 195,
 // 16 steps 4 waves 203, 8 steps 8 waves 202, 16 steps 16 waves 177; four channels a lane 222 against 153.  Gradient
@@ -628,10 +628,10 @@ uint64_t places(const GatedScanLaunch& p) {
 bool pairs(const GatedScanLaunch& p) { return p.bf16 && places(p) % 4 == 0; }
 // Rows of whole cache lines, 128 bytes: no two waves touch the same one (a wave's access is 128 or 256 bytes).
 // Such calls let the caches take what they write, and what they read, as data used once: 4 x 8192 x 5120 with
-// output gate 333 -> 312 us, 1 x 32768 x 2560 152 -> 146, forward and gradient of 8 x 2048 x 4096 351 -> 324 (fp32, 2 x
-// 4096 x 2560: 187 -> 165), of 4 x 1024 x 2048 54 -> 52; 1 x 512 x 1024 the same, alone or with a norm or a product
-// that reads y next; fp32 2 x 1024 x 2048 45 -> 47.  A forward call that saves states reads in the usual way, since a
-// gradient that may read the same again follows.  With lines that two waves share it is the other way round: 8 x
+// output gate 332 -> 312 us, 1 x 32768 x 2560 152 -> 146, forward and gradient of 8 x 2048 x 4096 347 -> 325 (fp32, 2 x
+// 4096 x 2560: 186 -> 166), of 4 x 1024 x 2048 58 -> 53 (fp32, 2 x 1024 x 2048: 49 -> 46); 1 x 512 x 1024 the same,
+// alone or with a norm or a product that reads y next.  A forward call that saves states reads in the usual way, since
+// a gradient that may read the same again follows.  With lines that two waves share it is the other way round: 8 x
 // 2048 x 2049 forward and gradient 204 -> 228 with such writes, 310 with both.
 bool lines(const GatedScanLaunch& p) { return places(p) % 128 == 0; }
 

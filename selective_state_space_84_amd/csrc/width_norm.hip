@@ -13,8 +13,10 @@
 //
 // Bound by HBM (a copy reaches 5.1 to 5.3 TB/s): the gated norm of 32768 rows of 5120 in bf16 takes 174 us, 5.8
 // TB/s; its gradient over 8 groups of 512 in 16384 rows 122 us, 5.5 TB/s; the residual norm of 32768 x 2560 with
-// an fp32 stream 181 us, 5.6 TB/s; its gradient of 16384 x 2560 130 us, 5.8 TB/s.  Groups that are not whole 16-byte
-// pieces are read value by value (gradient of 8192 x 2501: 94 us, 3.9 TB/s).
+// an fp32 stream 181 us, 5.6 TB/s (bf16: 120, 5.6); its gradient of 16384 x 2560 143 us, 5.3 TB/s (bf16: 95, 5.3).
+// Groups that are not whole 16-byte pieces are read value by value (gradient of 8192 x 2501: 93 us, 4.0 TB/s).  All
+// figures of this file with outputs that go to other memory from pass to pass: written over the same 250 MB, which the
+// last-level cache partly holds, that gradient takes 130 us.
 #include "col_sum.h"
 #include "gated_launch.h"
 #include "ssm_device.h"
@@ -29,8 +31,8 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // With bf16 values the gated norm and both gradients take the rows that they read, and bf16 rows that they write, as
 // data used once, which the caches need not keep: gated norm of 32768 x 5120 185 -> 174 us, its gradient over 8 groups
-// of 512 in 16384 rows 127 -> 122, the residual norm's of 16384 x 2560 with an fp32 stream 147 -> 130.  Not so
-// weights, fp32 values (gated gradient of 8192 x 4096 130 -> 148) and the residual update (32768 x 2560 with an fp32
+// of 512 in 16384 rows 128 -> 125, the residual norm's of 16384 x 2560 with an fp32 stream 147 -> 143.  Not so
+// weights, fp32 values (gated gradient of 8192 x 4096 130 -> 149) and the residual update (32768 x 2560 with an fp32
 // stream 181 -> 189).
 template <typename T>
 constexpr bool kOnce = sizeof(T) == 2;
@@ -140,9 +142,9 @@ __device__ __forceinline__ float lane_sum(float v) {
   return v;
 }
 
-// Sums of squares, and of products of two values, are 1/64 of what they are from a lane's 8 or 16 values on, so that those of
-// 16384 values up to 10^18 stay in fp32's range: a power of two, which rounds nothing, put back with the mean (one product a
-// lane and row).
+// Sums of squares, and of products of two values, go over the team as 1/64 of what a lane's 8 or 16 values add up to:
+// those of 16384 values up to 10^18 stay in fp32's range, and a power of two rounds nothing, put back with the
+// mean (one product a lane and row).
 constexpr float kShare = 1.0f / 64, kWhole = 64.0f;
 
 // A lane's place: TEAM lanes a group (0: the whole workgroup), NV pieces of 8
@@ -513,7 +515,8 @@ __global__ void __launch_bounds__(TEAM > 0 ? 256 : 1024) k_residual_norm_bwd(con
     n.take(s[0], s[1], inv, a.eps);
     m.rs = 1.0f;
     m.c = 0.0f;
-    if (POST) m.take(s[2], a.alpha * __builtin_fmaf(n.rs, __builtin_fmaf(-(kWhole * n.c), s[4], s[3]), s[5]), inv, a.eps);
+    if (POST)
+      m.take(s[2], a.alpha * __builtin_fmaf(n.rs, __builtin_fmaf(-(kWhole * n.c), s[4], s[3]), s[5]), inv, a.eps);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float wp[8], wo[8], g[8], gx[8];
@@ -553,11 +556,13 @@ struct Shape {
 
 // Workgroups of w waves a CU is given, each of which walks every so-many-th row.
 // Forward: eight times what a CU holds at once (32 waves of one piece a lane, 16 of two), so that CUs that
-// get ahead take more (32768 rows of 5120, gate first: 174 us; four times and 16 times 179; twice 188; 32768 x 2560
-// with residual: 181, 188, 180, 195; against that 32768 x 1024: 37.4, 34.2, 37.1, 35.6).
+// get ahead take more (32768 rows of 5120, gate first: 174 us; four times and 16 times 179; twice 187; 32768 x 2560
+// with residual: 181, 187, 180, 194, in bf16 120, 124, 123, 129; 32768 x 1024 with residual: 74, 75, 74, 77; against
+// that the gated norm of 32768 x 1024: 37.3, 34.2, 37.2, 35.7).
 // Gradients: eight waves, in whole workgroups: more only add sums of weights to write and to join, and
-// rows in between (16384 x 2560 with residual: 129 us, with 16 waves 165, with 24 154; 32768 x 768: 88, 92, 100;
-// 16384 x 8 x 512: 122, 127, 138; against that 32768 x 1024: 74.9, 70.7, 81.1).
+// rows in between (16384 x 2560 with residual: 143 us, with 16 waves 174, with 24 165, in bf16 95, 127, 116; 32768 x
+// 1024 with residual: 116, 125, 133; 32768 x 768: 94, 99, 106; 16384 x 8 x 512: 125, 128, 139; 16384 x 5120: 181, 186,
+// 190; against that the gated norm of 32768 x 1024: 73.9, 69.9, 79.6).
 int64_t groups_per_cu(int w, int nv, bool grad) {
   if (grad) return w < 8 ? (7 + w) / w : 1;
   return 8 * (nv == 1 ? 32 / w : 1);

@@ -1,6 +1,6 @@
 """Calls of the gated recurrence in every combination of what may be given and
-left out, and chains of pieces in blocks of both lengths that rows end in, against the 64-bit
-definitions within the bounds of plain64_gated.py."""
+left out, and chains of pieces in blocks of both lengths that rows end in,
+against the 64-bit definitions within the bounds of plain64_gated.py."""
 import numpy as np
 import pytest
 
@@ -47,8 +47,8 @@ def test_any_call(lib, seed):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("D", [16, 900])
 def test_long_padded_batch(lib, D, dtype):
-    """Rows that end in every kind of piece and block of a long chain: few chains, whose blocks have 32 pieces (4096 steps
-    forward, 2048 back), and many, whose blocks have 8; the last state in place of the first."""
+    """Rows that end in every kind of piece and block of a long chain: few chains, whose blocks have 32 pieces (4096
+    steps forward, 2048 back), and many, whose blocks have 8; the last state in place of the first."""
     import torch
     from selective_state_space_84_amd import binding as bd
     L = 9000

@@ -56,7 +56,7 @@ def test_gradients_along_their_signs(lib, groups, gate_first, post):
         leaves[n].copy_(old)
         ana = float((g.double() * (step / 1e-2)).sum())
         # The loss sums 4e4 terms of 1 with errors of 1e-6 each: 2e-4, in a difference over 1e-2 0.03, and 4/3 of that
-        # here, where both differences are joined so that h^4 is left of the step: 3e-8 of the derivative at most, by the
+        # here, where both differences are joined so that h^4 is left of the step: 3e-8 of the derivative at most by the
         # same differences in 64 bits.  (Along the gradient itself, whose largest values move z by 0.4, these are off by
         # up to 0.4%.)
         num = (4 * num[1] - num[0]) / 3
